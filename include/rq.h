@@ -230,6 +230,112 @@ typedef enum rq_out_type {
 int rq_wgemm_out(const void *x, int M, int K, int N, const rq_packed *w, void *y, int out_type, void *stream);
 int rq_wgemm_batch_out(const rq_wgemm_item *items, int count, int M, int out_type, void *stream);
 
+/* ---- products whose weights depend on the activation row ----
+ * The pages' path multiplies every activation row by the same matrix. These
+ * calls are this library's own addition beside it, over the same packed
+ * formats: rows grouped by expert, and rows with their own low-rank adapter.
+ *
+ * Conventions of this section: index arrays are int32 in device memory and are
+ * read on the device when the call runs, so a captured CUDA graph replays with
+ * new values. An index outside its range never causes an access out of range;
+ * each call says what such a row gets. `workspace` is device memory of at
+ * least the size that the call's *_workspace_size gives (16-byte aligned,
+ * contents unspecified before and after); it must not be used by another call
+ * that may run at the same time, so graphs that share one must run in order.
+ * These calls' kernels may read the packed planes, the adapters and the index
+ * arrays while the kernel launched just before them is still running only
+ * where that is safe under rq_wgemm's ordering rule: the packed planes must
+ * not be written by the kernel launched immediately before the call. */
+
+/* Activation applied to the fp32 result before it is rounded or stored. */
+typedef enum rq_act {
+    RQ_ACT_NONE = 0,
+    RQ_ACT_RELU_SQ = 1      /* max(v, 0)^2, the channel-mix activation of RWKV-7 */
+} rq_act;
+
+/* How the rows of a call fall into groups (device arrays; a host struct). */
+typedef struct rq_groups {
+    int E;                  /* groups (experts), 1..1024 */
+    int R;                  /* rows of the call: length of in_rows / out_rows, 1..2^20 */
+    const int *offsets;     /* [E + 1] rows offsets[e] .. offsets[e+1] - 1 belong to group e;
+                               values out of order or outside [0, R] are taken as the
+                               running maximum clamped to [0, R] */
+    const int *in_rows;     /* [R] row of x for each row, or NULL: row i reads x[i] */
+    const int *out_rows;    /* [R] row of y for each row, or NULL: row i writes y[i] */
+} rq_groups;
+
+/* Bytes of workspace for rq_wgemm_grouped with at most R rows (0: unsupported
+ * shape). Host only. */
+size_t rq_grouped_workspace_size(int fmt, int R, int K, int N, int E);
+
+/* y[out(i)] = act(x[in(i)] * w_hat_e^T) for every row i of every group e.
+ *   x    device bf16 [T][K]; 1 <= T <= 2^20
+ *   w    ONE packed matrix of E * N rows: expert e's [N][K] matrix is its rows
+ *        e N .. (e + 1) N - 1 (what rq_quantize_pack makes of the stacked
+ *        [E][N][K] weights); E * N <= 2^24
+ *   y    device [Ty][N], fp32 or bf16 by out_type; 1 <= Ty <= 2^20. Only rows
+ *        named by a group are written; no y row may overlap x.
+ * A row whose in(i) is outside [0, T) is a row of zeros; one whose out(i) is
+ * outside [0, Ty) is not stored. Two rows with the same out(i): one of the two
+ * results is stored, element by element. A non-finite x value reaches the y
+ * of its own rows only. */
+int rq_wgemm_grouped(const void *x, int T, int K, int N, const rq_packed *w, const rq_groups *g, void *y, int Ty,
+                     int act, int out_type, void *workspace, size_t workspace_bytes, void *stream);
+
+/* A set of low-rank adapters for one packed matrix [N][K] (a host struct of
+ * device pointers): slot a holds A_a [rank][K] and B_a [N][rank]. */
+typedef struct rq_lora {
+    int n;                  /* slots, 1..2^20 */
+    int rank;               /* rows of each slot's A: a multiple of 8, 8..256 */
+    const void *A;          /* device bf16 [n][rank][K] */
+    const void *B;          /* device bf16 [n][N][rank] */
+    const float *scales;    /* device [n] */
+    const int *ranks;       /* device [n] ranks in use, clamped to [0, rank], or NULL: all of
+                               `rank`. Rows of A and columns of B from there on do not count,
+                               whatever they hold. */
+} rq_lora;
+
+/* Bytes of workspace for rq_wgemm_lora with at most M rows. Host only. */
+size_t rq_lora_workspace_size(int fmt, int M, int K, int N, int rank);
+
+/* y[m] = x[m] * w_hat^T + scales[a] * B_a (A_a x[m]), a = row_adapter[m]; a row
+ * whose a is outside [0, n) has no adapter. Sums in fp32; A_a x[m] is kept in
+ * fp32 between the two products.
+ *   x  device bf16 [M][K], 1 <= M <= 2^20;  row_adapter device int32 [M]
+ *   y  device [M][N], fp32 or bf16 by out_type, overwritten */
+int rq_wgemm_lora(const void *x, int M, int K, int N, const rq_packed *w, const rq_lora *ad, const int *row_adapter,
+                  void *y, int out_type, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Outputs of rq_route_topk (device arrays; a host struct). */
+typedef struct rq_routing {
+    int *ids;               /* [T][k] chosen experts, best first; -1 where none is left */
+    float *weights;         /* [T][k] their softmax weights; 0 where ids is -1 */
+    int *offsets;           /* [E + 1] groups, as rq_groups takes them */
+    int *in_rows;           /* [T k] token of each row of the groups; -1 behind offsets[E] */
+    int *slots;             /* [T k] t k + j of each row of the groups; -1 behind offsets[E] */
+} rq_routing;
+
+size_t rq_route_workspace_size(int T, int E, int k);
+
+/* The router of a mixture of experts: the k largest of each token's E logits
+ * (equal ones: the lowest index first), their softmax weights
+ * p_e = exp(l_e - max) / sum_e' exp(l_e' - max) (renorm 1: divided by the sum
+ * of the k chosen ones), and the chosen (token, expert) pairs grouped by
+ * expert, in ascending (token, choice) order within each expert. A logit of
+ * -inf or NaN is never chosen, +inf counts as the largest finite fp32.
+ *   logits  device fp32 (RQ_OUT_F32) or bf16 (RQ_OUT_BF16) [T][E]
+ * Limits: 1 <= E <= 1024, 1 <= k <= min(E, 16), T k <= 2^20. Deterministic. */
+int rq_route_topk(const void *logits, int logits_type, int T, int E, int k, int renorm, const rq_routing *out,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* out[t] = sum_j weights[t][j] * y[t k + j] over the j with ids[t][j] >= 0, in
+ * ascending j in fp32 (rows of y whose ids is negative are not read; a token
+ * with none gets zeros).
+ *   y  device fp32 or bf16 [T k][N] (y_type): the products written with
+ *      out_rows = slots;  out  device fp32 or bf16 [T][N] (out_type) */
+int rq_route_combine(const void *y, int y_type, const int *ids, const float *weights, int T, int N, int k, void *out,
+                     int out_type, void *stream);
+
 /* Export w_hat as fp32 [N][K] into W_out (device).  ([CARD] summary: the
  * kernel output is bit-identical to the offline dequantization.) Bit-exact:
  * q * scale for the symmetric formats, fp32(S_j * q - M_j) for the

@@ -36,6 +36,10 @@ RQ_ERR_NOT_POSITIVE_DEFINITE = 7
 RQ_OUT_F32 = 0
 RQ_OUT_BF16 = 1
 
+RQ_ACT_NONE = 0
+RQ_ACT_RELU_SQ = 1
+ACTS = {None: RQ_ACT_NONE, "none": RQ_ACT_NONE, "relu2": RQ_ACT_RELU_SQ}
+
 RQ_W4_SYM_G64 = 1
 RQ_W8_SYM_G16 = 2
 RQ_W4_ASYM_SB32 = 3
@@ -48,7 +52,8 @@ FORMAT_IDS = {"w4g64": RQ_W4_SYM_G64, "w8g16": RQ_W8_SYM_G16, "w4sb32": RQ_W4_AS
               "w6g16": RQ_W6_SYM_G16}
 SB_FORMATS = (RQ_W4_ASYM_SB32, RQ_W5_ASYM_SB32, RQ_W6_ASYM_SB32)
 EXPORTS = ("rq_packed_size", "rq_quantize_pack", "rq_wgemm", "rq_wgemm_batch", "rq_wgemm_out", "rq_wgemm_batch_out",
-           "rq_dequant",
+           "rq_dequant", "rq_grouped_workspace_size", "rq_wgemm_grouped", "rq_lora_workspace_size", "rq_wgemm_lora",
+           "rq_route_workspace_size", "rq_route_topk", "rq_route_combine",
            "rq_act_sumsq", "rq_act_finalize", "rq_hessian_accum", "rq_gptq_prepare", "rq_gptq_quantize_pack",
            "rq_status_string", "rq_last_cuda_error", "rq_device_status", "rq_test_hooks", "rq_version")
 MAX_BATCH = 160
@@ -77,6 +82,21 @@ class RqPacked(ctypes.Structure):
 
 class RqWgemmItem(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("w", ctypes.POINTER(RqPacked)), ("y", ctypes.c_void_p)]
+
+
+class RqGroups(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int), ("R", ctypes.c_int), ("offsets", ctypes.c_void_p), ("in_rows", ctypes.c_void_p),
+                ("out_rows", ctypes.c_void_p)]
+
+
+class RqLora(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("rank", ctypes.c_int), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("ranks", ctypes.c_void_p)]
+
+
+class RqRouting(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("in_rows", ctypes.c_void_p), ("slots", ctypes.c_void_p)]
 
 
 class RqError(RuntimeError):
@@ -125,6 +145,21 @@ def _lib() -> ctypes.CDLL:
         L.rq_gptq_prepare.restype = I
         L.rq_gptq_quantize_pack.argtypes = [P, I, I, P, P, P, ctypes.POINTER(RqSearch), ctypes.POINTER(RqPacked), P]
         L.rq_gptq_quantize_pack.restype = I
+        Z = ctypes.c_size_t
+        L.rq_grouped_workspace_size.argtypes = [I, I, I, I, I]
+        L.rq_grouped_workspace_size.restype = Z
+        L.rq_wgemm_grouped.argtypes = [P, I, I, I, ctypes.POINTER(RqPacked), ctypes.POINTER(RqGroups), P, I, I, I, P, Z, P]
+        L.rq_wgemm_grouped.restype = I
+        L.rq_lora_workspace_size.argtypes = [I, I, I, I, I]
+        L.rq_lora_workspace_size.restype = Z
+        L.rq_wgemm_lora.argtypes = [P, I, I, I, ctypes.POINTER(RqPacked), ctypes.POINTER(RqLora), P, P, I, P, Z, P]
+        L.rq_wgemm_lora.restype = I
+        L.rq_route_workspace_size.argtypes = [I, I, I]
+        L.rq_route_workspace_size.restype = Z
+        L.rq_route_topk.argtypes = [P, I, I, I, I, I, ctypes.POINTER(RqRouting), P, Z, P]
+        L.rq_route_topk.restype = I
+        L.rq_route_combine.argtypes = [P, I, P, P, I, I, I, P, I, P]
+        L.rq_route_combine.restype = I
         L.rq_status_string.argtypes = [I]
         L.rq_status_string.restype = ctypes.c_char_p
         L.rq_last_cuda_error.argtypes = []
@@ -277,6 +312,231 @@ def rq_dequant(w: Packed, out: torch.Tensor | None = None, stream=None) -> torch
         out = torch.empty(w.N, w.K, dtype=torch.float32, device=w.codes.device)
     d = w.desc()
     _check(_lib().rq_dequant(ctypes.byref(d), _ptr(out), _stream(stream)), "rq_dequant")
+    return out
+
+
+# ------------------------------------- products that depend on the row --
+def _want(t: torch.Tensor, name: str, dtype, shape, device) -> None:
+    """Checks one tensor argument: dtype, shape (None: any size), a dense
+    layout, and that it lies on the call's GPU."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor")
+    if t.dim() != len(shape) or any(w is not None and int(s) != w for s, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+class _On:
+    """Makes `device` current, and `stream` (or the device's current stream)
+    the one that a call and its temporary workspace use."""
+
+    def __init__(self, device: torch.device, stream):
+        if device.type != "cuda":
+            raise ValueError("the tensors must be on a CUDA device")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        other = torch.cuda.current_device() != device.index
+        self._cm = torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device) if other else None
+        self._device = device
+
+    def __enter__(self) -> ctypes.c_void_p:
+        if self._cm is not None:
+            self._cm.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream(self._device).cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._cm is not None:
+            self._cm.__exit__(*exc)
+
+
+def _workspace(bytes_: int, device) -> torch.Tensor:
+    # from PyTorch's caching allocator, on the call's stream: freed to it on
+    # return, so calls on other streams and captured graphs get their own
+    return torch.empty(bytes_, dtype=torch.uint8, device=device)
+
+
+class GroupedExperts:
+    """E packed expert matrices [N][K] in one Packed of E * N rows, prepared for
+    rq_wgemm_grouped calls of at most max_rows rows."""
+
+    def __init__(self, w: Packed, E: int, max_rows: int = 4096):
+        E = int(E)
+        if E < 1 or w.N % E:
+            raise ValueError(f"{w.N} packed rows do not hold {E} equal experts")
+        self.w, self.E, self.N, self.K, self.max_rows = w, E, w.N // E, w.K, int(max_rows)
+        self.device = w.codes.device
+        self._desc = w.desc()
+        self._bytes = int(_lib().rq_grouped_workspace_size(w.fmt, self.max_rows, w.K, self.N, E))
+        if not self._bytes:
+            raise RqError(RQ_ERR_UNSUPPORTED_SHAPE, "rq_grouped_workspace_size")
+
+    def __call__(self, x: torch.Tensor, offsets: torch.Tensor, in_rows: torch.Tensor | None = None,
+                 out_rows: torch.Tensor | None = None, y: torch.Tensor | None = None, act=None,
+                 out_dtype=torch.float32, stream=None) -> torch.Tensor:
+        """y[out_rows[i]] = act(x[in_rows[i]] @ w_hat_e.T) for the rows i in
+        [offsets[e], offsets[e + 1]) of every expert e. The number of rows is
+        that of in_rows, else of out_rows, else of x. y is [*, N] fp32 or bf16;
+        without one a zeroed [rows, N] tensor of out_dtype is made. act: None
+        or "relu2" (max(v, 0)^2)."""
+        dev = self.device
+        _want(x, "x", torch.bfloat16, (None, self.K), dev)
+        _want(offsets, "offsets", torch.int32, (self.E + 1,), dev)
+        R = int((in_rows if in_rows is not None else out_rows if out_rows is not None else x).shape[0])
+        if in_rows is not None:
+            _want(in_rows, "in_rows", torch.int32, (R,), dev)
+        if out_rows is not None:
+            _want(out_rows, "out_rows", torch.int32, (R,), dev)
+        if R > self.max_rows:
+            raise ValueError(f"{R} rows, prepared for at most {self.max_rows}")
+        if act not in ACTS:
+            raise ValueError(f"unknown activation {act!r}")
+        with _On(dev, stream) as st:
+            if y is None:
+                y = torch.zeros(R, self.N, dtype=out_dtype, device=dev)
+            _want(y, "y", y.dtype, (None, self.N), dev)
+            out = _out_type(y.dtype)
+            if x.shape[0] == 0 or R == 0 or y.shape[0] == 0:
+                return y
+            ws = _workspace(self._bytes, dev)
+            g = RqGroups(self.E, R, offsets.data_ptr(), None if in_rows is None else in_rows.data_ptr(),
+                         None if out_rows is None else out_rows.data_ptr())
+            _check(_lib().rq_wgemm_grouped(_ptr(x), x.shape[0], self.K, self.N, self._desc, g, _ptr(y), y.shape[0],
+                                           ACTS[act], out, _ptr(ws), self._bytes, st), "rq_wgemm_grouped")
+        return y
+
+
+def rq_wgemm_grouped(x: torch.Tensor, w: Packed, offsets: torch.Tensor, in_rows=None, out_rows=None, y=None, act=None,
+                     out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    """Packed products grouped by expert: offsets int32 [E + 1], w a Packed of
+    E * N rows. See GroupedExperts, which keeps what repeated calls share."""
+    R = max(1, int((in_rows if in_rows is not None else out_rows if out_rows is not None else x).shape[0]))
+    return GroupedExperts(w, int(offsets.shape[0]) - 1, R)(x, offsets, in_rows, out_rows, y, act, out_dtype, stream)
+
+
+class LoraProjection:
+    """A packed matrix [N][K] with n slots of low-rank adapters, prepared for
+    rq_wgemm_lora calls of at most max_rows rows. A is bf16 [n][r][K], B bf16
+    [n][N][r], scales fp32 [n]; ranks int32 [n] (None: every slot uses all r).
+    Their contents may be replaced between calls."""
+
+    def __init__(self, w: Packed, A: torch.Tensor, B: torch.Tensor, scales: torch.Tensor, ranks: torch.Tensor | None = None,
+                 max_rows: int = 128):
+        dev = w.codes.device
+        if A.dim() != 3:
+            raise ValueError("A must be [slots][rank][K]")
+        n, r = int(A.shape[0]), int(A.shape[1])
+        _want(A, "A", torch.bfloat16, (n, r, w.K), dev)
+        _want(B, "B", torch.bfloat16, (n, w.N, r), dev)
+        _want(scales, "scales", torch.float32, (n,), dev)
+        if ranks is not None:
+            _want(ranks, "ranks", torch.int32, (n,), dev)
+        self.w, self.max_rows, self.device = w, int(max_rows), dev
+        self._keep = (A, B, scales, ranks)
+        self._desc = w.desc()
+        self._lora = RqLora(n, r, A.data_ptr(), B.data_ptr(), scales.data_ptr(), None if ranks is None else ranks.data_ptr())
+        self._bytes = int(_lib().rq_lora_workspace_size(w.fmt, self.max_rows, w.K, w.N, r))
+        if not self._bytes:
+            raise RqError(RQ_ERR_UNSUPPORTED_SHAPE, "rq_lora_workspace_size")
+
+    def __call__(self, x: torch.Tensor, row_adapter: torch.Tensor, y: torch.Tensor | None = None,
+                 out_dtype=torch.float32, stream=None) -> torch.Tensor:
+        """y[m] = x[m] @ w_hat.T + scales[a] * (x[m] @ A[a].T) @ B[a].T with
+        a = row_adapter[m] (int32 [M]; a row whose a is no slot has none)."""
+        dev, w = self.device, self.w
+        _want(x, "x", torch.bfloat16, (None, w.K), dev)
+        M = int(x.shape[0])
+        _want(row_adapter, "row_adapter", torch.int32, (M,), dev)
+        if M > self.max_rows:
+            raise ValueError(f"{M} rows, prepared for at most {self.max_rows}")
+        with _On(dev, stream) as st:
+            if y is None:
+                y = torch.empty(M, w.N, dtype=out_dtype, device=dev)
+            _want(y, "y", y.dtype, (M, w.N), dev)
+            out = _out_type(y.dtype)
+            if M == 0:
+                return y
+            ws = _workspace(self._bytes, dev)
+            _check(_lib().rq_wgemm_lora(_ptr(x), M, w.K, w.N, self._desc, self._lora, _ptr(row_adapter), _ptr(y), out,
+                                        _ptr(ws), self._bytes, st), "rq_wgemm_lora")
+        return y
+
+
+def rq_wgemm_lora(x: torch.Tensor, w: Packed, A: torch.Tensor, B: torch.Tensor, scales: torch.Tensor,
+                  row_adapter: torch.Tensor, ranks=None, y=None, out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    """A packed product with a low-rank adapter per row; see LoraProjection,
+    which keeps what repeated calls share."""
+    return LoraProjection(w, A, B, scales, ranks, max(1, int(x.shape[0])))(x, row_adapter, y, out_dtype, stream)
+
+
+@dataclass
+class Routing:
+    """What rq_route_topk gives: ids and weights [T][k], and the chosen pairs
+    grouped by expert (offsets [E + 1]; token and slot t k + j of each row)."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    offsets: torch.Tensor
+    in_rows: torch.Tensor
+    slots: torch.Tensor
+
+
+class TopkRouter:
+    """Top-k expert routing of [T][E] logits (fp32 or bf16, CUDA)."""
+
+    def __init__(self, E: int, k: int, renorm: bool = False):
+        self.E, self.k, self.renorm = int(E), int(k), bool(renorm)
+        if not _lib().rq_route_workspace_size(1, self.E, self.k):
+            raise ValueError("need 1 <= E <= 1024 and 1 <= k <= min(E, 16)")
+
+    def __call__(self, logits: torch.Tensor, stream=None) -> Routing:
+        T, k, E, dev = int(logits.shape[0]), self.k, self.E, logits.device
+        kind = _out_type(logits.dtype)
+        _want(logits, "logits", logits.dtype, (None, E), dev)
+        with _On(dev, stream) as st:
+            if T == 0:
+                z = torch.empty(0, dtype=torch.int32, device=dev)
+                return Routing(z.view(0, k), z.float().view(0, k), torch.zeros(E + 1, dtype=torch.int32, device=dev), z, z)
+            size = int(_lib().rq_route_workspace_size(T, E, k))
+            if not size:
+                raise RqError(RQ_ERR_INVALID_ARG, "rq_route_workspace_size")
+            # one buffer for the outputs, each at a multiple of 16 bytes, and one for the workspace
+            P, Q = (T * k + 3) & ~3, (E + 4) & ~3
+            b = torch.empty(4 * P + Q, dtype=torch.int32, device=dev)
+            r = Routing(b[:T * k].view(T, k), b[P:P + T * k].view(torch.float32).view(T, k), b[4 * P:4 * P + E + 1],
+                        b[2 * P:2 * P + T * k], b[3 * P:3 * P + T * k])
+            ws = _workspace(size, dev)
+            p = b.data_ptr()
+            out = RqRouting(p, p + 4 * P, p + 16 * P, p + 8 * P, p + 12 * P)
+            _check(_lib().rq_route_topk(_ptr(logits), kind, T, E, k, int(self.renorm), out, _ptr(ws), size, st),
+                   "rq_route_topk")
+        return r
+
+
+def rq_route_topk(logits: torch.Tensor, k: int, renorm: bool = False, stream=None) -> Routing:
+    """The k largest of each token's logits with their softmax weights, and the
+    chosen pairs grouped by expert; see include/rq.h."""
+    return TopkRouter(int(logits.shape[1]), k, renorm)(logits, stream)
+
+
+def rq_route_combine(y: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, out: torch.Tensor | None = None,
+                     out_dtype=None, stream=None) -> torch.Tensor:
+    """out[t] = sum_j weights[t][j] * y[t k + j] over the j with ids[t][j] >= 0
+    (y [T k][N], fp32 or bf16; out of out_dtype, by default y's)."""
+    dev = y.device
+    T, k, N = int(ids.shape[0]), int(ids.shape[1]), int(y.shape[1])
+    kind = _out_type(y.dtype)
+    _want(y, "y", y.dtype, (T * k, N), dev)
+    _want(ids, "ids", torch.int32, (T, k), dev)
+    _want(weights, "weights", torch.float32, (T, k), dev)
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(T, N, dtype=y.dtype if out_dtype is None else out_dtype, device=dev)
+        _want(out, "out", out.dtype, (T, N), dev)
+        if T:
+            _check(_lib().rq_route_combine(_ptr(y), kind, _ptr(ids), _ptr(weights), T, N, k, _ptr(out),
+                                           _out_type(out.dtype), st), "rq_route_combine")
     return out
 
 

@@ -179,6 +179,97 @@ int rq_wgemm_batch(const rq_wgemm_item* items, int count, int M, void* stream) {
     return rq_wgemm_batch_out(items, count, M, RQ_OUT_F32, stream);
 }
 
+// Limits of the row-dependent products (rows of x, rows of the call, rows of
+// y; experts; adapter rank).
+constexpr int kMaxRows = 1 << 20, kMaxExperts = 1024, kMaxRank = 256;
+
+size_t rq_grouped_workspace_size(int fmt, int R, int K, int N, int E) {
+    if (E < 1 || E > kMaxExperts || N < 1 || N > (1 << 24) / E || R < 1 || R > kMaxRows) return 0;
+    if (shape_status(fmt, K, E * N) != RQ_OK) return 0;
+    return rq::rows_workspace(fmt, R, K, N, E, 0);
+}
+
+int rq_wgemm_grouped(const void* x, int T, int K, int N, const rq_packed* w, const rq_groups* g, void* y, int Ty, int act,
+                     int out_type, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!x || !w || !g || !y || !g->offsets || !workspace) return RQ_ERR_INVALID_ARG;
+    if (T < 1 || T > kMaxRows || Ty < 1 || Ty > kMaxRows || g->R < 1 || g->R > kMaxRows) return RQ_ERR_INVALID_ARG;
+    if (g->E < 1 || g->E > kMaxExperts || N < 1 || N > (1 << 24) / g->E) return RQ_ERR_INVALID_ARG;
+    if (act != RQ_ACT_NONE && act != RQ_ACT_RELU_SQ) return RQ_ERR_INVALID_ARG;
+    if (out_type != RQ_OUT_F32 && out_type != RQ_OUT_BF16) return RQ_ERR_INVALID_ARG;
+    const int s = check_packed(w, K, g->E * N);
+    if (s != RQ_OK) return s;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(workspace) || !aligned16(g->offsets) ||
+        (g->in_rows && !aligned16(g->in_rows)) || (g->out_rows && !aligned16(g->out_rows)))
+        return RQ_ERR_MISALIGNED;
+    if (workspace_bytes < rq::rows_workspace(w->fmt, g->R, K, N, g->E, 0)) return RQ_ERR_INVALID_ARG;
+    rq::RowsArgs a = {};
+    a.fmt = w->fmt; a.T = T; a.K = K; a.N = N; a.E = g->E; a.R = g->R; a.Ty = Ty;
+    a.x = x; a.codes = w->codes; a.scales = w->scales;
+    a.offsets = g->offsets; a.in_rows = g->in_rows; a.out_rows = g->out_rows;
+    a.y = y; a.ybf16 = out_type == RQ_OUT_BF16; a.act = act; a.ws = workspace;
+    return cuda_status(rq::launch_rows(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t rq_lora_workspace_size(int fmt, int M, int K, int N, int rank) {
+    if (M < 1 || M > kMaxRows || rank < 8 || rank > kMaxRank || rank % 8 != 0) return 0;
+    if (shape_status(fmt, K, N) != RQ_OK) return 0;
+    return rq::rows_workspace(fmt, M, K, N, 1, rank);
+}
+
+int rq_wgemm_lora(const void* x, int M, int K, int N, const rq_packed* w, const rq_lora* ad, const int* row_adapter, void* y,
+                  int out_type, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!x || !w || !ad || !row_adapter || !y || !workspace) return RQ_ERR_INVALID_ARG;
+    if (M < 1 || M > kMaxRows || ad->n < 1 || ad->n > kMaxRows) return RQ_ERR_INVALID_ARG;
+    if (!ad->A || !ad->B || !ad->scales) return RQ_ERR_INVALID_ARG;
+    if (out_type != RQ_OUT_F32 && out_type != RQ_OUT_BF16) return RQ_ERR_INVALID_ARG;
+    const int s = check_packed(w, K, N);
+    if (s != RQ_OK) return s;
+    if (ad->rank < 8 || ad->rank > kMaxRank || ad->rank % 8 != 0) return RQ_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(workspace) || !aligned16(row_adapter) || !aligned16(ad->A) ||
+        !aligned16(ad->B) || !aligned16(ad->scales) || (ad->ranks && !aligned16(ad->ranks)))
+        return RQ_ERR_MISALIGNED;
+    if (workspace_bytes < rq::rows_workspace(w->fmt, M, K, N, 1, ad->rank)) return RQ_ERR_INVALID_ARG;
+    rq::RowsArgs a = {};
+    a.fmt = w->fmt; a.T = M; a.K = K; a.N = N; a.E = 1; a.R = M; a.Ty = M;
+    a.x = x; a.codes = w->codes; a.scales = w->scales;
+    a.y = y; a.ybf16 = out_type == RQ_OUT_BF16; a.ws = workspace;
+    a.adapter = row_adapter; a.A = ad->A; a.B = ad->B; a.alpha = ad->scales; a.ranks = ad->ranks;
+    a.n_adapters = ad->n; a.r = ad->rank;
+    return cuda_status(rq::launch_rows(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t rq_route_workspace_size(int T, int E, int k) {
+    if (T < 1 || T > kMaxRows || E < 1 || E > kMaxExperts || k < 1 || k > 16 || k > E || T > kMaxRows / k) return 0;
+    return rq::route_workspace(T, E, k);
+}
+
+int rq_route_topk(const void* logits, int logits_type, int T, int E, int k, int renorm, const rq_routing* out,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+    if (!logits || !out || !workspace) return RQ_ERR_INVALID_ARG;
+    if (!out->ids || !out->weights || !out->offsets || !out->in_rows || !out->slots) return RQ_ERR_INVALID_ARG;
+    if (logits_type != RQ_OUT_F32 && logits_type != RQ_OUT_BF16) return RQ_ERR_INVALID_ARG;
+    if (renorm != 0 && renorm != 1) return RQ_ERR_INVALID_ARG;
+    const size_t need = rq_route_workspace_size(T, E, k);
+    if (need == 0 || workspace_bytes < need) return RQ_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned16(out->ids) || !aligned16(out->weights) || !aligned16(out->offsets) ||
+        !aligned16(out->in_rows) || !aligned16(out->slots) || !aligned16(workspace))
+        return RQ_ERR_MISALIGNED;
+    rq::RouteArgs a = {logits, logits_type == RQ_OUT_BF16, T, E, k, renorm, out->ids, out->weights, out->offsets,
+                       out->in_rows, out->slots, workspace};
+    return cuda_status(rq::launch_route(a, static_cast<cudaStream_t>(stream)));
+}
+
+int rq_route_combine(const void* y, int y_type, const int* ids, const float* weights, int T, int N, int k, void* out,
+                     int out_type, void* stream) {
+    if (!y || !ids || !weights || !out) return RQ_ERR_INVALID_ARG;
+    if ((y_type != RQ_OUT_F32 && y_type != RQ_OUT_BF16) || (out_type != RQ_OUT_F32 && out_type != RQ_OUT_BF16))
+        return RQ_ERR_INVALID_ARG;
+    if (T < 1 || T > kMaxRows || k < 1 || k > 16 || T > kMaxRows / k || N < 1 || N > (1 << 24)) return RQ_ERR_INVALID_ARG;
+    if (!aligned16(y) || !aligned16(ids) || !aligned16(weights) || !aligned16(out)) return RQ_ERR_MISALIGNED;
+    rq::CombineArgs a = {y, ids, weights, out, T, k, N, y_type == RQ_OUT_BF16, out_type == RQ_OUT_BF16};
+    return cuda_status(rq::launch_combine(a, static_cast<cudaStream_t>(stream)));
+}
+
 int rq_dequant(const rq_packed* w, float* W_out, void* stream) {
     if (!w || !W_out) return RQ_ERR_INVALID_ARG;
     int s = check_packed(w, w->K, w->N);
@@ -240,6 +331,6 @@ int rq_test_hooks(long long wait_ns, int flags) {
     return RQ_OK;
 }
 
-int rq_version(void) { return 200; }
+int rq_version(void) { return 300; }
 
 }  // extern "C"

@@ -103,6 +103,53 @@ constexpr int kTcMinM = 3;
 bool tc_supported(int fmt, int M);
 cudaError_t launch_tc(const WgemmArgs* a, int count, cudaStream_t st);
 
+// Products whose weights depend on the activation row (rq_rows.cu): E packed
+// matrices of N rows each in one plane, rows [offsets[e], offsets[e + 1]) of
+// the call multiplied by matrix e (offsets NULL: E = 1, every row); and one
+// shared matrix with a low-rank adapter per row (adapter != NULL).
+struct RowsArgs {
+    int fmt, T, K, N, E, R, Ty;
+    const void* x;             // bf16 [T][K]
+    const void* codes;         // planes of a packed [E N][K] matrix
+    const void* scales;
+    const int* offsets;        // [E + 1]
+    const int* in_rows;        // [R] row of x, or NULL: row i
+    const int* out_rows;       // [R] row of y, or NULL: row i
+    void* y;                   // [Ty][N]
+    int ybf16, act;            // act 1: max(v, 0)^2
+    const int* adapter;        // [R] adapter of each row, or NULL
+    const void* A;             // bf16 [n_adapters][r][K]
+    const void* B;             // bf16 [n_adapters][N][r]
+    const float* alpha;        // [n_adapters]
+    const int* ranks;          // [n_adapters] or NULL: all r
+    int n_adapters, r;
+    void* ws;
+};
+size_t rows_workspace(int fmt, int R, int K, int N, int E, int rank);
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st);
+
+// Expert routing (rq_route.cu).
+struct RouteArgs {
+    const void* logits;        // fp32 or bf16 [T][E]
+    int bf16, T, E, k, renorm;
+    int* ids;                  // [T][k]
+    float* weights;            // [T][k]
+    int* offsets;              // [E + 1]
+    int* in_rows;              // [T k]
+    int* slots;                // [T k]
+    void* ws;
+};
+struct CombineArgs {
+    const void* y;             // [T k][N]
+    const int* ids;
+    const float* weights;
+    void* out;                 // [T][N]
+    int T, k, N, ybf16, obf16;
+};
+size_t route_workspace(int T, int E, int k);
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t st);
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st);
+
 // Per-channel sums of squares of bf16 activations (adds into sum_sq) and
 // their finalization into fp32 E[x^2].
 cudaError_t launch_act_sumsq(const void* x, int R, int K, double* sum_sq, cudaStream_t st);
