@@ -312,12 +312,13 @@ int rq_last_cuda_error(void) { return t_last_cuda; }
 int rq_device_status(void* stream, int* word) {
     if (!word) return RQ_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    unsigned a = 0, b = 0, c = 0, d = 0;
+    unsigned a = 0, b = 0, c = 0, d = 0, r = 0;
     int s = cuda_status(rq::status_pack(st, &a));
     if (s == RQ_OK) s = cuda_status(rq::status_gemv(st, &b));
     if (s == RQ_OK) s = cuda_status(rq::status_tc(st, &c));
     if (s == RQ_OK) s = cuda_status(rq::status_gptq(st, &d));
-    const unsigned w = a | b | c | d;
+    if (s == RQ_OK) s = cuda_status(rq::status_rows(st, &r));
+    const unsigned w = a | b | c | d | r;
     *word = (int)w;
     if (s != RQ_OK) return s;
     if (w & ~(unsigned)rq::kStatusNotSpd) return RQ_ERR_DEVICE_TIMEOUT;

@@ -160,6 +160,7 @@ cudaError_t status_pack(cudaStream_t st, unsigned* word);
 cudaError_t status_gptq(cudaStream_t st, unsigned* word);
 cudaError_t status_gemv(cudaStream_t st, unsigned* word);
 cudaError_t status_tc(cudaStream_t st, unsigned* word);
+cudaError_t status_rows(cudaStream_t st, unsigned* word);
 
 int sm_count();   // multiprocessors of the current device
 

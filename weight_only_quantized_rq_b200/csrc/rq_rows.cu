@@ -1,7 +1,46 @@
 // rq_rows.cu -- packed products whose weights depend on the activation row:
-// products grouped by expert, and low-rank adapters beside a shared packed
-// projection.
+// products grouped by expert with ragged sizes, and a low-rank adapter per row
+// beside a shared packed projection.
+//
+//   grouped  y[i] = act(x[in(i)] W_e^T),            i in [offsets[e], offsets[e + 1])
+//   adapter  y[m] = x[m] W^T + s_a B_a (A_a x[m]),  a = row_adapter[m]
+//
+// Two launches per call:
+//
+// prep_kernel  lays the rows out for the tensor cores: per group, tiles of
+//   eight rows (the last one padded with zeros), each tile as the B fragments
+//   of mma.m16n8k16 in the order that the weights' codes unpack in, so that the
+//   product kernel reads 16 bytes per lane with no bank conflict and no
+//   permutation. For the superblock formats it adds each row's sums over the
+//   32-weight groups (w = S u - M needs sum x). It clears the split counters,
+//   and for adapters it also computes t = s_a A_a x[m] in fp32. It lets the
+//   product kernel start once its own predecessors are done, so the product's
+//   weight copies run while prep works.
+//
+// rows_kernel  multiplies. Bound by the weight stream while a group has few
+//   rows: what has to be read is the packed plane of each expert in use.
+//   * Codes are exact small integers in bf16 (q, |q| <= 127; u <= 63 for the
+//     superblocks), x is bf16: every product is exact in the tensor core's
+//     fp32 sums, and the group's scale multiplies the fp32 group sum. So no
+//     weight is rounded, and fp32 results are good to fp32 (about 5e-7 on the
+//     sums here), unlike weights rounded to bf16 before the product (2e-3).
+//   * mma.sync, not tcgen05: with a handful of rows the products are not what
+//     counts. The A operand of mma.sync comes straight from the registers that
+//     unpacked it, and its result is in registers when the group's scale is
+//     applied; through tensor memory each 64-weight group would need its own
+//     accumulator and a read back (measured for this library's other kernel:
+//     1.9 against 2.4 TB/s).
+//   * A unit of work is 128 weight rows x K x up to 8 NB activation rows.
+//     Warps 0-3 take 32 weight rows each over the first half of every stage's
+//     K, warps 4-7 over the second half: 32 rows per warp halve the shared-
+//     memory reads of x against 16.
+//   * All units' K stages form one line that the CTAs (two per SM) share out
+//     evenly, so neither ragged groups nor few tiles leave SMs idle. A unit cut
+//     by a CTA border is summed through the workspace: each part is written,
+//     the last to arrive adds all parts in K order (the same bits whoever is
+//     last; nobody waits).
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -12,138 +51,999 @@
 namespace rq {
 namespace {
 
-// Eight consecutive weights k8 .. k8 + 7 of one packed row, as fp32 (exact for
-// the symmetric formats, one rounding of S q - M for the superblocks).
+constexpr int kRowsPerTile = 128;      // weight rows of a unit
+constexpr int kMathWarps = 8;
+constexpr int kRowsThreads = 32 * (kMathWarps + 1);
+constexpr int kMaxRing = 8;
+constexpr size_t kRowsSmemMax = 113 * 1024;   // two CTAs per SM
+
+// Geometry of a format's K stage.
 template <int FMT>
-__device__ __forceinline__ void w_hat8(const uint8_t* codes, const uint8_t* scales, size_t row, int K, int k8, float (&w)[8]) {
-    if constexpr (is_sb(FMT)) {
-        constexpr int BITS = sb_bits(FMT);
-        const uint8_t* r = codes + (row * (K / 256) + k8 / 256) * sb_record(FMT);
-        const uint4 hd = *reinterpret_cast<const uint4*>(r);
-        const int kk = k8 % 256, j = kk / 32;
-        const float S = __half2float(__ushort_as_half((uint16_t)(hd.x & 0xffffu))) * (float)sb_field(hd.y, hd.z, hd.w, 0, j);
-        const float M = __half2float(__ushort_as_half((uint16_t)(hd.x >> 16))) * (float)sb_field(hd.y, hd.z, hd.w, 1, j);
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(r + 16 + kk / 2);
+struct Geo {
+    static constexpr int KS = is_w8(FMT) || FMT == kFmtW6G16 ? 128 : 256;         // K per stage
+    static constexpr int RB = FMT == kFmtW4G64 ? 128 : is_w8(FMT) ? 128 : FMT == kFmtW6G16 ? 96 : sb_record(FMT);
+    static constexpr int XB = KS * 16 + (is_sb(FMT) ? 256 : 0);                   // bytes of one 8-row tile's stage
+    static constexpr bool SWZ = RB == 128;
+};
+
+struct Plan {                          // what both kernels know of a call
+    const int* offsets;
+    int E, R, N, K, T;                 // T: stages per unit
+    int NB;                            // 8-row tiles per unit at most
+};
+
+struct RowsParams {
+    CUtensorMap cmap;                  // codes: uint8 [E N][row bytes], box [128][RB]
+    Plan pl;
+    const uint8_t* scales;
+    unsigned long long total_rows;     // E N
+    uint32_t srb;                      // scale bytes per weight row
+    const uint8_t* xf;                 // prepared activations
+    float* part;                       // partial tiles, two per CTA
+    unsigned* count;                   // arrivals per split unit, by its first CTA
+    const int* out_rows;
+    void* y;
+    int Ty, ybf16, act;
+    const int* adapter;
+    const int* ranks;
+    const __nv_bfloat16* B;
+    const float* t;                    // [R][r]
+    int n_adapters, r;
+    int ring, stage_bytes;
+    unsigned long long wait_ns;
+    int test_flags;
+};
+
+struct PrepParams {
+    Plan pl;
+    const __nv_bfloat16* x;
+    const int* in_rows;
+    int rows_x;
+    uint8_t* xf;
+    unsigned* count;
+    int n_count;
+    int tiles_max, kblocks;
+    const int* adapter;
+    const int* ranks;
+    const __nv_bfloat16* A;
+    const float* alpha;
+    float* t;
+    int n_adapters, r;
+};
+
+// ------------------------------------------------------------------ groups
+// First row and first 8-row tile of each group, and its first unit, computed
+// by one warp from the offsets (their running maximum, clamped to [0, R]).
+struct Groups {
+    int* row;          // [E + 1]
+    int* tile;         // [E + 1]
+    long long* unit;   // [E + 1]
+};
+__host__ __device__ inline size_t groups_bytes(int E) { return round16((size_t)(E + 1) * 16); }
+
+__device__ __forceinline__ Groups groups_at(void* p, int E) {
+    Groups g;
+    g.unit = static_cast<long long*>(p);
+    g.row = reinterpret_cast<int*>(g.unit + E + 1);
+    g.tile = g.row + E + 1;
+    return g;
+}
+
+__device__ __forceinline__ void scan_groups(const Plan& pl, Groups g, int lane) {
+    const int tiles_n = (pl.N + kRowsPerTile - 1) / kRowsPerTile, chunk = 8 * pl.NB;
+    int top = 0, tile0 = 0;
+    long long unit0 = 0;
+    for (int e0 = 0; e0 <= pl.E; e0 += 32) {
+        const int e = e0 + lane;
+        // end of group e - 1 = start of group e
+        int v = 0;
+        if (pl.offsets) v = e <= pl.E ? min(max(pl.offsets[e], 0), pl.R) : 0;
+        else v = e >= 1 ? pl.R : 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(~0u, v, o);
+            if (lane >= o) v = max(v, w);
+        }
+        v = max(v, top);
+        const int prev = __shfl_up_sync(~0u, v, 1);
+        const int m = lane == 0 ? (e0 ? v - top : 0) : v - prev;       // rows of group e - 1
+        int tl = (m + 7) / 8;
+        long long un = (long long)((m + chunk - 1) / chunk) * tiles_n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int a = __shfl_up_sync(~0u, tl, o);
+            const long long b = __shfl_up_sync(~0u, un, o);
+            if (lane >= o) { tl += a; un += b; }
+        }
+        if (e <= pl.E) {
+            g.row[e] = v;
+            g.tile[e] = tile0 + tl;
+            g.unit[e] = unit0 + un;
+        }
+        top = __shfl_sync(~0u, v, 31);
+        tile0 += __shfl_sync(~0u, tl, 31);
+        unit0 += __shfl_sync(~0u, un, 31);
+    }
+    __syncwarp();
+}
+
+// Last e with a[e] <= v (a ascending, a[0] <= v): the group that holds v, as
+// groups without members repeat their successor's start.
+template <class T>
+__device__ __forceinline__ int find_group(const T* a, int E, T v) {
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a[mid] <= v) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// ------------------------------------------------------------------- prep
+constexpr int kPrepThreads = 256;
+
+__device__ __forceinline__ float bf16_sum8(uint4 v) {
+    return ((bf16lo_f32(v.x) + bf16hi_f32(v.x)) + (bf16lo_f32(v.y) + bf16hi_f32(v.y))) +
+           ((bf16lo_f32(v.z) + bf16hi_f32(v.z)) + (bf16lo_f32(v.w) + bf16hi_f32(v.w)));
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kPrepThreads) prep_kernel(const PrepParams p) {
+    using G = Geo<FMT>;
+    extern __shared__ __align__(16) uint8_t sm[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dep_wait();
+    grid_dep_launch();                                   // the product kernel may start: all earlier work is done
+    const int nx = p.tiles_max * p.kblocks;
+    if ((int)blockIdx.x < nx) {
+        if (blockIdx.x == 0)
+            for (int i = tid; i < p.n_count; i += kPrepThreads) p.count[i] = 0u;
+        Groups g = groups_at(sm, p.pl.E);
+        if (warp == 0) scan_groups(p.pl, g, lane);
+        __syncthreads();
+        const int tile = blockIdx.x / p.kblocks, kb = blockIdx.x % p.kblocks;
+        if (tile >= g.tile[p.pl.E]) return;
+        const int e = find_group(g.tile, p.pl.E, tile);
+        const int row = g.row[e] + 8 * (tile - g.tile[e]) + (lane >> 2);     // lane = 4 (row in tile) + chunk in four
+        int src = -1;
+        if (row < g.row[e + 1]) {
+            src = p.in_rows ? p.in_rows[row] : row;
+            if (src < 0 || src >= p.rows_x) src = -1;
+        }
+        const int c_end = min((kb + 1) * 256, p.pl.T * G::KS / 8);           // 8-value chunks of this block's K range
+        uint8_t* out = p.xf + (size_t)tile * p.pl.T * G::XB;
+        for (int c0 = kb * 256 + 4 * warp; c0 < c_end; c0 += 4 * (kPrepThreads / 32)) {
+            const int c = c0 + (lane & 3);
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (src >= 0 && 8 * c < p.pl.K)
+                v = *reinterpret_cast<const uint4*>(p.x + (size_t)src * p.pl.K + 8 * c);
+            const int st = 8 * c / G::KS, cs = c - st * (G::KS / 8);         // stage, chunk in the stage
+            uint8_t* o = out + (size_t)st * G::XB;
+            if constexpr (G::KS == 256) {
+                // nibble words unpack as the pairs (0, 4), (1, 5), (2, 6), (3, 7)
+                uint4 w;
+                w.x = prmt(v.x, v.z, 0x5410u);
+                w.y = prmt(v.x, v.z, 0x7632u);
+                w.z = prmt(v.y, v.w, 0x5410u);
+                w.w = prmt(v.y, v.w, 0x7632u);
+                *reinterpret_cast<uint4*>(o + ((cs >> 2) * 32 + lane) * 16) = w;
+                if constexpr (is_sb(FMT)) {
+                    float s = bf16_sum8(v);
+                    s += __shfl_xor_sync(~0u, s, 1);
+                    s += __shfl_xor_sync(~0u, s, 2);
+                    if ((lane & 3) == 0) *reinterpret_cast<float*>(o + G::KS * 16 + ((cs >> 2) * 8 + (lane >> 2)) * 4) = s;
+                }
+            } else {
+                // four-weight words unpack as the pairs (0, 2), (1, 3); lane t of a quad takes weights
+                // 4t .. 4t + 3 of each 16-weight step, two steps per 16 bytes
+                const int g8 = lane >> 2;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t q = (c >> (4 * i)) & 15u;
-            if (BITS == 5) q |= ((r[144 + kk / 8] >> i) & 1u) << 4;
-            if (BITS == 6) q |= ((r[144 + kk / 4 + i / 4] >> (2 * (i % 4))) & 3u) << 4;
-            w[i] = fmaf(S, (float)q, -M);
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t a = h ? v.z : v.x, b = h ? v.w : v.y;
+                    const int t = 2 * (cs & 1) + h, half = (cs >> 1) & 1;
+                    const uint2 w = make_uint2(prmt(a, b, 0x5410u), prmt(a, b, 0x7632u));
+                    *reinterpret_cast<uint2*>(o + ((cs >> 2) * 32 + g8 * 4 + t) * 16 + half * 8) = w;
+                }
+            }
         }
     } else {
-        constexpr int G = sym_group(FMT);
-        const float s = __half2float(reinterpret_cast<const __half*>(scales)[row * (K / G) + k8 / G]);
-        if constexpr (FMT == kFmtW4G64) {
-            const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + (row * K + k8) / 2);
+        // t[m][j] = s_a A_a[j] . x[m]: one warp per (m, j)
+        const int per = (p.r + 7) / 8;
+        const int b = blockIdx.x - nx, m = b / per, j = (b % per) * 8 + warp;
+        const int a = p.adapter[m];
+        if (a < 0 || a >= p.n_adapters) return;
+        if (p.ranks && j >= p.ranks[a]) return;
+        const uint4* x = reinterpret_cast<const uint4*>(p.x + (size_t)m * p.pl.K);
+        const uint4* w = reinterpret_cast<const uint4*>(p.A + ((size_t)a * p.r + j) * p.pl.K);
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 4
+        for (int c = lane; c < p.pl.K / 8; c += 32) {
+            const uint4 u = x[c], v = w[c];
+            const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = s * (float)((int)((c >> (4 * i)) & 15u) - 8);
-        } else if constexpr (FMT == kFmtW6G16) {
-            const uint8_t* r = codes + (row * (K / 64) + k8 / 64) * 48;
-            const int kk = k8 % 64;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int q = ((r[(kk + i) / 2] >> (4 * (i & 1))) & 15) | (((r[32 + (kk + i) / 4] >> (2 * (i % 4))) & 3) << 4);
-                w[i] = s * (float)(q - 32);
+            for (int i = 0; i < 4; ++i) {
+                s0 = fmaf(bf16lo_f32(uu[i]), bf16lo_f32(vv[i]), s0);
+                s1 = fmaf(bf16hi_f32(uu[i]), bf16hi_f32(vv[i]), s1);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = s * (float)((int)codes[row * K + k8 + i] - 128);
         }
+        float s = s0 + s1;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+        if (lane == 0) p.t[(size_t)m * p.r + j] = s * p.alpha[a];
     }
 }
 
-// t[m][j] = scale_a * (x[m] . A_a[j]): one warp per (m, j).
-__global__ void shrink_kernel(RowsArgs a) {
-    const int j = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), m = blockIdx.y, lane = threadIdx.x & 31;
-    const int ad = a.adapter[m];
-    if (j >= a.r || ad < 0 || ad >= a.n_adapters || (a.ranks && j >= a.ranks[ad])) return;
-    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + (size_t)m * a.K;
-    const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(a.A) + ((size_t)ad * a.r + j) * a.K;
-    float s = 0.0f;
-    for (int k = lane; k < a.K; k += 32) s = fmaf(__bfloat162float(x[k]), __bfloat162float(A[k]), s);
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-    if (lane == 0) static_cast<float*>(a.ws)[(size_t)m * a.r + j] = s * a.alpha[ad];
+// ------------------------------------------------------------ PTX wrappers
+__device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void bulk_x(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(n) : "memory"); }
+
+// D += A B, A 16 x 16 (row), B 16 x 8 (col), bf16 with fp32 sums.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// One warp per packed row (one output feature of one expert), eight
-// activation rows of the group at a time.
+// (v & m) | c
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t m, uint32_t c) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(v), "r"(m), "r"(c));
+    return d;
+}
+// (v & m) ^ c
+__device__ __forceinline__ uint32_t and_xor(uint32_t v, uint32_t m, uint32_t c) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(v), "r"(m), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// ------------------------------------------------------------------ unpack
+// A bf16 has seven fraction bits, so 0x4300 | v is 128 + v for v < 128:
+// exact, and the subtraction of an integer from it is exact too.
+
+// Eight nibbles of w as the pairs (0, 4), (1, 5), (2, 6), (3, 7), minus `off` - 128.
+template <uint32_t OFF2>
+__device__ __forceinline__ void unpack_nibbles(uint32_t w, uint32_t (&o)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = sub_bf16x2(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u), OFF2);
+}
+// The same with the codes' higher bits: h holds them at bits 16 (k / 4) + B (k % 4), B = 1 or 2 bits per code.
+template <int B, uint32_t OFF2>
+__device__ __forceinline__ void unpack_wide(uint32_t w, uint32_t h, uint32_t (&o)[4]) {
+    constexpr uint32_t HM = B == 1 ? 0x00100010u : 0x00300030u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int s = 4 - B * i;
+        const uint32_t hs = s >= 0 ? h << (s < 0 ? 0 : s) : h >> (s < 0 ? -s : 0);
+        o[i] = sub_bf16x2(and_or(hs, HM, and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u)), OFF2);
+    }
+}
+// Four bytes u = q + 128 of w as the pairs (0, 2), (1, 3): the low seven bits
+// under 128, minus 128 where the byte's top bit is set (0x4300) and 256 where
+// it is not (0x4380).
+__device__ __forceinline__ void unpack_bytes(uint32_t w, uint32_t (&o)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t v = i ? w >> 8 : w;
+        o[i] = sub_bf16x2(and_or(v, 0x007F007Fu, 0x43004300u), and_xor(v, 0x00800080u, 0x43804380u));
+    }
+}
+
+// --------------------------------------------------------------- one stage
+// The scale words of a thread's four weight rows for its half of a stage, in
+// registers: fp16 bits, two per 32-bit word.
 template <int FMT>
-__global__ void rows_kernel(RowsArgs a) {
-    const size_t row = (size_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (size_t)a.E * a.N) return;
-    const int e = (int)(row / a.N), n = (int)(row % a.N);
-    int o0 = 0, o1 = a.R;
-    if (a.offsets) {                                     // the running maximum keeps any offsets in order and in range
-        for (int i = 0; i <= e; ++i) o0 = max(o0, min(a.offsets[i], a.R));
-        o1 = max(o0, min(a.offsets[e + 1], a.R));
-    }
-    const uint8_t* codes = static_cast<const uint8_t*>(a.codes);
-    const uint8_t* scales = static_cast<const uint8_t*>(a.scales);
-    for (int i0 = o0; i0 < o1; i0 += 8) {
-        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        const __nv_bfloat16* xr[8];
+struct Scales {
+    static constexpr int W = is_sb(FMT) ? 1 : sym_group(FMT) == 16 ? 2 : 1;
+    uint32_t w[4][W];
+};
+
+template <int FMT>
+__device__ __forceinline__ void load_scales(const RowsParams& p, const uint32_t (&row)[4], int stage, int half, Scales<FMT>& s) {
+    if constexpr (!is_sb(FMT)) {
+        constexpr int GS = sym_group(FMT), PER = Geo<FMT>::KS / 2 / GS;      // groups of a half stage: 1, 2 or 4
+        const int groups = p.pl.K / GS, gi = (2 * stage + half) * PER;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = i0 + i < o1 ? (a.in_rows ? a.in_rows[i0 + i] : i0 + i) : -1;
-            xr[i] = r >= 0 && r < a.T ? static_cast<const __nv_bfloat16*>(a.x) + (size_t)r * a.K : nullptr;
+        for (int i = 0; i < 4; ++i) {
+            const uint8_t* a = p.scales + (size_t)row[i] * p.srb + 2 * gi;
+            if constexpr (PER == 4) {                    // K % 64 == 0: the four groups exist or none does, 8-byte aligned
+                const uint2 v = gi < groups ? __ldg(reinterpret_cast<const uint2*>(a)) : make_uint2(0u, 0u);
+                s.w[i][0] = v.x;
+                s.w[i][1] = v.y;
+            } else if constexpr (PER == 2) {
+                uint32_t v = 0u;
+                if (gi + 1 < groups && (p.srb & 3u) == 0u) v = __ldg(reinterpret_cast<const uint32_t*>(a));
+                else if (gi < groups) {
+                    v = __ldg(reinterpret_cast<const uint16_t*>(a));
+                    if (gi + 1 < groups) v |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(a + 2)) << 16;
+                }
+                s.w[i][0] = v;
+            } else {
+                s.w[i][0] = gi < groups ? (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(a)) : 0u;
+            }
         }
-        for (int k8 = 8 * lane; k8 < a.K; k8 += 256) {
-            float w[8];
-            w_hat8<FMT>(codes, scales, row, a.K, k8, w);
+    }
+}
+
+__device__ __forceinline__ float half_at(uint32_t w, int h) {
+    return __half2float(__ushort_as_half((uint16_t)(h ? w >> 16 : w & 0xffffu)));
+}
+
+// One warp's share of a stage: weight rows wr .. wr + 31 over half the
+// stage's K, all live 8-row tiles. acc[m16][tile]: D fragment (weight rows
+// 16 m16 + lane / 4, + 8; activation rows 2 (lane % 4), + 1).
+template <int FMT, int NB>
+__device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t smin, int wr, int half, int lane, int tiles,
+                                           const Scales<FMT>& sc, float (&acc)[2][NB][4]) {
+    using G = Geo<FMT>;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t xl = xs + lane * 16;
+    if constexpr (FMT == kFmtW4G64) {
+#pragma unroll
+        for (int gi = 0; gi < 2; ++gi) {
+            const int gr = 2 * half + gi;
+            uint32_t a[2][4][4];                         // [m16][step][register]
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int mr = 0; mr < 4; ++mr) {         // row 8 mr + g of the warp's 32
+                    const uint32_t r = wr + 8 * mr + g;
+                    uint32_t o[4];
+                    unpack_nibbles<0x43084308u>(lds32_a(cs + r * 128 + (((2 * gr + j) ^ g) << 4) + 4 * t), o);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        a[mr >> 1][2 * j + h][mr & 1] = o[2 * h];
+                        a[mr >> 1][2 * j + h][2 + (mr & 1)] = o[2 * h + 1];
+                    }
+                }
+            float s[4];
+#pragma unroll
+            for (int mr = 0; mr < 4; ++mr) s[mr] = half_at(sc.w[mr][0], gi);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                if (NB > 1 && nb >= tiles) break;
+                const uint4 x0 = lds128_a(xl + nb * G::XB + (2 * gr) * 512), x1 = lds128_a(xl + nb * G::XB + (2 * gr + 1) * 512);
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma16816(d, a[mt][0], x0.x, x0.y);
+                    mma16816(d, a[mt][1], x0.z, x0.w);
+                    mma16816(d, a[mt][2], x1.x, x1.y);
+                    mma16816(d, a[mt][3], x1.z, x1.w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[mt][nb][i] = fmaf(s[2 * mt + (i >> 1)], d[i], acc[mt][nb][i]);
+                }
+            }
+        }
+    } else if constexpr (is_w8(FMT) || FMT == kFmtW6G16) {
+        constexpr bool G16 = sym_group(FMT) == 16;
+        float gsum[2][NB][4];
+        if (!G16) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) gsum[mt][nb][i] = 0.0f;
+        }
+#pragma unroll
+        for (int sp = 0; sp < 2; ++sp) {                 // pairs of 16-weight steps
+            uint32_t a[2][2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int mr = 0; mr < 4; ++mr) {
+                    const uint32_t r = wr + 8 * mr + g;
+                    const int st = 2 * sp + h;           // step in the half stage
+                    uint32_t o[2];
+                    if constexpr (FMT == kFmtW6G16) {
+                        const uint32_t b = cs + r * G::RB + 48 * half;
+                        const uint32_t n = lds16_a(b + 8 * st + 2 * t);
+                        uint32_t pl;
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(pl) : "r"(b + 32 + 4 * st + t));
+                        const uint32_t w = n | (n << 8), hh = pl | (pl << 12);
+                        o[0] = sub_bf16x2(and_or(hh << 4, 0x00300030u, and_or(w, 0x000F000Fu, 0x43004300u)), 0x43204320u);
+                        o[1] = sub_bf16x2(and_or(hh << 2, 0x00300030u, and_or(w >> 4, 0x000F000Fu, 0x43004300u)), 0x43204320u);
+                    } else {
+                        unpack_bytes(lds32_a(cs + r * 128 + (((4 * half + st) ^ g) << 4) + 4 * t), o);
+                    }
+                    a[mr >> 1][h][mr & 1] = o[0];
+                    a[mr >> 1][h][2 + (mr & 1)] = o[1];
+                }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                if (NB > 1 && nb >= tiles) break;
+                const uint4 x = lds128_a(xl + nb * G::XB + (2 * half + sp) * 512);
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    if constexpr (G16) {
+                        float d0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma16816(d0, a[mt][0], x.x, x.y);
+                        mma16816(d1, a[mt][1], x.z, x.w);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t w = sc.w[2 * mt + (i >> 1)][sp];
+                            acc[mt][nb][i] = fmaf(half_at(w, 0), d0[i], acc[mt][nb][i]);
+                            acc[mt][nb][i] = fmaf(half_at(w, 1), d1[i], acc[mt][nb][i]);
+                        }
+                    } else {
+                        mma16816(gsum[mt][nb], a[mt][0], x.x, x.y);
+                        mma16816(gsum[mt][nb], a[mt][1], x.z, x.w);
+                    }
+                }
+            }
+        }
+        if constexpr (!G16) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[mt][nb][i] = fmaf(half_at(sc.w[2 * mt + (i >> 1)][0], 0), gsum[mt][nb][i], acc[mt][nb][i]);
+        }
+    } else {
+        // superblocks: lane = weight row decodes the row's four (S, M) of this half into shared memory
+        {
+            const uint4 hd = lds128_a(cs + (uint32_t)(wr + lane) * G::RB);
+            const float d = half_at(hd.x, 0), dm = half_at(hd.x, 1);
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // fields 4 half + j of the scales (bits 6 ..) and of the mins (bits 48 + 6 ..)
+                const uint32_t f0 = half ? __funnelshift_r(hd.y, hd.z, 24) : hd.y;         // scale fields from bit 0
+                const uint32_t f1 = half ? __funnelshift_r(hd.w, 0u, 8) : __funnelshift_r(hd.z, hd.w, 16);
+                v[2 * j] = __fmul_rn(d, (float)((f0 >> (6 * j)) & 63u));
+                v[2 * j + 1] = __fmul_rn(dm, (float)((f1 >> (6 * j)) & 63u));
+            }
+            __syncwarp();                                // the previous stage's values have been read
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" :: "r"(smin + lane * 32), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" :: "r"(smin + lane * 32 + 16), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
+            __syncwarp();
+        }
+#pragma unroll
+        for (int gp = 0; gp < 4; ++gp) {
+            const int gr = 4 * half + gp;
+            uint32_t a[2][2][4];
+            float2 sm2[4];
+#pragma unroll
+            for (int mr = 0; mr < 4; ++mr) {
+                const uint32_t rb = cs + (uint32_t)(wr + 8 * mr + g) * G::RB;
+                const uint32_t w = lds32_a(rb + 16 + 16 * gr + 4 * t);
+                uint32_t o[4];
+                if constexpr (FMT == kFmtW4SB32) {
+                    unpack_nibbles<0x43004300u>(w, o);
+                } else if constexpr (FMT == kFmtW5SB32) {
+                    uint32_t h;
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(h) : "r"(rb + 144 + 4 * gr + t));
+                    unpack_wide<1, 0x43004300u>(w, h | (h << 12), o);
+                } else {
+                    const uint32_t h = lds16_a(rb + 144 + 8 * gr + 2 * t);
+                    unpack_wide<2, 0x43004300u>(w, h | (h << 8), o);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    a[mr >> 1][h][mr & 1] = o[2 * h];
+                    a[mr >> 1][h][2 + (mr & 1)] = o[2 * h + 1];
+                }
+                sm2[mr] = lds64f_a(smin + (8 * mr + g) * 32 + 8 * gp);
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                if (NB > 1 && nb >= tiles) break;
+                const uint4 x = lds128_a(xl + nb * G::XB + gr * 512);
+                const float2 xsum = lds64f_a(xs + nb * G::XB + G::KS * 16 + gr * 32 + t * 8);
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma16816(d, a[mt][0], x.x, x.y);
+                    mma16816(d, a[mt][1], x.z, x.w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 m = sm2[2 * mt + (i >> 1)];
+                        acc[mt][nb][i] = fmaf(m.x, d[i], acc[mt][nb][i]);
+                        acc[mt][nb][i] = fmaf(-m.y, i & 1 ? xsum.y : xsum.x, acc[mt][nb][i]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------- product
+struct Work { int e, n0, row0, rows, tile0; };   // a unit: expert, first weight row, first row and rows, first 8-row tile
+
+__device__ __forceinline__ Work get_work(const Plan& pl, const Groups& g, long long unit) {
+    const int e = find_group(g.unit, pl.E, unit), m = g.row[e + 1] - g.row[e];
+    const int chunk = 8 * pl.NB, chunks = (m + chunk - 1) / chunk;
+    const long long i = unit - g.unit[e];
+    const int nt = (int)(i / chunks), c = (int)(i - (long long)nt * chunks);
+    Work w;
+    w.e = e;
+    w.n0 = nt * kRowsPerTile;
+    w.row0 = g.row[e] + c * chunk;
+    w.rows = min(chunk, m - c * chunk);
+    w.tile0 = g.tile[e] + c * pl.NB;
+    return w;
+}
+
+// The adapter's term for weight rows n .. n + 3 of row m.
+__device__ __forceinline__ void add_adapter(const RowsParams& p, int m, int n, float (&v)[4]) {
+    const int a = p.adapter[m];
+    if (a < 0 || a >= p.n_adapters) return;
+    const int rank = p.ranks ? min(p.ranks[a], p.r) : p.r;
+    const float* t = p.t + (size_t)m * p.r;
+    const __nv_bfloat16* B = p.B + ((size_t)a * p.pl.N + n) * p.r;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < rank; j += 8) {
+        float tv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) tv[i] = j + i < rank ? t[j + i] : 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (n + q >= p.pl.N) break;
+            const uint4 b = __ldg(reinterpret_cast<const uint4*>(B + (size_t)q * p.r + j));
+            const uint32_t bb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (!xr[i]) continue;
-                const uint4 v = *reinterpret_cast<const uint4*>(xr[i] + k8);
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[i] = fmaf(w[2 * j], bf16lo_f32(u[j]), acc[i]);
-                    acc[i] = fmaf(w[2 * j + 1], bf16hi_f32(u[j]), acc[i]);
-                }
+                const float w = i & 1 ? bf16hi_f32(bb[i >> 1]) : bf16lo_f32(bb[i >> 1]);
+                if (j + i < rank) s[q] = fmaf(tv[i], w, s[q]);           // past the rank the slot may hold anything
             }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            for (int o = 16; o; o >>= 1) acc[i] += __shfl_xor_sync(~0u, acc[i], o);
-            if (lane != 0 || i0 + i >= o1) continue;
-            const int m = i0 + i;
-            float v = acc[i];
-            if (a.adapter) {
-                const int ad = a.adapter[m];
-                if (ad >= 0 && ad < a.n_adapters) {
-                    const int rank = a.ranks ? min(a.ranks[ad], a.r) : a.r;
-                    const __nv_bfloat16* B = static_cast<const __nv_bfloat16*>(a.B) + ((size_t)ad * a.N + n) * a.r;
-                    float s = 0.0f;
-                    for (int j = 0; j < rank; ++j) s = fmaf(static_cast<float*>(a.ws)[(size_t)m * a.r + j], __bfloat162float(B[j]), s);
-                    v += s;
-                }
-            }
-            if (a.act == 1) { v = v > 0.0f || v != v ? v : 0.0f; v *= v; }
-            const int out = a.out_rows ? a.out_rows[m] : m;
-            if (out >= 0 && out < a.Ty) store_y(a.y, (size_t)out * a.N + n, v, a.ybf16);
         }
     }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] += s[q];
+}
+
+template <int FMT, int NB>
+__global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const __grid_constant__ RowsParams p) {
+    using G = Geo<FMT>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);         // the swizzled tiles need 1024-byte alignment
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ring = p.ring;
+    uint8_t* at = smem + (size_t)ring * p.stage_bytes;
+    float* red = reinterpret_cast<float*>(at);                           // 8 NB x 132 floats
+    at += 8 * NB * 132 * 4;
+    const uint32_t smin = smem_u32(at) + warp * 1024;                    // superblock (S, M) of the warp's rows
+    if (is_sb(FMT)) at += kMathWarps * 1024;
+    uint64_t* full = reinterpret_cast<uint64_t*>(at);
+    uint64_t* empty = full + kMaxRing;
+    at += 2 * kMaxRing * 8;
+    int* flag = reinterpret_cast<int*>(at);
+    at += 16;
+    const Groups g = groups_at(at, p.pl.E);
+
+    if (tid == 0) {
+        for (int s = 0; s < ring; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kMathWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 0) scan_groups(p.pl, g, lane);
+    __syncthreads();
+    grid_dep_launch();
+
+    const int T = p.pl.T;
+    const long long S = g.unit[p.pl.E] * T;
+    const long long Gc = min((long long)gridDim.x, S);                   // CTAs with work
+    if ((long long)blockIdx.x >= Gc) {
+        grid_dep_wait();                                  // no kernel after this one runs beside prep_kernel
+        return;
+    }
+    const long long s0 = blockIdx.x * S / Gc, s1 = ((long long)blockIdx.x + 1) * S / Gc;
+
+    if (warp == kMathWarps) {
+        // ------------------------------------------------------------ copies
+        // The codes of the first `ring` stages are asked for before the
+        // prepared activations are waited for.
+        const uint32_t base = smem_u32(smem);
+        const int n = (int)min(s1 - s0, (long long)0x7fffffff);
+        int issued = 0;
+        bool ok = true;
+        auto expect = [&](const Work& w) { return (uint32_t)(kRowsPerTile * G::RB + ((w.rows + 7) / 8) * G::XB); };
+        auto scales_ahead = [&](const Work& w, int k, bool first) {      // 32-byte sectors of the tile's scale rows into L2
+            if constexpr (!is_sb(FMT)) {
+                constexpr int BS = G::KS / sym_group(FMT) * 2;           // scale bytes per row and stage
+                if (first || (k * BS) % 32 == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const unsigned long long row = (unsigned long long)w.e * p.pl.N + w.n0 + 32 * i + lane;
+                        if (row < p.total_rows && (uint32_t)(k * BS) < p.srb) prefetch_l2(p.scales + row * p.srb + k * BS);
+                    }
+                }
+            }
+        };
+        const int head = min(n, ring);
+        const bool copies = !(p.test_flags & kTestNoCopies);
+        {
+            long long s = s0;
+            for (int i = 0; i < head;) {
+                const Work w = get_work(p.pl, g, s / T);
+                for (int k = (int)(s % T); k < T && i < head; ++k, ++i, ++s) {
+                    if (lane == 0 && copies) {
+                        mbar_arrive_expect_tx(&full[i], expect(w));
+                        tma_codes(base + i * p.stage_bytes, &p.cmap, k * G::RB, w.e * p.pl.N + w.n0, &full[i]);
+                    }
+                    scales_ahead(w, k, i == 0);
+                }
+            }
+        }
+        grid_dep_wait();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        long long s = s0;
+        int slot = 0, wrap = 0;
+        for (int i = 0; i < n && ok;) {
+            const Work w = get_work(p.pl, g, s / T);
+            const int tiles = (w.rows + 7) / 8;
+            for (int k = (int)(s % T); k < T && i < n; ++k, ++i, ++s) {
+                if (wrap && !__all_sync(~0u, mbar_wait_bounded(&empty[slot], (uint32_t)(wrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns))) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0 && copies) {
+                    const uint32_t st = base + slot * p.stage_bytes;
+                    if (wrap) {
+                        mbar_arrive_expect_tx(&full[slot], expect(w));
+                        tma_codes(st, &p.cmap, k * G::RB, w.e * p.pl.N + w.n0, &full[slot]);
+                    }
+                    for (int j = 0; j < tiles; ++j)
+                        bulk_x(st + kRowsPerTile * G::RB + j * G::XB, p.xf + ((size_t)(w.tile0 + j) * T + k) * G::XB, G::XB, &full[slot]);
+                    ++issued;
+                }
+                if (wrap) scales_ahead(w, k, false);
+                if (++slot == ring) { slot = 0; ++wrap; }
+            }
+        }
+        // copies in flight (a consumer gave up) land before the CTA leaves
+        if (lane == 0)
+            for (int q = 0; q < ring && q < issued; ++q) {
+                const int uses = issued / ring + (q < issued % ring ? 1 : 0);
+                mbar_wait_bounded(&full[q], (uint32_t)(uses - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
+            }
+        return;
+    }
+
+    // ---------------------------------------------------------------- math
+    const int wr = 32 * (warp & 3), half = warp >> 2;
+    const uint32_t base = smem_u32(smem);
+    bool alive = true;                                    // false after a wait ran out: go on without waiting
+    int slot = 0, wrap = 0;
+    grid_dep_wait();                                      // counters and adapter terms come from prep_kernel
+    for (long long s = s0; s < s1;) {
+        const long long unit = s / T;
+        const Work w = get_work(p.pl, g, unit);
+        const int k0 = (int)(s - unit * T), k1 = (int)min((long long)T, k0 + (s1 - s));
+        const int tiles = (w.rows + 7) / 8;
+        float acc[2][NB][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[mt][nb][i] = 0.0f;
+        uint32_t row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            row[i] = (uint32_t)min((unsigned long long)w.e * p.pl.N + w.n0 + wr + 8 * i + (lane >> 2), p.total_rows - 1);
+        Scales<FMT> nxt;
+        load_scales<FMT>(p, row, k0, half, nxt);
+        for (int k = k0; k < k1; ++k) {
+            const Scales<FMT> cur = nxt;
+            if (k + 1 < k1) load_scales<FMT>(p, row, k + 1, half, nxt);
+            if (alive) alive = __all_sync(~0u, mbar_wait_bounded(&full[slot], (uint32_t)wrap & 1u, kStatusTmaWait, 0u, p.wait_ns));
+            const uint32_t st = base + slot * p.stage_bytes;
+            stage_math<FMT, NB>(st, st + kRowsPerTile * G::RB, smin, wr, half, lane, tiles, cur, acc);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot]);
+            if (++slot == ring) { slot = 0; ++wrap; }
+        }
+        s += k1 - k0;
+
+        // the two halves of K
+        bar_sync(1, 256);                                 // the previous unit's tile has been stored
+        if (half) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                    *reinterpret_cast<float4*>(red + ((mt * NB + nb) * 128 + tid - 128) * 4) =
+                        make_float4(acc[mt][nb][0], acc[mt][nb][1], acc[mt][nb][2], acc[mt][nb][3]);
+        }
+        bar_sync(1, 256);
+        if (!half) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const float4 v = *reinterpret_cast<const float4*>(red + ((mt * NB + nb) * 128 + tid) * 4);
+                    acc[mt][nb][0] += v.x;
+                    acc[mt][nb][1] += v.y;
+                    acc[mt][nb][2] += v.z;
+                    acc[mt][nb][3] += v.w;
+                }
+            bool mine = true;                             // whether this CTA stores the unit
+            if (k0 > 0 || k1 < T) {
+                // a part of a unit: CTA c's part lies in slot 2c (it began in an earlier CTA) or 2c + 1
+                const long long us = unit * T;
+                const int first = (int)(((us + 1) * Gc - 1) / S), last = (int)(((us + T) * Gc - 1) / S);
+                float4* mypart = reinterpret_cast<float4*>(p.part) + (size_t)(2 * blockIdx.x + (k0 == 0)) * (256 * NB);
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                        __stcg(mypart + (mt * NB + nb) * 128 + tid, make_float4(acc[mt][nb][0], acc[mt][nb][1], acc[mt][nb][2], acc[mt][nb][3]));
+                __threadfence();
+                bar_sync(2, 128);
+                if (tid == 0) *flag = atomicAdd(&p.count[first], 1u) == (unsigned)(last - first);
+                bar_sync(2, 128);
+                mine = *flag != 0;
+                if (mine) {
+                    __threadfence();
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            for (int c = first; c <= last; ++c) {
+                                const float4 u = __ldcg(reinterpret_cast<const float4*>(p.part) +
+                                                        (size_t)(2 * c + (c == first)) * (256 * NB) + (mt * NB + nb) * 128 + tid);
+                                v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+                            }
+                            acc[mt][nb][0] = v.x; acc[mt][nb][1] = v.y; acc[mt][nb][2] = v.z; acc[mt][nb][3] = v.w;
+                        }
+                }
+            } else {
+                bar_sync(2, 128);                         // `red` has been read
+                if (tid == 0) *flag = 1;
+            }
+            if (mine) {                                   // the tile as [activation row][weight row]
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            red[(8 * nb + 2 * (lane & 3) + (i & 1)) * 132 + wr + 16 * mt + (lane >> 2) + 8 * (i >> 1)] = acc[mt][nb][i];
+            }
+        }
+        bar_sync(1, 256);
+        if (*flag) {
+            const int n = w.n0 + 4 * lane, N = p.pl.N;
+            for (int i = warp; i < w.rows; i += kMathWarps) {
+                const int m = w.row0 + i;
+                const int out = p.out_rows ? p.out_rows[m] : m;
+                if (out < 0 || out >= p.Ty || n >= N) continue;
+                const float4 f = *reinterpret_cast<const float4*>(red + i * 132 + 4 * lane);
+                float v[4] = {f.x, f.y, f.z, f.w};
+                if (p.adapter) add_adapter(p, m, n, v);
+                if (p.act) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        v[q] = v[q] > 0.0f || v[q] != v[q] ? v[q] : 0.0f;
+                        v[q] *= v[q];
+                    }
+                }
+                const size_t o = (size_t)out * N + n;
+                if ((N & 3) == 0) {
+                    if (p.ybf16) {
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + o) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                    } else {
+                        *reinterpret_cast<float4*>(static_cast<float*>(p.y) + o) = make_float4(v[0], v[1], v[2], v[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (n + q < N) store_y(p.y, o + q, v[q], p.ybf16);
+                }
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+    static EncodeTiled fn = nullptr;
+    static int tried = 0;
+    if (!__atomic_load_n(&tried, __ATOMIC_ACQUIRE)) {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiled>(f);
+        __atomic_store_n(&tried, 1, __ATOMIC_RELEASE);
+    }
+    return fn;
+}
+
+constexpr int kMaxCtas = 512;          // CTAs of a launch at most (two per SM)
+
+// 8-row tiles per unit: as many as an even split of the rows fills, since a
+// group with more rows than a unit holds streams its weights once per unit.
+int pick_nb(int R, int E) {
+    const int per = (R + E - 1) / E;
+    return R <= 8 || per <= 3 ? 1 : per <= 12 ? 2 : 4;
+}
+
+struct Layout { size_t xf, part, count, t, total; int tiles, T; };
+
+template <int FMT>
+Layout layout(int R, int K, int E, int rank) {
+    Layout l;
+    l.T = (K + Geo<FMT>::KS - 1) / Geo<FMT>::KS;
+    l.tiles = R / 8 + (E < R ? E : R);                   // sum of ceil(m_e / 8) at most
+    l.xf = 0;
+    l.part = round16((size_t)l.tiles * l.T * Geo<FMT>::XB);
+    l.count = l.part + (size_t)2 * kMaxCtas * pick_nb(R, E) * 4096;
+    l.t = l.count + kMaxCtas * 4;
+    l.total = l.t + round16((size_t)R * rank * 4);
+    return l;
+}
+
+template <int FMT, int NB>
+cudaError_t launch_product(const RowsParams& p0, cudaStream_t st) {
+    using G = Geo<FMT>;
+    RowsParams p = p0;
+    p.stage_bytes = (kRowsPerTile * G::RB + NB * G::XB + 1023) & ~1023;
+    const size_t fixed = 1024 + 8 * NB * 132 * 4 + (is_sb(FMT) ? kMathWarps * 1024 : 0) + 2 * kMaxRing * 8 + 16 + groups_bytes(p.pl.E);
+    p.ring = (int)((kRowsSmemMax - fixed) / p.stage_bytes);
+    if (p.ring > kMaxRing) p.ring = kMaxRing;
+    if (p.ring < 2) return cudaErrorInvalidValue;
+    auto kern = rows_kernel<FMT, NB>;
+    static unsigned long long attr_done = 0ull;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsSmemMax);
+        if (e != cudaSuccess) return e;
+        __atomic_fetch_or(&attr_done, bit, __ATOMIC_RELEASE);
+    }
+    int ctas = 2 * sm_count();
+    if (ctas > kMaxCtas) ctas = kMaxCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kRowsThreads);
+    cfg.dynamicSmemBytes = fixed + (size_t)p.ring * p.stage_bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
+    using G = Geo<FMT>;
+    const EncodeTiled enc = encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const Layout l = layout<FMT>(a.R, a.K, a.E, a.adapter ? a.r : 0);
+    uint8_t* ws = static_cast<uint8_t*>(a.ws);
+    Plan pl = {a.offsets, a.E, a.R, a.N, a.K, l.T, pick_nb(a.R, a.E)};
+
+    PrepParams q = {};
+    q.pl = pl;
+    q.x = static_cast<const __nv_bfloat16*>(a.x);
+    q.in_rows = a.in_rows;
+    q.rows_x = a.T;
+    q.xf = ws + l.xf;
+    q.count = reinterpret_cast<unsigned*>(ws + l.count);
+    q.n_count = kMaxCtas;
+    q.tiles_max = l.tiles;
+    q.kblocks = (l.T * G::KS / 8 + 255) / 256;
+    q.adapter = a.adapter;
+    q.ranks = a.ranks;
+    q.A = static_cast<const __nv_bfloat16*>(a.A);
+    q.alpha = a.alpha;
+    q.t = reinterpret_cast<float*>(ws + l.t);
+    q.n_adapters = a.n_adapters;
+    q.r = a.r;
+    const long long blocks = (long long)q.tiles_max * q.kblocks + (a.adapter ? (long long)a.R * ((a.r + 7) / 8) : 0);
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kPrepThreads);
+    cfg.dynamicSmemBytes = groups_bytes(a.E);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, prep_kernel<FMT>, q);
+    if (e != cudaSuccess) return e;
+
+    RowsParams p = {};
+    const uint64_t crb = code_row_bytes(FMT, a.K), rows = (uint64_t)a.E * a.N;
+    const cuuint64_t dims[2] = {crb, rows}, strides[1] = {crb};
+    const cuuint32_t box[2] = {(cuuint32_t)G::RB, (cuuint32_t)kRowsPerTile}, es[2] = {1, 1};
+    if (enc(&p.cmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(a.codes), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, G::SWZ ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    p.pl = pl;
+    p.scales = static_cast<const uint8_t*>(a.scales);
+    p.total_rows = rows;
+    p.srb = (uint32_t)scale_row_bytes(FMT, a.K);
+    p.xf = ws + l.xf;
+    p.part = reinterpret_cast<float*>(ws + l.part);
+    p.count = reinterpret_cast<unsigned*>(ws + l.count);
+    p.out_rows = a.out_rows;
+    p.y = a.y;
+    p.Ty = a.Ty;
+    p.ybf16 = a.ybf16;
+    p.act = a.act;
+    p.adapter = a.adapter;
+    p.ranks = a.ranks;
+    p.B = static_cast<const __nv_bfloat16*>(a.B);
+    p.t = reinterpret_cast<const float*>(ws + l.t);
+    p.n_adapters = a.n_adapters;
+    p.r = a.r;
+    p.wait_ns = wait_limit_ns();
+    p.test_flags = test_flags();
+    if (pl.NB == 1) return launch_product<FMT, 1>(p, st);
+    if (pl.NB == 2) return launch_product<FMT, 2>(p, st);
+    return launch_product<FMT, 4>(p, st);
 }
 
 }  // namespace
 
-size_t rows_workspace(int, int R, int, int, int, int rank) { return round16((size_t)R * rank * 4) + 16; }
+size_t rows_workspace(int fmt, int R, int K, int, int E, int rank) {
+    switch (fmt) {
+        case kFmtW4G64: return layout<kFmtW4G64>(R, K, E, rank).total;
+        case kFmtW8G16: return layout<kFmtW8G16>(R, K, E, rank).total;
+        case kFmtW8G64: return layout<kFmtW8G64>(R, K, E, rank).total;
+        case kFmtW6G16: return layout<kFmtW6G16>(R, K, E, rank).total;
+        case kFmtW4SB32: return layout<kFmtW4SB32>(R, K, E, rank).total;
+        case kFmtW5SB32: return layout<kFmtW5SB32>(R, K, E, rank).total;
+        default: return layout<kFmtW6SB32>(R, K, E, rank).total;
+    }
+}
 
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
-    if (a.adapter) shrink_kernel<<<dim3((a.r + 7) / 8, a.R), 256, 0, st>>>(a);
-    const unsigned grid = (unsigned)(((size_t)a.E * a.N + 7) / 8);
     switch (a.fmt) {
-        case kFmtW4G64: rows_kernel<kFmtW4G64><<<grid, 256, 0, st>>>(a); break;
-        case kFmtW8G16: rows_kernel<kFmtW8G16><<<grid, 256, 0, st>>>(a); break;
-        case kFmtW8G64: rows_kernel<kFmtW8G64><<<grid, 256, 0, st>>>(a); break;
-        case kFmtW6G16: rows_kernel<kFmtW6G16><<<grid, 256, 0, st>>>(a); break;
-        case kFmtW4SB32: rows_kernel<kFmtW4SB32><<<grid, 256, 0, st>>>(a); break;
-        case kFmtW5SB32: rows_kernel<kFmtW5SB32><<<grid, 256, 0, st>>>(a); break;
-        default: rows_kernel<kFmtW6SB32><<<grid, 256, 0, st>>>(a); break;
+        case kFmtW4G64: return launch_fmt<kFmtW4G64>(a, st);
+        case kFmtW8G16: return launch_fmt<kFmtW8G16>(a, st);
+        case kFmtW8G64: return launch_fmt<kFmtW8G64>(a, st);
+        case kFmtW6G16: return launch_fmt<kFmtW6G16>(a, st);
+        case kFmtW4SB32: return launch_fmt<kFmtW4SB32>(a, st);
+        case kFmtW5SB32: return launch_fmt<kFmtW5SB32>(a, st);
+        default: return launch_fmt<kFmtW6SB32>(a, st);
     }
-    return cudaGetLastError();
+}
+
+cudaError_t status_rows(cudaStream_t st, unsigned* word) {
+    unsigned v = 0, z = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_status, &z, sizeof(z), 0, cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    *word = v;
+    return e;
 }
 
 }  // namespace rq
