@@ -52,10 +52,12 @@ namespace rq {
 namespace {
 
 constexpr int kRowsPerTile = 128;      // weight rows of a unit
-constexpr int kMathWarps = 8;
+constexpr int kMathWarps = 4;          // 32 weight rows each
 constexpr int kRowsThreads = 32 * (kMathWarps + 1);
-constexpr int kMaxRing = 8;
-constexpr size_t kRowsSmemMax = 113 * 1024;   // two CTAs per SM
+constexpr int kMaxRing = 6;
+constexpr int kDescs = 8;              // unit descriptors in flight: more than kMaxRing + 1
+constexpr int kWarpScratch = 1280;     // shared bytes per math warp: an 8 x 32 result tile, or superblock scales
+constexpr size_t kSmemPerSm = 228 * 1024;
 
 // Geometry of a format's K stage.
 template <int FMT>
@@ -63,8 +65,14 @@ struct Geo {
     static constexpr int KS = is_w8(FMT) || FMT == kFmtW6G16 ? 128 : 256;         // K per stage
     static constexpr int RB = FMT == kFmtW4G64 ? 128 : is_w8(FMT) ? 128 : FMT == kFmtW6G16 ? 96 : sb_record(FMT);
     static constexpr int XB = KS * 16 + (is_sb(FMT) ? 256 : 0);                   // bytes of one 8-row tile's stage
+    static constexpr int SB = is_sb(FMT) ? 0 : KS / sym_group(FMT) * 2;           // scale bytes of a weight row's stage
     static constexpr bool SWZ = RB == 128;
 };
+
+// CTAs per SM: four while their accumulators and two stages each fit.
+__host__ __device__ constexpr int ctas_per_sm(int fmt, int nb) {
+    return nb == 4 || fmt == kFmtW5SB32 || fmt == kFmtW6SB32 ? 3 : 4;
+}
 
 struct Plan {                          // what both kernels know of a call
     const int* offsets;
@@ -282,8 +290,16 @@ __device__ __forceinline__ void bulk_x(uint32_t dst, const void* src, uint32_t b
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
-__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(n) : "memory"); }
+// Asynchronous copy of B (4 or 8) bytes, or zeros where !in; cp_async_arrive
+// makes the mbarrier receive one arrival when this thread's copies so far are
+// in shared memory.
+template <int B>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" :: "r"(dst), "l"(src), "n"(B), "r"(in ? B : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
 
 // D += A B, A 16 x 16 (row), B 16 x 8 (col), bf16 with fp32 sums.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -344,8 +360,8 @@ __device__ __forceinline__ void unpack_bytes(uint32_t w, uint32_t (&o)[2]) {
 }
 
 // --------------------------------------------------------------- one stage
-// The scale words of a thread's four weight rows for its half of a stage, in
-// registers: fp16 bits, two per 32-bit word.
+// The scales of a thread's four weight rows for half a stage: fp16 bits, two
+// per 32-bit word, from the stage's scale block ([128 rows][SB bytes]).
 template <int FMT>
 struct Scales {
     static constexpr int W = is_sb(FMT) ? 1 : sym_group(FMT) == 16 ? 2 : 1;
@@ -353,28 +369,19 @@ struct Scales {
 };
 
 template <int FMT>
-__device__ __forceinline__ void load_scales(const RowsParams& p, const uint32_t (&row)[4], int stage, int half, Scales<FMT>& s) {
-    if constexpr (!is_sb(FMT)) {
-        constexpr int GS = sym_group(FMT), PER = Geo<FMT>::KS / 2 / GS;      // groups of a half stage: 1, 2 or 4
-        const int groups = p.pl.K / GS, gi = (2 * stage + half) * PER;
+__device__ __forceinline__ void read_scales(uint32_t ss, int wr, int half, int g, Scales<FMT>& s) {
+    constexpr int SB = Geo<FMT>::SB;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint8_t* a = p.scales + (size_t)row[i] * p.srb + 2 * gi;
-            if constexpr (PER == 4) {                    // K % 64 == 0: the four groups exist or none does, 8-byte aligned
-                const uint2 v = gi < groups ? __ldg(reinterpret_cast<const uint2*>(a)) : make_uint2(0u, 0u);
-                s.w[i][0] = v.x;
-                s.w[i][1] = v.y;
-            } else if constexpr (PER == 2) {
-                uint32_t v = 0u;
-                if (gi + 1 < groups && (p.srb & 3u) == 0u) v = __ldg(reinterpret_cast<const uint32_t*>(a));
-                else if (gi < groups) {
-                    v = __ldg(reinterpret_cast<const uint16_t*>(a));
-                    if (gi + 1 < groups) v |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(a + 2)) << 16;
-                }
-                s.w[i][0] = v;
-            } else {
-                s.w[i][0] = gi < groups ? (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(a)) : 0u;
-            }
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = ss + (uint32_t)(wr + 8 * i + g) * SB + half * (SB / 2);
+        if constexpr (SB == 16) {
+            const float2 v = lds64f_a(a);
+            s.w[i][0] = __float_as_uint(v.x);
+            s.w[i][1] = __float_as_uint(v.y);
+        } else if constexpr (SB == 8) {
+            s.w[i][0] = lds32_a(a);
+        } else if constexpr (SB == 4) {
+            s.w[i][0] = lds16_a(a);
         }
     }
 }
@@ -565,13 +572,23 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t sm
 }
 
 // ----------------------------------------------------------------- product
+// One stretch of a unit in one CTA, written by the copy warp ahead of the
+// stretch's first stage.
+struct Desc {
+    int n0;            // first weight row within the expert
+    int row0, rows;    // rows of the call
+    int k0, k1;        // stages
+    int first, last;   // CTAs that share the unit
+    int e;
+};
+
 struct Work { int e, n0, row0, rows, tile0; };   // a unit: expert, first weight row, first row and rows, first 8-row tile
 
 __device__ __forceinline__ Work get_work(const Plan& pl, const Groups& g, long long unit) {
     const int e = find_group(g.unit, pl.E, unit), m = g.row[e + 1] - g.row[e];
     const int chunk = 8 * pl.NB, chunks = (m + chunk - 1) / chunk;
     const long long i = unit - g.unit[e];
-    const int nt = (int)(i / chunks), c = (int)(i - (long long)nt * chunks);
+    const int nt = i < 0x7fffffff ? (int)i / chunks : (int)(i / chunks), c = (int)(i - (long long)nt * chunks);
     Work w;
     w.e = e;
     w.n0 = nt * kRowsPerTile;
@@ -581,20 +598,20 @@ __device__ __forceinline__ Work get_work(const Plan& pl, const Groups& g, long l
     return w;
 }
 
-// The adapter's term for weight rows n .. n + 3 of row m.
-__device__ __forceinline__ void add_adapter(const RowsParams& p, int m, int n, float (&v)[4]) {
+// The adapter's term for weight rows n .. n + 7 of row m.
+__device__ __forceinline__ void add_adapter(const RowsParams& p, int m, int n, float (&v)[8]) {
     const int a = p.adapter[m];
     if (a < 0 || a >= p.n_adapters) return;
     const int rank = p.ranks ? min(p.ranks[a], p.r) : p.r;
     const float* t = p.t + (size_t)m * p.r;
     const __nv_bfloat16* B = p.B + ((size_t)a * p.pl.N + n) * p.r;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     for (int j = 0; j < rank; j += 8) {
         float tv[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) tv[i] = j + i < rank ? t[j + i] : 0.0f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 8; ++q) {
             if (n + q >= p.pl.N) break;
             const uint4 b = __ldg(reinterpret_cast<const uint4*>(B + (size_t)q * p.r + j));
             const uint32_t bb[4] = {b.x, b.y, b.z, b.w};
@@ -606,11 +623,36 @@ __device__ __forceinline__ void add_adapter(const RowsParams& p, int m, int n, f
         }
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] += s[q];
+    for (int q = 0; q < 8; ++q) v[q] += s[q];
+}
+
+// v[0..7] to columns n .. n + 7 of y's row `out`.
+__device__ __forceinline__ void store8(const RowsParams& p, int out, int n, const float (&v)[8]) {
+    const int N = p.pl.N;
+    const size_t o = (size_t)out * N + n;
+    if ((N & 7) == 0 || ((N & 3) == 0 && !p.ybf16 && n + 8 <= N)) {
+        if (p.ybf16) {
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                u[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + o) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+            float* y = static_cast<float*>(p.y) + o;
+            *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(y + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (n + q < N) store_y(p.y, o + q, v[q], p.ybf16);
+    }
 }
 
 template <int FMT, int NB>
-__global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kernel(const __grid_constant__ RowsParams p) {
     using G = Geo<FMT>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -618,25 +660,23 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const __grid_cons
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ring = p.ring;
     uint8_t* at = smem + (size_t)ring * p.stage_bytes;
-    float* red = reinterpret_cast<float*>(at);                           // 8 NB x 132 floats
-    at += 8 * NB * 132 * 4;
-    const uint32_t smin = smem_u32(at) + warp * 1024;                    // superblock (S, M) of the warp's rows
-    if (is_sb(FMT)) at += kMathWarps * 1024;
+    float* scratch = reinterpret_cast<float*>(at + warp * kWarpScratch); // of a math warp
+    at += kMathWarps * kWarpScratch;
     uint64_t* full = reinterpret_cast<uint64_t*>(at);
     uint64_t* empty = full + kMaxRing;
     at += 2 * kMaxRing * 8;
-    int* flag = reinterpret_cast<int*>(at);
-    at += 16;
+    Desc* desc = reinterpret_cast<Desc*>(at);
+    at += kDescs * sizeof(Desc);
     const Groups g = groups_at(at, p.pl.E);
 
     if (tid == 0) {
         for (int s = 0; s < ring; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], is_sb(FMT) ? 1 : 33);                    // the copy thread, and the scale copies of 32 lanes
             mbar_init(&empty[s], kMathWarps);
         }
         fence_mbar_init();
     }
-    if (warp == 0) scan_groups(p.pl, g, lane);
+    if (warp == kMathWarps) scan_groups(p.pl, g, lane);
     __syncthreads();
     grid_dep_launch();
 
@@ -644,74 +684,93 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const __grid_cons
     const long long S = g.unit[p.pl.E] * T;
     const long long Gc = min((long long)gridDim.x, S);                   // CTAs with work
     if ((long long)blockIdx.x >= Gc) {
-        grid_dep_wait();                                  // no kernel after this one runs beside prep_kernel
+        grid_dep_wait();                                                 // no kernel after this one runs beside prep_kernel
         return;
     }
     const long long s0 = blockIdx.x * S / Gc, s1 = ((long long)blockIdx.x + 1) * S / Gc;
+    const uint32_t base = smem_u32(smem);
+    constexpr uint32_t kXOff = kRowsPerTile * G::RB, kSOff = kXOff + NB * G::XB;   // parts of a stage: codes, x, scales
 
     if (warp == kMathWarps) {
         // ------------------------------------------------------------ copies
-        // The codes of the first `ring` stages are asked for before the
+        // The weights of the first `ring` stages are asked for before the
         // prepared activations are waited for.
-        const uint32_t base = smem_u32(smem);
-        const int n = (int)min(s1 - s0, (long long)0x7fffffff);
-        int issued = 0;
-        bool ok = true;
-        auto expect = [&](const Work& w) { return (uint32_t)(kRowsPerTile * G::RB + ((w.rows + 7) / 8) * G::XB); };
-        auto scales_ahead = [&](const Work& w, int k, bool first) {      // 32-byte sectors of the tile's scale rows into L2
+        const bool copies = !(p.test_flags & kTestNoCopies);
+        auto weights = [&](const Work& w, int k, int slot) {
+            const uint32_t st = base + slot * p.stage_bytes;
+            const int row0 = w.e * p.pl.N + w.n0;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&full[slot], (uint32_t)(kRowsPerTile * G::RB + ((w.rows + 7) / 8) * G::XB));
+                tma_codes(st, &p.cmap, k * G::RB, row0, &full[slot]);
+            }
             if constexpr (!is_sb(FMT)) {
-                constexpr int BS = G::KS / sym_group(FMT) * 2;           // scale bytes per row and stage
-                if (first || (k * BS) % 32 == 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const unsigned long long row = (unsigned long long)w.e * p.pl.N + w.n0 + 32 * i + lane;
-                        if (row < p.total_rows && (uint32_t)(k * BS) < p.srb) prefetch_l2(p.scales + row * p.srb + k * BS);
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 32 * i + lane;
+                    const unsigned long long row = min((unsigned long long)(row0 + r), p.total_rows - 1);
+                    const uint8_t* src = p.scales + row * p.srb;
+                    const uint32_t dst = st + kSOff + r * G::SB;
+                    const uint32_t b0 = k * G::SB;
+                    if (G::SB >= 8 && (p.srb & 7u) == 0u) {
+#pragma unroll
+                        for (int b = 0; b < G::SB; b += 8) cp_async<8>(dst + b, b0 + b < p.srb ? src + b0 + b : src, b0 + b < p.srb);
+                    } else if ((p.srb & 3u) == 0u) {
+#pragma unroll
+                        for (int b = 0; b < G::SB; b += 4) cp_async<4>(dst + b, b0 + b < p.srb ? src + b0 + b : src, b0 + b < p.srb);
+                    } else {                                             // an odd number of scales per row
+#pragma unroll
+                        for (int b = 0; b < G::SB; b += 2) {
+                            const uint16_t v = b0 + b < p.srb ? *reinterpret_cast<const uint16_t*>(src + b0 + b) : (uint16_t)0;
+                            asm volatile("st.shared.u16 [%0], %1;" :: "r"(dst + b), "h"(v) : "memory");
+                        }
                     }
                 }
+                if ((p.srb & 3u) == 0u) cp_async_arrive(&full[slot]);
+                else mbar_arrive(&full[slot]);
             }
         };
-        const int head = min(n, ring);
-        const bool copies = !(p.test_flags & kTestNoCopies);
-        {
-            long long s = s0;
-            for (int i = 0; i < head;) {
-                const Work w = get_work(p.pl, g, s / T);
-                for (int k = (int)(s % T); k < T && i < head; ++k, ++i, ++s) {
-                    if (lane == 0 && copies) {
-                        mbar_arrive_expect_tx(&full[i], expect(w));
-                        tma_codes(base + i * p.stage_bytes, &p.cmap, k * G::RB, w.e * p.pl.N + w.n0, &full[i]);
-                    }
-                    scales_ahead(w, k, i == 0);
-                }
+        auto describe = [&](const Work& w, long long unit, int k0, int k1, int u) {
+            if (lane == 0) {
+                const long long us = unit * T;
+                Desc d = {w.n0, w.row0, w.rows, k0, k1, (int)blockIdx.x, (int)blockIdx.x, w.e};
+                if (k0 > 0) d.first = (int)(((us + 1) * Gc - 1) / S);
+                if (k1 < T) d.last = (int)(((us + T) * Gc - 1) / S);
+                desc[u % kDescs] = d;
+            }
+        };
+        const int n = (int)(s1 - s0);
+        const long long unit0 = s0 / T;
+        const int kfirst = (int)(s0 - unit0 * T), head = min(n, ring);
+        if (copies) {
+            int i = 0, k = kfirst, u = 0;
+            for (long long unit = unit0; i < head; ++unit, k = 0, ++u) {
+                const Work w = get_work(p.pl, g, unit);
+                describe(w, unit, k, min(T, k + n - i), u);
+                for (; k < T && i < head; ++k, ++i) weights(w, k, i);
             }
         }
         grid_dep_wait();
         asm volatile("fence.proxy.async.global;" ::: "memory");
-        long long s = s0;
-        int slot = 0, wrap = 0;
-        for (int i = 0; i < n && ok;) {
-            const Work w = get_work(p.pl, g, s / T);
-            const int tiles = (w.rows + 7) / 8;
-            for (int k = (int)(s % T); k < T && i < n; ++k, ++i, ++s) {
+        int slot = 0, wrap = 0, issued = 0, u = 0, k = kfirst;
+        bool ok = copies;
+        for (long long unit = unit0; ok && issued < n; ++unit, k = 0, ++u) {
+            const Work w = get_work(p.pl, g, unit);
+            const int k1 = min(T, k + n - issued), tiles = (w.rows + 7) / 8;
+            for (bool begin = true; k < k1; ++k, begin = false) {
                 if (wrap && !__all_sync(~0u, mbar_wait_bounded(&empty[slot], (uint32_t)(wrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns))) {
                     ok = false;
                     break;
                 }
-                if (lane == 0 && copies) {
-                    const uint32_t st = base + slot * p.stage_bytes;
-                    if (wrap) {
-                        mbar_arrive_expect_tx(&full[slot], expect(w));
-                        tma_codes(st, &p.cmap, k * G::RB, w.e * p.pl.N + w.n0, &full[slot]);
-                    }
-                    for (int j = 0; j < tiles; ++j)
-                        bulk_x(st + kRowsPerTile * G::RB + j * G::XB, p.xf + ((size_t)(w.tile0 + j) * T + k) * G::XB, G::XB, &full[slot]);
-                    ++issued;
-                }
-                if (wrap) scales_ahead(w, k, false);
+                if (begin && wrap) describe(w, unit, k, k1, u);
+                __syncwarp();
+                if (wrap) weights(w, k, slot);
+                if (lane < tiles)
+                    bulk_x(base + slot * p.stage_bytes + kXOff + lane * G::XB, p.xf + ((size_t)(w.tile0 + lane) * T + k) * G::XB, G::XB, &full[slot]);
+                ++issued;
                 if (++slot == ring) { slot = 0; ++wrap; }
             }
         }
-        // copies in flight (a consumer gave up) land before the CTA leaves
+        // copies in flight (a math warp gave up) land before the CTA leaves
         if (lane == 0)
             for (int q = 0; q < ring && q < issued; ++q) {
                 const int uses = issued / ring + (q < issued % ring ? 1 : 0);
@@ -721,16 +780,15 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const __grid_cons
     }
 
     // ---------------------------------------------------------------- math
-    const int wr = 32 * (warp & 3), half = warp >> 2;
-    const uint32_t base = smem_u32(smem);
-    bool alive = true;                                    // false after a wait ran out: go on without waiting
-    int slot = 0, wrap = 0;
+    // A warp keeps to its own 32 weight rows from the codes to y: no barrier
+    // among the warps. One whose wait runs out leaves.
+    const int wr = 32 * warp;
+    int slot = 0, wrap = 0, left = (int)(s1 - s0);
     grid_dep_wait();                                      // counters and adapter terms come from prep_kernel
-    for (long long s = s0; s < s1;) {
-        const long long unit = s / T;
-        const Work w = get_work(p.pl, g, unit);
-        const int k0 = (int)(s - unit * T), k1 = (int)min((long long)T, k0 + (s1 - s));
-        const int tiles = (w.rows + 7) / 8;
+    for (int u = 0; left > 0; ++u) {
+        if (!__all_sync(~0u, mbar_wait_bounded(&full[slot], (uint32_t)wrap & 1u, kStatusTmaWait, 0u, p.wait_ns))) return;
+        const Desc d = desc[u % kDescs];
+        const int tiles = (d.rows + 7) / 8;
         float acc[2][NB][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -738,124 +796,80 @@ __global__ void __launch_bounds__(kRowsThreads, 2) rows_kernel(const __grid_cons
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[mt][nb][i] = 0.0f;
-        uint32_t row[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            row[i] = (uint32_t)min((unsigned long long)w.e * p.pl.N + w.n0 + wr + 8 * i + (lane >> 2), p.total_rows - 1);
-        Scales<FMT> nxt;
-        load_scales<FMT>(p, row, k0, half, nxt);
-        for (int k = k0; k < k1; ++k) {
-            const Scales<FMT> cur = nxt;
-            if (k + 1 < k1) load_scales<FMT>(p, row, k + 1, half, nxt);
-            if (alive) alive = __all_sync(~0u, mbar_wait_bounded(&full[slot], (uint32_t)wrap & 1u, kStatusTmaWait, 0u, p.wait_ns));
+        for (int k = d.k0; k < d.k1; ++k) {
+            if (k > d.k0 && !__all_sync(~0u, mbar_wait_bounded(&full[slot], (uint32_t)wrap & 1u, kStatusTmaWait, 0u, p.wait_ns))) return;
             const uint32_t st = base + slot * p.stage_bytes;
-            stage_math<FMT, NB>(st, st + kRowsPerTile * G::RB, smin, wr, half, lane, tiles, cur, acc);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                Scales<FMT> sc;
+                read_scales<FMT>(st + kSOff, wr, half, lane >> 2, sc);
+                stage_math<FMT, NB>(st, st + kXOff, smem_u32(scratch), wr, half, lane, tiles, sc, acc);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
             if (++slot == ring) { slot = 0; ++wrap; }
         }
-        s += k1 - k0;
+        left -= d.k1 - d.k0;
 
-        // the two halves of K
-        bar_sync(1, 256);                                 // the previous unit's tile has been stored
-        if (half) {
+        if (d.first != d.last) {
+            // a part of a unit: CTA c's part lies in slot 2c (it began in an earlier CTA) or 2c + 1
+            constexpr int kPart = kMathWarps * 2 * NB * 32;              // float4 per slot
+            float4* part = reinterpret_cast<float4*>(p.part) + warp * (2 * NB * 32) + lane;
+            float4* mypart = part + (size_t)(2 * blockIdx.x + (d.k0 == 0)) * kPart;
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
-                    *reinterpret_cast<float4*>(red + ((mt * NB + nb) * 128 + tid - 128) * 4) =
-                        make_float4(acc[mt][nb][0], acc[mt][nb][1], acc[mt][nb][2], acc[mt][nb][3]);
-        }
-        bar_sync(1, 256);
-        if (!half) {
+                    __stcg(mypart + (mt * NB + nb) * 32, make_float4(acc[mt][nb][0], acc[mt][nb][1], acc[mt][nb][2], acc[mt][nb][3]));
+            __threadfence();
+            __syncwarp();
+            unsigned old = 0;
+            if (lane == 0) old = atomicAdd(&p.count[d.first * kMathWarps + warp], 1u);
+            old = __shfl_sync(~0u, old, 0);
+            if (old != (unsigned)(d.last - d.first)) continue;           // not the last to arrive
+            __threadfence();
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    const float4 v = *reinterpret_cast<const float4*>(red + ((mt * NB + nb) * 128 + tid) * 4);
-                    acc[mt][nb][0] += v.x;
-                    acc[mt][nb][1] += v.y;
-                    acc[mt][nb][2] += v.z;
-                    acc[mt][nb][3] += v.w;
-                }
-            bool mine = true;                             // whether this CTA stores the unit
-            if (k0 > 0 || k1 < T) {
-                // a part of a unit: CTA c's part lies in slot 2c (it began in an earlier CTA) or 2c + 1
-                const long long us = unit * T;
-                const int first = (int)(((us + 1) * Gc - 1) / S), last = (int)(((us + T) * Gc - 1) / S);
-                float4* mypart = reinterpret_cast<float4*>(p.part) + (size_t)(2 * blockIdx.x + (k0 == 0)) * (256 * NB);
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-                        __stcg(mypart + (mt * NB + nb) * 128 + tid, make_float4(acc[mt][nb][0], acc[mt][nb][1], acc[mt][nb][2], acc[mt][nb][3]));
-                __threadfence();
-                bar_sync(2, 128);
-                if (tid == 0) *flag = atomicAdd(&p.count[first], 1u) == (unsigned)(last - first);
-                bar_sync(2, 128);
-                mine = *flag != 0;
-                if (mine) {
-                    __threadfence();
-#pragma unroll
-                    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            for (int c = first; c <= last; ++c) {
-                                const float4 u = __ldcg(reinterpret_cast<const float4*>(p.part) +
-                                                        (size_t)(2 * c + (c == first)) * (256 * NB) + (mt * NB + nb) * 128 + tid);
-                                v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-                            }
-                            acc[mt][nb][0] = v.x; acc[mt][nb][1] = v.y; acc[mt][nb][2] = v.z; acc[mt][nb][3] = v.w;
-                        }
-                }
-            } else {
-                bar_sync(2, 128);                         // `red` has been read
-                if (tid == 0) *flag = 1;
-            }
-            if (mine) {                                   // the tile as [activation row][weight row]
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            red[(8 * nb + 2 * (lane & 3) + (i & 1)) * 132 + wr + 16 * mt + (lane >> 2) + 8 * (i >> 1)] = acc[mt][nb][i];
-            }
-        }
-        bar_sync(1, 256);
-        if (*flag) {
-            const int n = w.n0 + 4 * lane, N = p.pl.N;
-            for (int i = warp; i < w.rows; i += kMathWarps) {
-                const int m = w.row0 + i;
-                const int out = p.out_rows ? p.out_rows[m] : m;
-                if (out < 0 || out >= p.Ty || n >= N) continue;
-                const float4 f = *reinterpret_cast<const float4*>(red + i * 132 + 4 * lane);
-                float v[4] = {f.x, f.y, f.z, f.w};
-                if (p.adapter) add_adapter(p, m, n, v);
-                if (p.act) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        v[q] = v[q] > 0.0f || v[q] != v[q] ? v[q] : 0.0f;
-                        v[q] *= v[q];
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int c = d.first; c <= d.last; ++c) {
+                        const float4 w = __ldcg(part + (size_t)(2 * c + (c == d.first)) * kPart + (mt * NB + nb) * 32);
+                        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
                     }
+                    acc[mt][nb][0] = v.x; acc[mt][nb][1] = v.y; acc[mt][nb][2] = v.z; acc[mt][nb][3] = v.w;
                 }
-                const size_t o = (size_t)out * N + n;
-                if ((N & 3) == 0) {
-                    if (p.ybf16) {
-                        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + o) =
-                            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                    } else {
-                        *reinterpret_cast<float4*>(static_cast<float*>(p.y) + o) = make_float4(v[0], v[1], v[2], v[3]);
-                    }
-                } else {
+        }
+        // through shared memory to eight consecutive weight rows per lane
+        const int n = d.n0 + wr + 8 * (lane & 3);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (n + q < N) store_y(p.y, o + q, v[q], p.ybf16);
+        for (int nb = 0; nb < NB; ++nb) {
+            if (nb >= tiles) break;
+            __syncwarp();
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    scratch[(2 * (lane & 3) + (i & 1)) * 36 + 16 * mt + (lane >> 2) + 8 * (i >> 1)] = acc[mt][nb][i];
+            __syncwarp();
+            const int i = 8 * nb + (lane >> 2), m = d.row0 + i;
+            if (i >= d.rows || n >= p.pl.N) continue;
+            const int out = p.out_rows ? p.out_rows[m] : m;
+            if (out < 0 || out >= p.Ty) continue;
+            const float* f = scratch + (lane >> 2) * 36 + 8 * (lane & 3);
+            const float4 f0 = *reinterpret_cast<const float4*>(f), f1 = *reinterpret_cast<const float4*>(f + 4);
+            float v[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+            if (p.adapter) add_adapter(p, m, n, v);
+            if (p.act) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    v[q] = v[q] > 0.0f || v[q] != v[q] ? v[q] : 0.0f;
+                    v[q] *= v[q];
                 }
             }
+            store8(p, out, n, v);
         }
+        __syncwarp();                                     // scratch is read before it is written again
     }
 }
 
@@ -878,7 +892,7 @@ EncodeTiled encoder() {
     return fn;
 }
 
-constexpr int kMaxCtas = 512;          // CTAs of a launch at most (two per SM)
+constexpr int kMaxCtas = 768;          // CTAs of a launch at most
 
 // 8-row tiles per unit: as many as an even split of the rows fills, since a
 // group with more rows than a unit holds streams its weights once per unit.
@@ -897,7 +911,7 @@ Layout layout(int R, int K, int E, int rank) {
     l.xf = 0;
     l.part = round16((size_t)l.tiles * l.T * Geo<FMT>::XB);
     l.count = l.part + (size_t)2 * kMaxCtas * pick_nb(R, E) * 4096;
-    l.t = l.count + kMaxCtas * 4;
+    l.t = l.count + kMaxCtas * kMathWarps * 4;
     l.total = l.t + round16((size_t)R * rank * 4);
     return l;
 }
@@ -906,9 +920,12 @@ template <int FMT, int NB>
 cudaError_t launch_product(const RowsParams& p0, cudaStream_t st) {
     using G = Geo<FMT>;
     RowsParams p = p0;
-    p.stage_bytes = (kRowsPerTile * G::RB + NB * G::XB + 1023) & ~1023;
-    const size_t fixed = 1024 + 8 * NB * 132 * 4 + (is_sb(FMT) ? kMathWarps * 1024 : 0) + 2 * kMaxRing * 8 + 16 + groups_bytes(p.pl.E);
-    p.ring = (int)((kRowsSmemMax - fixed) / p.stage_bytes);
+    p.stage_bytes = (kRowsPerTile * (G::RB + G::SB) + NB * G::XB + 1023) & ~1023;
+    const size_t fixed = 1024 + kMathWarps * kWarpScratch + 2 * kMaxRing * 8 + kDescs * sizeof(Desc) + groups_bytes(p.pl.E);
+    constexpr size_t smem_max = kSmemPerSm / 2 - 1024;
+    int per_sm = ctas_per_sm(FMT, NB);
+    while (per_sm > 2 && kSmemPerSm / per_sm - 1024 < fixed + 2 * (size_t)p.stage_bytes) --per_sm;   // two stages at least
+    p.ring = (int)((kSmemPerSm / per_sm - 1024 - fixed) / p.stage_bytes);
     if (p.ring > kMaxRing) p.ring = kMaxRing;
     if (p.ring < 2) return cudaErrorInvalidValue;
     auto kern = rows_kernel<FMT, NB>;
@@ -918,11 +935,11 @@ cudaError_t launch_product(const RowsParams& p0, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsSmemMax);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_max);
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&attr_done, bit, __ATOMIC_RELEASE);
     }
-    int ctas = 2 * sm_count();
+    int ctas = per_sm * sm_count();
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -953,7 +970,7 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
     q.rows_x = a.T;
     q.xf = ws + l.xf;
     q.count = reinterpret_cast<unsigned*>(ws + l.count);
-    q.n_count = kMaxCtas;
+    q.n_count = kMaxCtas * kMathWarps;
     q.tiles_max = l.tiles;
     q.kblocks = (l.T * G::KS / 8 + 255) / 256;
     q.adapter = a.adapter;
