@@ -54,9 +54,9 @@ namespace {
 constexpr int kRowsPerTile = 128;      // weight rows of a unit
 constexpr int kMathWarps = 4;          // 32 weight rows each
 constexpr int kRowsThreads = 32 * (kMathWarps + 1);
-constexpr int kMaxRing = 6;
+constexpr int kMaxRing = 6;            // code slots at most
+constexpr int kXRing = 2;              // slots of activations and scales
 constexpr int kDescs = 8;              // unit descriptors in flight: more than kMaxRing + 1
-constexpr int kWarpScratch = 1280;     // shared bytes per math warp: an 8 x 32 result tile, or superblock scales
 constexpr size_t kSmemPerSm = 228 * 1024;
 
 // Geometry of a format's K stage.
@@ -64,9 +64,18 @@ template <int FMT>
 struct Geo {
     static constexpr int KS = is_w8(FMT) || FMT == kFmtW6G16 ? 128 : 256;         // K per stage
     static constexpr int RB = FMT == kFmtW4G64 ? 128 : is_w8(FMT) ? 128 : FMT == kFmtW6G16 ? 96 : sb_record(FMT);
-    static constexpr int XB = KS * 16 + (is_sb(FMT) ? 256 : 0);                   // bytes of one 8-row tile's stage
+    static constexpr int XB = KS * 16 + (is_w8(FMT) ? 0 : 256);                   // bytes of one 8-row tile's stage
     static constexpr int SB = is_sb(FMT) ? 0 : KS / sym_group(FMT) * 2;           // scale bytes of a weight row's stage
     static constexpr bool SWZ = RB == 128;
+    static constexpr int CB = (kRowsPerTile * RB + 1023) & ~1023;                 // a code slot
+    // Codes that fit a thread's registers are taken out of their slot at once, so that the slot refills
+    // while they are used (the wider codes' high-bit planes do not fit).
+    static constexpr bool EARLY = RB == 128 || FMT == kFmtW4SB32;
+    static constexpr int SCRATCH = is_sb(FMT) ? 2048 : 1024;                      // shared bytes of a math warp
+    // Sub-byte codes u unpack as 2^B + u (B code bits, the top of bf16's seven fraction bits); the products
+    // start from -OFF sum x, so that they give sum q x (symmetric) or sum u x (superblocks).
+    static constexpr int B = FMT == kFmtW6G16 ? 6 : FMT == kFmtW4G64 ? 4 : is_sb(FMT) ? sb_bits(FMT) : 0;
+    static constexpr float OFF = is_sb(FMT) ? (float)(1 << B) : 1.5f * (float)(1 << B);
 };
 
 // CTAs per SM: four while their accumulators and two stages each fit.
@@ -97,7 +106,7 @@ struct RowsParams {
     const __nv_bfloat16* B;
     const float* t;                    // [R][r]
     int n_adapters, r;
-    int ring, stage_bytes;
+    int ring, xslot;                   // code slots; bytes of an activation slot
     unsigned long long wait_ns;
     int test_flags;
 };
@@ -187,7 +196,9 @@ __device__ __forceinline__ int find_group(const T* a, int E, T v) {
 }
 
 // ------------------------------------------------------------------- prep
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 128;
+constexpr int kPrepUnroll = 4;         // 16-byte chunks per thread
+constexpr int kPrepChunks = 4 * (kPrepThreads / 32) * kPrepUnroll;   // of each of a block's eight rows
 
 __device__ __forceinline__ float bf16_sum8(uint4 v) {
     return ((bf16lo_f32(v.x) + bf16hi_f32(v.x)) + (bf16lo_f32(v.y) + bf16hi_f32(v.y))) +
@@ -195,7 +206,7 @@ __device__ __forceinline__ float bf16_sum8(uint4 v) {
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kPrepThreads) prep_kernel(const PrepParams p) {
+__global__ void __launch_bounds__(kPrepThreads, 16) prep_kernel(const PrepParams p) {
     using G = Geo<FMT>;
     extern __shared__ __align__(16) uint8_t sm[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -217,13 +228,20 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const PrepParams p) 
             src = p.in_rows ? p.in_rows[row] : row;
             if (src < 0 || src >= p.rows_x) src = -1;
         }
-        const int c_end = min((kb + 1) * 256, p.pl.T * G::KS / 8);           // 8-value chunks of this block's K range
+        const int c_end = p.pl.T * G::KS / 8;                                // 8-value chunks of a row, padded to whole stages
         uint8_t* out = p.xf + (size_t)tile * p.pl.T * G::XB;
-        for (int c0 = kb * 256 + 4 * warp; c0 < c_end; c0 += 4 * (kPrepThreads / 32)) {
-            const int c = c0 + (lane & 3);
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (src >= 0 && 8 * c < p.pl.K)
-                v = *reinterpret_cast<const uint4*>(p.x + (size_t)src * p.pl.K + 8 * c);
+        uint4 vv[kPrepUnroll];
+#pragma unroll
+        for (int q = 0; q < kPrepUnroll; ++q) {
+            const int c = kb * kPrepChunks + q * (kPrepThreads / 8) + 4 * warp + (lane & 3);
+            vv[q] = make_uint4(0u, 0u, 0u, 0u);
+            if (src >= 0 && 8 * c < p.pl.K) vv[q] = *reinterpret_cast<const uint4*>(p.x + (size_t)src * p.pl.K + 8 * c);
+        }
+#pragma unroll
+        for (int q = 0; q < kPrepUnroll; ++q) {
+            const int c = kb * kPrepChunks + q * (kPrepThreads / 8) + 4 * warp + (lane & 3);
+            if (c >= c_end) break;                       // the same for the whole warp
+            const uint4 v = vv[q];
             const int st = 8 * c / G::KS, cs = c - st * (G::KS / 8);         // stage, chunk in the stage
             uint8_t* o = out + (size_t)st * G::XB;
             if constexpr (G::KS == 256) {
@@ -234,12 +252,10 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const PrepParams p) 
                 w.z = prmt(v.y, v.w, 0x5410u);
                 w.w = prmt(v.y, v.w, 0x7632u);
                 *reinterpret_cast<uint4*>(o + ((cs >> 2) * 32 + lane) * 16) = w;
-                if constexpr (is_sb(FMT)) {
-                    float s = bf16_sum8(v);
-                    s += __shfl_xor_sync(~0u, s, 1);
-                    s += __shfl_xor_sync(~0u, s, 2);
-                    if ((lane & 3) == 0) *reinterpret_cast<float*>(o + G::KS * 16 + ((cs >> 2) * 8 + (lane >> 2)) * 4) = s;
-                }
+                float s = bf16_sum8(v);                  // the row's sum over 32 weights
+                s += __shfl_xor_sync(~0u, s, 1);
+                s += __shfl_xor_sync(~0u, s, 2);
+                if ((lane & 3) == 0) *reinterpret_cast<float*>(o + G::KS * 16 + ((cs >> 2) * 8 + (lane >> 2)) * 4) = -G::OFF * s;
             } else {
                 // four-weight words unpack as the pairs (0, 2), (1, 3); lane t of a quad takes weights
                 // 4t .. 4t + 3 of each 16-weight step, two steps per 16 bytes
@@ -251,19 +267,24 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const PrepParams p) 
                     const uint2 w = make_uint2(prmt(a, b, 0x5410u), prmt(a, b, 0x7632u));
                     *reinterpret_cast<uint2*>(o + ((cs >> 2) * 32 + g8 * 4 + t) * 16 + half * 8) = w;
                 }
+                if constexpr (!is_w8(FMT)) {
+                    float s = bf16_sum8(v);              // over 16 weights
+                    s += __shfl_xor_sync(~0u, s, 1);
+                    if ((lane & 1) == 0) *reinterpret_cast<float*>(o + G::KS * 16 + ((cs >> 1) * 8 + g8) * 4) = -G::OFF * s;
+                }
             }
         }
     } else {
         // t[m][j] = s_a A_a[j] . x[m]: one warp per (m, j)
-        const int per = (p.r + 7) / 8;
-        const int b = blockIdx.x - nx, m = b / per, j = (b % per) * 8 + warp;
+        const int per = p.r / (kPrepThreads / 32);
+        const int b = blockIdx.x - nx, m = b / per, j = (b % per) * (kPrepThreads / 32) + warp;
         const int a = p.adapter[m];
         if (a < 0 || a >= p.n_adapters) return;
         if (p.ranks && j >= p.ranks[a]) return;
         const uint4* x = reinterpret_cast<const uint4*>(p.x + (size_t)m * p.pl.K);
         const uint4* w = reinterpret_cast<const uint4*>(p.A + ((size_t)a * p.r + j) * p.pl.K);
         float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll 4
+#pragma unroll 2
         for (int c = lane; c < p.pl.K / 8; c += 32) {
             const uint4 u = x[c], v = w[c];
             const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
@@ -301,12 +322,13 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
 
-// D += A B, A 16 x 16 (row), B 16 x 8 (col), bf16 with fp32 sums.
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// D = A B + C, A 16 x 16 (row), B 16 x 8 (col), bf16 with fp32 sums.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1,
+                                         float c2, float c3) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // (v & m) | c
@@ -328,24 +350,21 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 }
 
 // ------------------------------------------------------------------ unpack
-// A bf16 has seven fraction bits, so 0x4300 | v is 128 + v for v < 128:
-// exact, and the subtraction of an integer from it is exact too.
+// A bf16 has seven fraction bits. Codes of B < 7 bits go to the top B of them
+// under the exponent of 2^B: 2^B + u, exact, with one shift and one logic
+// operation per two weights (two more for the bits above a nibble).
+__device__ __forceinline__ uint32_t shift_to(uint32_t w, int from, int to) { return from >= to ? w >> (from - to) : w << (to - from); }
 
-// Eight nibbles of w as the pairs (0, 4), (1, 5), (2, 6), (3, 7), minus `off` - 128.
-template <uint32_t OFF2>
-__device__ __forceinline__ void unpack_nibbles(uint32_t w, uint32_t (&o)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = sub_bf16x2(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u), OFF2);
-}
-// The same with the codes' higher bits: h holds them at bits 16 (k / 4) + B (k % 4), B = 1 or 2 bits per code.
-template <int B, uint32_t OFF2>
-__device__ __forceinline__ void unpack_wide(uint32_t w, uint32_t h, uint32_t (&o)[4]) {
-    constexpr uint32_t HM = B == 1 ? 0x00100010u : 0x00300030u;
+// Eight nibbles of w as the pairs (0, 4), (1, 5), (2, 6), (3, 7); h holds the
+// codes' B - 4 higher bits at bits 16 (k / 4) + (B - 4) (k % 4).
+template <int B>
+__device__ __forceinline__ void unpack_nibbles(uint32_t w, uint32_t h, uint32_t (&o)[4]) {
+    constexpr uint32_t P = 7 - B, M = 0x000F000Fu << P, E = (0x4180u + 0x80u * (B - 4)) * 0x10001u;
+    constexpr uint32_t HM = (B == 5 ? 0x00010001u : 0x00030003u) << (P + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int s = 4 - B * i;
-        const uint32_t hs = s >= 0 ? h << (s < 0 ? 0 : s) : h >> (s < 0 ? -s : 0);
-        o[i] = sub_bf16x2(and_or(hs, HM, and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u)), OFF2);
+        o[i] = and_or(shift_to(w, 4 * i, P), M, E);
+        if (B > 4) o[i] = and_or(shift_to(h, (B - 4) * i, P + 4), HM, o[i]);
     }
 }
 // Four bytes u = q + 128 of w as the pairs (0, 2), (1, 3): the low seven bits
@@ -390,53 +409,52 @@ __device__ __forceinline__ float half_at(uint32_t w, int h) {
     return __half2float(__ushort_as_half((uint16_t)(h ? w >> 16 : w & 0xffffu)));
 }
 
-// One warp's share of a stage: weight rows wr .. wr + 31 over half the
+// The 32-bit code words of a thread's four weight rows (8 mr + lane / 4 of the
+// warp's 32) in a stage: word lane % 4 of each of the stage's eight 16-byte
+// chunks.
+template <int FMT>
+__device__ __forceinline__ void take_codes(uint32_t cs, int wr, int lane, uint32_t (&cw)[8][4]) {
+    using G = Geo<FMT>;
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int mr = 0; mr < 4; ++mr) {
+            const uint32_t r = wr + 8 * mr + g;
+            cw[c][mr] = lds32_a(G::SWZ ? cs + r * 128 + ((c ^ g) << 4) + 4 * t : cs + r * G::RB + 16 + 16 * c + 4 * t);
+        }
+}
+
+// A superblock stage's scales, each lane those of weight row wr + lane: S_j and
+// M_j / 2^B of the eight groups to shared memory.
+template <int FMT>
+__device__ __forceinline__ void decode_superblock(uint32_t cs, uint32_t smin, int wr, int lane) {
+    using G = Geo<FMT>;
+    const uint4 hd = lds128_a(cs + (uint32_t)(wr + lane) * G::RB);
+    const float d = half_at(hd.x, 0), dm = __fmul_rn(half_at(hd.x, 1), 1.0f / G::OFF);
+    __syncwarp();                                        // the previous stage's values have been read
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        // fields 2q and 2q + 1 of the scales (from bit 12 q of the string) and of the mins (from bit 48 + 12 q)
+        const uint32_t f0 = q < 2 ? hd.y >> (12 * q) : __funnelshift_r(q == 2 ? hd.y : hd.z, q == 2 ? hd.z : 0u, (12 * q) & 31);
+        const uint32_t f1 = q < 2 ? __funnelshift_r(hd.z, hd.w, 16 + 12 * q) : hd.w >> (12 * q - 16);
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(smin + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)), "f"(__fmul_rn(d, (float)(f0 & 63u))), "f"(__fmul_rn(dm, (float)(f1 & 63u))),
+                        "f"(__fmul_rn(d, (float)((f0 >> 6) & 63u))), "f"(__fmul_rn(dm, (float)((f1 >> 6) & 63u))) : "memory");
+    }
+    __syncwarp();
+}
+
+// One warp's share of a stage: weight rows wr .. wr + 31 over half `half` of the
 // stage's K, all live 8-row tiles. acc[m16][tile]: D fragment (weight rows
 // 16 m16 + lane / 4, + 8; activation rows 2 (lane % 4), + 1).
 template <int FMT, int NB>
-__device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t smin, int wr, int half, int lane, int tiles,
-                                           const Scales<FMT>& sc, float (&acc)[2][NB][4]) {
+__device__ __forceinline__ void stage_math(uint32_t cs, const uint32_t (&cw)[8][4], uint32_t xs, uint32_t smin, int wr, int half,
+                                           int lane, int tiles, const Scales<FMT>& sc, float (&acc)[2][NB][4]) {
     using G = Geo<FMT>;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t xl = xs + lane * 16;
-    if constexpr (FMT == kFmtW4G64) {
-#pragma unroll
-        for (int gi = 0; gi < 2; ++gi) {
-            const int gr = 2 * half + gi;
-            uint32_t a[2][4][4];                         // [m16][step][register]
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int mr = 0; mr < 4; ++mr) {         // row 8 mr + g of the warp's 32
-                    const uint32_t r = wr + 8 * mr + g;
-                    uint32_t o[4];
-                    unpack_nibbles<0x43084308u>(lds32_a(cs + r * 128 + (((2 * gr + j) ^ g) << 4) + 4 * t), o);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        a[mr >> 1][2 * j + h][mr & 1] = o[2 * h];
-                        a[mr >> 1][2 * j + h][2 + (mr & 1)] = o[2 * h + 1];
-                    }
-                }
-            float s[4];
-#pragma unroll
-            for (int mr = 0; mr < 4; ++mr) s[mr] = half_at(sc.w[mr][0], gi);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                if (NB > 1 && nb >= tiles) break;
-                const uint4 x0 = lds128_a(xl + nb * G::XB + (2 * gr) * 512), x1 = lds128_a(xl + nb * G::XB + (2 * gr + 1) * 512);
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma16816(d, a[mt][0], x0.x, x0.y);
-                    mma16816(d, a[mt][1], x0.z, x0.w);
-                    mma16816(d, a[mt][2], x1.x, x1.y);
-                    mma16816(d, a[mt][3], x1.z, x1.w);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[mt][nb][i] = fmaf(s[2 * mt + (i >> 1)], d[i], acc[mt][nb][i]);
-                }
-            }
-        }
-    } else if constexpr (is_w8(FMT) || FMT == kFmtW6G16) {
+    if constexpr (is_w8(FMT) || FMT == kFmtW6G16) {
         constexpr bool G16 = sym_group(FMT) == 16;
         float gsum[2][NB][4];
         if (!G16) {
@@ -454,19 +472,18 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t sm
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int mr = 0; mr < 4; ++mr) {
-                    const uint32_t r = wr + 8 * mr + g;
                     const int st = 2 * sp + h;           // step in the half stage
                     uint32_t o[2];
                     if constexpr (FMT == kFmtW6G16) {
-                        const uint32_t b = cs + r * G::RB + 48 * half;
+                        const uint32_t b = cs + (uint32_t)(wr + 8 * mr + g) * G::RB + 48 * half;
                         const uint32_t n = lds16_a(b + 8 * st + 2 * t);
                         uint32_t pl;
                         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(pl) : "r"(b + 32 + 4 * st + t));
-                        const uint32_t w = n | (n << 8), hh = pl | (pl << 12);
-                        o[0] = sub_bf16x2(and_or(hh << 4, 0x00300030u, and_or(w, 0x000F000Fu, 0x43004300u)), 0x43204320u);
-                        o[1] = sub_bf16x2(and_or(hh << 2, 0x00300030u, and_or(w >> 4, 0x000F000Fu, 0x43004300u)), 0x43204320u);
+                        const uint32_t w = n | (n << 8), hh = pl | (pl << 12);     // pairs (0, 2), (1, 3), as for the bytes
+                        o[0] = and_or(hh << 5, 0x00600060u, and_or(w << 1, 0x001E001Eu, 0x42804280u));
+                        o[1] = and_or(hh << 3, 0x00600060u, and_or(w >> 3, 0x001E001Eu, 0x42804280u));
                     } else {
-                        unpack_bytes(lds32_a(cs + r * 128 + (((4 * half + st) ^ g) << 4) + 4 * t), o);
+                        unpack_bytes(cw[4 * half + st][mr], o);
                     }
                     a[mr >> 1][h][mr & 1] = o[0];
                     a[mr >> 1][h][2 + (mr & 1)] = o[1];
@@ -478,9 +495,14 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t sm
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     if constexpr (G16) {
-                        float d0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma16816(d0, a[mt][0], x.x, x.y);
-                        mma16816(d1, a[mt][1], x.z, x.w);
+                        float d0[4], d1[4];
+                        float2 c0 = make_float2(0.0f, 0.0f), c1 = c0;
+                        if constexpr (FMT == kFmtW6G16) {
+                            c0 = lds64f_a(xs + nb * G::XB + G::KS * 16 + (4 * half + 2 * sp) * 32 + t * 8);
+                            c1 = lds64f_a(xs + nb * G::XB + G::KS * 16 + (4 * half + 2 * sp + 1) * 32 + t * 8);
+                        }
+                        mma16816(d0, a[mt][0], x.x, x.y, c0.x, c0.y, c0.x, c0.y);
+                        mma16816(d1, a[mt][1], x.z, x.w, c1.x, c1.y, c1.x, c1.y);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t w = sc.w[2 * mt + (i >> 1)][sp];
@@ -488,8 +510,9 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t sm
                             acc[mt][nb][i] = fmaf(half_at(w, 1), d1[i], acc[mt][nb][i]);
                         }
                     } else {
-                        mma16816(gsum[mt][nb], a[mt][0], x.x, x.y);
-                        mma16816(gsum[mt][nb], a[mt][1], x.z, x.w);
+                        float (&q)[4] = gsum[mt][nb];
+                        mma16816(q, a[mt][0], x.x, x.y, q[0], q[1], q[2], q[3]);
+                        mma16816(q, a[mt][1], x.z, x.w, q[0], q[1], q[2], q[3]);
                     }
                 }
             }
@@ -504,66 +527,51 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t sm
                         acc[mt][nb][i] = fmaf(half_at(sc.w[2 * mt + (i >> 1)][0], 0), gsum[mt][nb][i], acc[mt][nb][i]);
         }
     } else {
-        // superblocks: lane = weight row decodes the row's four (S, M) of this half into shared memory
-        {
-            const uint4 hd = lds128_a(cs + (uint32_t)(wr + lane) * G::RB);
-            const float d = half_at(hd.x, 0), dm = half_at(hd.x, 1);
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // fields 4 half + j of the scales (bits 6 ..) and of the mins (bits 48 + 6 ..)
-                const uint32_t f0 = half ? __funnelshift_r(hd.y, hd.z, 24) : hd.y;         // scale fields from bit 0
-                const uint32_t f1 = half ? __funnelshift_r(hd.w, 0u, 8) : __funnelshift_r(hd.z, hd.w, 16);
-                v[2 * j] = __fmul_rn(d, (float)((f0 >> (6 * j)) & 63u));
-                v[2 * j + 1] = __fmul_rn(dm, (float)((f1 >> (6 * j)) & 63u));
-            }
-            __syncwarp();                                // the previous stage's values have been read
-            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" :: "r"(smin + lane * 32), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
-            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" :: "r"(smin + lane * 32 + 16), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
-            __syncwarp();
-        }
+        // nibble formats, 32 weights at a time (a superblock group, half of a group of 64)
 #pragma unroll
         for (int gp = 0; gp < 4; ++gp) {
             const int gr = 4 * half + gp;
-            uint32_t a[2][2][4];
+            uint32_t a[2][2][4];                         // [m16][step][register]
             float2 sm2[4];
 #pragma unroll
-            for (int mr = 0; mr < 4; ++mr) {
-                const uint32_t rb = cs + (uint32_t)(wr + 8 * mr + g) * G::RB;
-                const uint32_t w = lds32_a(rb + 16 + 16 * gr + 4 * t);
-                uint32_t o[4];
-                if constexpr (FMT == kFmtW4SB32) {
-                    unpack_nibbles<0x43004300u>(w, o);
-                } else if constexpr (FMT == kFmtW5SB32) {
-                    uint32_t h;
-                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(h) : "r"(rb + 144 + 4 * gr + t));
-                    unpack_wide<1, 0x43004300u>(w, h | (h << 12), o);
+            for (int mr = 0; mr < 4; ++mr) {             // row 8 mr + g of the warp's 32
+                uint32_t o[4], h = 0u;
+                if constexpr (FMT == kFmtW4G64) {
+                    unpack_nibbles<4>(cw[gr][mr], 0u, o);
+                    sm2[mr].x = half_at(sc.w[mr][0], gp >> 1);
                 } else {
-                    const uint32_t h = lds16_a(rb + 144 + 8 * gr + 2 * t);
-                    unpack_wide<2, 0x43004300u>(w, h | (h << 8), o);
+                    const uint32_t rb = cs + (uint32_t)(wr + 8 * mr + g) * G::RB;
+                    if constexpr (FMT == kFmtW5SB32) {
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(h) : "r"(rb + 144 + 4 * gr + t));
+                        h |= h << 12;
+                    } else if constexpr (FMT == kFmtW6SB32) {
+                        h = lds16_a(rb + 144 + 8 * gr + 2 * t);
+                        h |= h << 8;
+                    }
+                    unpack_nibbles<G::B>(G::EARLY ? cw[gr][mr] : lds32_a(rb + 16 + 16 * gr + 4 * t), h, o);
+                    sm2[mr] = lds64f_a(smin + (8 * mr + g) * 64 + (((gr >> 1) ^ ((g >> 1) & 3)) << 4) + 8 * (gr & 1));
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    a[mr >> 1][h][mr & 1] = o[2 * h];
-                    a[mr >> 1][h][2 + (mr & 1)] = o[2 * h + 1];
+                for (int s = 0; s < 2; ++s) {
+                    a[mr >> 1][s][mr & 1] = o[2 * s];
+                    a[mr >> 1][s][2 + (mr & 1)] = o[2 * s + 1];
                 }
-                sm2[mr] = lds64f_a(smin + (8 * mr + g) * 32 + 8 * gp);
             }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 if (NB > 1 && nb >= tiles) break;
                 const uint4 x = lds128_a(xl + nb * G::XB + gr * 512);
-                const float2 xsum = lds64f_a(xs + nb * G::XB + G::KS * 16 + gr * 32 + t * 8);
+                const float2 xc = lds64f_a(xs + nb * G::XB + G::KS * 16 + gr * 32 + t * 8);   // -OFF sum x of two rows
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma16816(d, a[mt][0], x.x, x.y);
-                    mma16816(d, a[mt][1], x.z, x.w);
+                    float d[4];
+                    mma16816(d, a[mt][0], x.x, x.y, xc.x, xc.y, xc.x, xc.y);
+                    mma16816(d, a[mt][1], x.z, x.w, d[0], d[1], d[2], d[3]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 m = sm2[2 * mt + (i >> 1)];
                         acc[mt][nb][i] = fmaf(m.x, d[i], acc[mt][nb][i]);
-                        acc[mt][nb][i] = fmaf(-m.y, i & 1 ? xsum.y : xsum.x, acc[mt][nb][i]);
+                        if (is_sb(FMT)) acc[mt][nb][i] = fmaf(m.y, i & 1 ? xc.y : xc.x, acc[mt][nb][i]);
                     }
                 }
             }
@@ -598,32 +606,30 @@ __device__ __forceinline__ Work get_work(const Plan& pl, const Groups& g, long l
     return w;
 }
 
-// The adapter's term for weight rows n .. n + 7 of row m.
-__device__ __forceinline__ void add_adapter(const RowsParams& p, int m, int n, float (&v)[8]) {
-    const int a = p.adapter[m];
-    if (a < 0 || a >= p.n_adapters) return;
-    const int rank = p.ranks ? min(p.ranks[a], p.r) : p.r;
+// The adapter's term for weight rows n .. n + 7 of row m: adapter a, of which
+// `rank` counts.
+__device__ __forceinline__ void add_adapter(const RowsParams& p, int m, int a, int rank, int n, float (&v)[8]) {
     const float* t = p.t + (size_t)m * p.r;
     const __nv_bfloat16* B = p.B + ((size_t)a * p.pl.N + n) * p.r;
-    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    const int rows = min(8, p.pl.N - n);
     for (int j = 0; j < rank; j += 8) {
-        float tv[8];
+        uint4 b[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) tv[i] = j + i < rank ? t[j + i] : 0.0f;
+        for (int q = 0; q < 8; ++q) b[q] = __ldg(reinterpret_cast<const uint4*>(B + (size_t)min(q, rows - 1) * p.r + j));
+        const float4 t0 = *reinterpret_cast<const float4*>(t + j), t1 = *reinterpret_cast<const float4*>(t + j + 4);
+        const float tv[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            if (n + q >= p.pl.N) break;
-            const uint4 b = __ldg(reinterpret_cast<const uint4*>(B + (size_t)q * p.r + j));
-            const uint32_t bb[4] = {b.x, b.y, b.z, b.w};
+            const uint32_t bb[4] = {b[q].x, b[q].y, b[q].z, b[q].w};
+            float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float w = i & 1 ? bf16hi_f32(bb[i >> 1]) : bf16lo_f32(bb[i >> 1]);
-                if (j + i < rank) s[q] = fmaf(tv[i], w, s[q]);           // past the rank the slot may hold anything
+                if (j + i < rank) s = fmaf(tv[i], w, s);                 // past the rank the slot may hold anything
             }
+            v[q] += s;
         }
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] += s[q];
 }
 
 // v[0..7] to columns n .. n + 7 of y's row `out`.
@@ -654,25 +660,31 @@ __device__ __forceinline__ void store8(const RowsParams& p, int out, int n, cons
 template <int FMT, int NB>
 __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kernel(const __grid_constant__ RowsParams p) {
     using G = Geo<FMT>;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);         // the swizzled tiles need 1024-byte alignment
+    extern __shared__ __align__(1024) uint8_t smem[];                    // the swizzled code tiles need this alignment
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ring = p.ring;
-    uint8_t* at = smem + (size_t)ring * p.stage_bytes;
-    float* scratch = reinterpret_cast<float*>(at + warp * kWarpScratch); // of a math warp
-    at += kMathWarps * kWarpScratch;
-    uint64_t* full = reinterpret_cast<uint64_t*>(at);
-    uint64_t* empty = full + kMaxRing;
-    at += 2 * kMaxRing * 8;
+    uint8_t* at = smem + (size_t)ring * G::CB;
+    const uint32_t xbase = smem_u32(at);
+    at += kXRing * p.xslot;
+    float* scratch = reinterpret_cast<float*>(at + warp * G::SCRATCH);   // of a math warp
+    at += kMathWarps * G::SCRATCH;
+    uint64_t* cfull = reinterpret_cast<uint64_t*>(at);
+    uint64_t* cempty = cfull + kMaxRing;
+    uint64_t* xfull = cempty + kMaxRing;
+    uint64_t* xempty = xfull + kXRing;
+    at += 2 * (kMaxRing + kXRing) * 8;
     Desc* desc = reinterpret_cast<Desc*>(at);
     at += kDescs * sizeof(Desc);
     const Groups g = groups_at(at, p.pl.E);
 
     if (tid == 0) {
         for (int s = 0; s < ring; ++s) {
-            mbar_init(&full[s], is_sb(FMT) ? 1 : 33);                    // the copy thread, and the scale copies of 32 lanes
-            mbar_init(&empty[s], kMathWarps);
+            mbar_init(&cfull[s], 1);
+            mbar_init(&cempty[s], kMathWarps);
+        }
+        for (int s = 0; s < kXRing; ++s) {
+            mbar_init(&xfull[s], is_sb(FMT) ? 1 : 33);                   // the copy thread, and the scale copies of 32 lanes
+            mbar_init(&xempty[s], kMathWarps);
         }
         fence_mbar_init();
     }
@@ -688,28 +700,84 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
         return;
     }
     const long long s0 = blockIdx.x * S / Gc, s1 = ((long long)blockIdx.x + 1) * S / Gc;
+    const int n = (int)(s1 - s0);                                        // stages of this CTA
     const uint32_t base = smem_u32(smem);
-    constexpr uint32_t kXOff = kRowsPerTile * G::RB, kSOff = kXOff + NB * G::XB;   // parts of a stage: codes, x, scales
+    constexpr uint32_t kSOff = NB * G::XB;                               // scales behind the activations of a slot
 
     if (warp == kMathWarps) {
         // ------------------------------------------------------------ copies
-        // The weights of the first `ring` stages are asked for before the
-        // prepared activations are waited for.
+        // Two streams: code tiles, and activations with scales. The codes of
+        // the first `ring` stages are asked for before the prepared
+        // activations are waited for.
         const bool copies = !(p.test_flags & kTestNoCopies);
-        auto weights = [&](const Work& w, int k, int slot) {
-            const uint32_t st = base + slot * p.stage_bytes;
-            const int row0 = w.e * p.pl.N + w.n0;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&full[slot], (uint32_t)(kRowsPerTile * G::RB + ((w.rows + 7) / 8) * G::XB));
-                tma_codes(st, &p.cmap, k * G::RB, row0, &full[slot]);
+        if (!copies) return;
+        struct Cursor {                                                  // walks the CTA's stages
+            long long unit;
+            int i, k, u;
+            Work w;
+        };
+        auto begin = [&](Cursor& c) {
+            c.unit = s0 / T;
+            c.k = (int)(s0 - c.unit * T);
+            c.i = c.u = 0;
+            c.w = get_work(p.pl, g, c.unit);
+        };
+        auto next = [&](Cursor& c) {
+            if (++c.i < n && ++c.k == T) {
+                c.k = 0;
+                ++c.u;
+                c.w = get_work(p.pl, g, ++c.unit);
             }
+        };
+        auto codes = [&](const Cursor& c, int slot) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&cfull[slot], (uint32_t)(kRowsPerTile * G::RB));
+                tma_codes(base + slot * G::CB, &p.cmap, c.k * G::RB, c.w.e * p.pl.N + c.w.n0, &cfull[slot]);
+            }
+        };
+        Cursor cc, cx;
+        begin(cc);
+        cx = cc;
+        int cslot = 0, cwrap = 0, xslot = 0, xwrap = 0;
+        bool ok = true;
+        while (cc.i < min(n, ring)) {
+            codes(cc, cslot);
+            if (++cslot == ring) { cslot = 0; ++cwrap; }
+            next(cc);
+        }
+        grid_dep_wait();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        // In the order in which slots come free: a stage's activations when
+        // the stage kXRing before has been used, then the codes that follow
+        // the ones taken out for the next stage.
+        while (cx.i < n) {
+            if (xwrap && !__all_sync(~0u, mbar_wait_bounded(&xempty[xslot], (uint32_t)(xwrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns))) {
+                ok = false;
+                break;
+            }
+            const Work& w = cx.w;
+            const uint32_t xs = xbase + xslot * p.xslot;
+            const int tiles = (w.rows + 7) / 8, k = cx.k;
+            if (lane == 0) {
+                if (k == 0 || cx.i == 0) {
+                    const long long us = cx.unit * T;
+                    Desc d = {w.n0, w.row0, w.rows, k, min(T, k + n - cx.i), (int)blockIdx.x, (int)blockIdx.x, w.e};
+                    if (d.k0 > 0) d.first = (int)(((us + 1) * Gc - 1) / S);
+                    if (d.k1 < T) d.last = (int)(((us + T) * Gc - 1) / S);
+                    desc[cx.u % kDescs] = d;
+                }
+                mbar_arrive_expect_tx(&xfull[xslot], (uint32_t)(tiles * G::XB));
+            }
+            __syncwarp();
+            if (lane < tiles)
+                bulk_x(xs + lane * G::XB, p.xf + ((size_t)(w.tile0 + lane) * T + k) * G::XB, G::XB, &xfull[xslot]);
             if constexpr (!is_sb(FMT)) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = 32 * i + lane;
-                    const unsigned long long row = min((unsigned long long)(row0 + r), p.total_rows - 1);
+                    const unsigned long long row = min((unsigned long long)w.e * p.pl.N + w.n0 + r, p.total_rows - 1);
                     const uint8_t* src = p.scales + row * p.srb;
-                    const uint32_t dst = st + kSOff + r * G::SB;
+                    const uint32_t dst = xs + kSOff + r * G::SB;
                     const uint32_t b0 = k * G::SB;
                     if (G::SB >= 8 && (p.srb & 7u) == 0u) {
 #pragma unroll
@@ -725,57 +793,29 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
                         }
                     }
                 }
-                if ((p.srb & 3u) == 0u) cp_async_arrive(&full[slot]);
-                else mbar_arrive(&full[slot]);
+                if ((p.srb & 3u) == 0u) cp_async_arrive(&xfull[xslot]);
+                else mbar_arrive(&xfull[xslot]);
             }
-        };
-        auto describe = [&](const Work& w, long long unit, int k0, int k1, int u) {
-            if (lane == 0) {
-                const long long us = unit * T;
-                Desc d = {w.n0, w.row0, w.rows, k0, k1, (int)blockIdx.x, (int)blockIdx.x, w.e};
-                if (k0 > 0) d.first = (int)(((us + 1) * Gc - 1) / S);
-                if (k1 < T) d.last = (int)(((us + T) * Gc - 1) / S);
-                desc[u % kDescs] = d;
-            }
-        };
-        const int n = (int)(s1 - s0);
-        const long long unit0 = s0 / T;
-        const int kfirst = (int)(s0 - unit0 * T), head = min(n, ring);
-        if (copies) {
-            int i = 0, k = kfirst, u = 0;
-            for (long long unit = unit0; i < head; ++unit, k = 0, ++u) {
-                const Work w = get_work(p.pl, g, unit);
-                describe(w, unit, k, min(T, k + n - i), u);
-                for (; k < T && i < head; ++k, ++i) weights(w, k, i);
-            }
-        }
-        grid_dep_wait();
-        asm volatile("fence.proxy.async.global;" ::: "memory");
-        int slot = 0, wrap = 0, issued = 0, u = 0, k = kfirst;
-        bool ok = copies;
-        for (long long unit = unit0; ok && issued < n; ++unit, k = 0, ++u) {
-            const Work w = get_work(p.pl, g, unit);
-            const int k1 = min(T, k + n - issued), tiles = (w.rows + 7) / 8;
-            for (bool begin = true; k < k1; ++k, begin = false) {
-                if (wrap && !__all_sync(~0u, mbar_wait_bounded(&empty[slot], (uint32_t)(wrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns))) {
+            next(cx);
+            if (++xslot == kXRing) { xslot = 0; ++xwrap; }
+            if (cc.i < n && cx.i >= kXRing) {
+                if (!__all_sync(~0u, mbar_wait_bounded(&cempty[cslot], (uint32_t)(cwrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns))) {
                     ok = false;
                     break;
                 }
-                if (begin && wrap) describe(w, unit, k, k1, u);
-                __syncwarp();
-                if (wrap) weights(w, k, slot);
-                if (lane < tiles)
-                    bulk_x(base + slot * p.stage_bytes + kXOff + lane * G::XB, p.xf + ((size_t)(w.tile0 + lane) * T + k) * G::XB, G::XB, &full[slot]);
-                ++issued;
-                if (++slot == ring) { slot = 0; ++wrap; }
+                codes(cc, cslot);
+                if (++cslot == ring) { cslot = 0; ++cwrap; }
+                next(cc);
             }
         }
+        (void)ok;
         // copies in flight (a math warp gave up) land before the CTA leaves
-        if (lane == 0)
-            for (int q = 0; q < ring && q < issued; ++q) {
-                const int uses = issued / ring + (q < issued % ring ? 1 : 0);
-                mbar_wait_bounded(&full[q], (uint32_t)(uses - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
-            }
+        if (lane == 0) {
+            for (int q = 0; q < ring && q < cc.i; ++q)
+                mbar_wait_bounded(&cfull[q], (uint32_t)(cc.i / ring + (q < cc.i % ring ? 1 : 0) - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
+            for (int q = 0; q < kXRing && q < cx.i; ++q)
+                mbar_wait_bounded(&xfull[q], (uint32_t)(cx.i / kXRing + (q < cx.i % kXRing ? 1 : 0) - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
+        }
         return;
     }
 
@@ -783,12 +823,29 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
     // A warp keeps to its own 32 weight rows from the codes to y: no barrier
     // among the warps. One whose wait runs out leaves.
     const int wr = 32 * warp;
-    int slot = 0, wrap = 0, left = (int)(s1 - s0);
+    const uint32_t sm = smem_u32(scratch);
+    int cslot = 0, cwrap = 0, xslot = 0, xwrap = 0, left = n;
+    auto wait = [&](uint64_t* bar, int wrap) {
+        return __all_sync(~0u, mbar_wait_bounded(bar, (uint32_t)wrap & 1u, kStatusTmaWait, 0u, p.wait_ns));
+    };
     grid_dep_wait();                                      // counters and adapter terms come from prep_kernel
     for (int u = 0; left > 0; ++u) {
-        if (!__all_sync(~0u, mbar_wait_bounded(&full[slot], (uint32_t)wrap & 1u, kStatusTmaWait, 0u, p.wait_ns))) return;
+        if (!wait(&xfull[xslot], xwrap)) return;
         const Desc d = desc[u % kDescs];
         const int tiles = (d.rows + 7) / 8;
+        // this lane's rows of y, and their adapters, for the end
+        int out[NB], ad[NB], rk[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int i = 8 * nb + (lane >> 2), m = d.row0 + i;
+            out[nb] = i >= d.rows ? -1 : p.out_rows ? p.out_rows[m] : m;
+            ad[nb] = -1;
+            rk[nb] = 0;
+            if (p.adapter && i < d.rows) {
+                ad[nb] = p.adapter[m];
+                if (ad[nb] >= 0 && ad[nb] < p.n_adapters) rk[nb] = p.ranks ? min(p.ranks[ad[nb]], p.r) : p.r;
+            }
+        }
         float acc[2][NB][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -797,17 +854,29 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[mt][nb][i] = 0.0f;
         for (int k = d.k0; k < d.k1; ++k) {
-            if (k > d.k0 && !__all_sync(~0u, mbar_wait_bounded(&full[slot], (uint32_t)wrap & 1u, kStatusTmaWait, 0u, p.wait_ns))) return;
-            const uint32_t st = base + slot * p.stage_bytes;
+            if (!wait(&cfull[cslot], cwrap)) return;
+            const uint32_t cs = base + cslot * G::CB, xs = xbase + xslot * p.xslot;
+            uint32_t cw[8][4];
+            if constexpr (is_sb(FMT)) decode_superblock<FMT>(cs, sm, wr, lane);
+            if constexpr (G::EARLY) {
+                take_codes<FMT>(cs, wr, lane, cw);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cempty[cslot]);
+            }
+            if (k > d.k0 && !wait(&xfull[xslot], xwrap)) return;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 Scales<FMT> sc;
-                read_scales<FMT>(st + kSOff, wr, half, lane >> 2, sc);
-                stage_math<FMT, NB>(st, st + kXOff, smem_u32(scratch), wr, half, lane, tiles, sc, acc);
+                read_scales<FMT>(xs + kSOff, wr, half, lane >> 2, sc);
+                stage_math<FMT, NB>(cs, cw, xs, sm, wr, half, lane, tiles, sc, acc);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[slot]);
-            if (++slot == ring) { slot = 0; ++wrap; }
+            if (lane == 0) {
+                if (!G::EARLY) mbar_arrive(&cempty[cslot]);
+                mbar_arrive(&xempty[xslot]);
+            }
+            if (++cslot == ring) { cslot = 0; ++cwrap; }
+            if (++xslot == kXRing) { xslot = 0; ++xwrap; }
         }
         left -= d.k1 - d.k0;
 
@@ -819,8 +888,11 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-                    __stcg(mypart + (mt * NB + nb) * 32, make_float4(acc[mt][nb][0], acc[mt][nb][1], acc[mt][nb][2], acc[mt][nb][3]));
+                for (int nb = 0; nb < NB; ++nb) {
+                    if (nb < tiles)
+                        __stcg(mypart + (mt * NB + nb) * 32, make_float4(acc[mt][nb][0], acc[mt][nb][1], acc[mt][nb][2], acc[mt][nb][3]));
+                    acc[mt][nb][0] = acc[mt][nb][1] = acc[mt][nb][2] = acc[mt][nb][3] = 0.0f;
+                }
             __threadfence();
             __syncwarp();
             unsigned old = 0;
@@ -828,20 +900,35 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
             old = __shfl_sync(~0u, old, 0);
             if (old != (unsigned)(d.last - d.first)) continue;           // not the last to arrive
             __threadfence();
+            constexpr int kAhead = NB == 1 ? 4 : NB == 2 ? 2 : 1;        // parts read together
+            for (int c0 = d.first; c0 <= d.last; c0 += kAhead) {
+                float4 v[kAhead][2][NB];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+                for (int q = 0; q < kAhead; ++q)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int c = d.first; c <= d.last; ++c) {
-                        const float4 w = __ldcg(part + (size_t)(2 * c + (c == d.first)) * kPart + (mt * NB + nb) * 32);
-                        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
-                    }
-                    acc[mt][nb][0] = v.x; acc[mt][nb][1] = v.y; acc[mt][nb][2] = v.z; acc[mt][nb][3] = v.w;
-                }
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            const int c = c0 + q;
+                            v[q][mt][nb] = c <= d.last && nb < tiles
+                                ? __ldcg(part + (size_t)(2 * c + (c == d.first)) * kPart + (mt * NB + nb) * 32)
+                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        }
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            acc[mt][nb][0] += v[q][mt][nb].x;
+                            acc[mt][nb][1] += v[q][mt][nb].y;
+                            acc[mt][nb][2] += v[q][mt][nb].z;
+                            acc[mt][nb][3] += v[q][mt][nb].w;
+                        }
+            }
         }
         // through shared memory to eight consecutive weight rows per lane
-        const int n = d.n0 + wr + 8 * (lane & 3);
+        const int nn = d.n0 + wr + 8 * (lane & 3);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             if (nb >= tiles) break;
@@ -849,17 +936,17 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    scratch[(2 * (lane & 3) + (i & 1)) * 36 + 16 * mt + (lane >> 2) + 8 * (i >> 1)] = acc[mt][nb][i];
+                for (int i = 0; i < 4; ++i) {
+                    // [activation row r][weight row], 16-byte chunks swizzled by r: no bank conflict either way
+                    const int r = 2 * (lane & 3) + (i & 1), c = 16 * mt + (lane >> 2) + 8 * (i >> 1);
+                    scratch[r * 32 + (((c >> 2) ^ r) << 2) + (c & 3)] = acc[mt][nb][i];
+                }
             __syncwarp();
-            const int i = 8 * nb + (lane >> 2), m = d.row0 + i;
-            if (i >= d.rows || n >= p.pl.N) continue;
-            const int out = p.out_rows ? p.out_rows[m] : m;
-            if (out < 0 || out >= p.Ty) continue;
-            const float* f = scratch + (lane >> 2) * 36 + 8 * (lane & 3);
-            const float4 f0 = *reinterpret_cast<const float4*>(f), f1 = *reinterpret_cast<const float4*>(f + 4);
+            if (out[nb] < 0 || out[nb] >= p.Ty || nn >= p.pl.N) continue;
+            const float4* f = reinterpret_cast<const float4*>(scratch) + (lane >> 2) * 8;
+            const float4 f0 = f[(2 * (lane & 3)) ^ (lane >> 2)], f1 = f[(2 * (lane & 3) + 1) ^ (lane >> 2)];
             float v[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-            if (p.adapter) add_adapter(p, m, n, v);
+            if (rk[nb] > 0) add_adapter(p, d.row0 + 8 * nb + (lane >> 2), ad[nb], rk[nb], nn, v);
             if (p.act) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -867,7 +954,7 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
                     v[q] *= v[q];
                 }
             }
-            store8(p, out, n, v);
+            store8(p, out[nb], nn, v);
         }
         __syncwarp();                                     // scratch is read before it is written again
     }
@@ -920,12 +1007,13 @@ template <int FMT, int NB>
 cudaError_t launch_product(const RowsParams& p0, cudaStream_t st) {
     using G = Geo<FMT>;
     RowsParams p = p0;
-    p.stage_bytes = (kRowsPerTile * (G::RB + G::SB) + NB * G::XB + 1023) & ~1023;
-    const size_t fixed = 1024 + kMathWarps * kWarpScratch + 2 * kMaxRing * 8 + kDescs * sizeof(Desc) + groups_bytes(p.pl.E);
+    p.xslot = (NB * G::XB + kRowsPerTile * G::SB + 127) & ~127;
+    const size_t fixed = kXRing * (size_t)p.xslot + kMathWarps * G::SCRATCH + 2 * (kMaxRing + kXRing) * 8 + kDescs * sizeof(Desc) +
+                         groups_bytes(p.pl.E);
     constexpr size_t smem_max = kSmemPerSm / 2 - 1024;
     int per_sm = ctas_per_sm(FMT, NB);
-    while (per_sm > 2 && kSmemPerSm / per_sm - 1024 < fixed + 2 * (size_t)p.stage_bytes) --per_sm;   // two stages at least
-    p.ring = (int)((kSmemPerSm / per_sm - 1024 - fixed) / p.stage_bytes);
+    while (per_sm > 2 && kSmemPerSm / per_sm - 1024 < fixed + 2 * (size_t)G::CB) --per_sm;   // two code slots at least
+    p.ring = (int)((kSmemPerSm / per_sm - 1024 - fixed) / G::CB);
     if (p.ring > kMaxRing) p.ring = kMaxRing;
     if (p.ring < 2) return cudaErrorInvalidValue;
     auto kern = rows_kernel<FMT, NB>;
@@ -944,7 +1032,7 @@ cudaError_t launch_product(const RowsParams& p0, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kRowsThreads);
-    cfg.dynamicSmemBytes = fixed + (size_t)p.ring * p.stage_bytes;
+    cfg.dynamicSmemBytes = fixed + (size_t)p.ring * G::CB;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -972,7 +1060,7 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
     q.count = reinterpret_cast<unsigned*>(ws + l.count);
     q.n_count = kMaxCtas * kMathWarps;
     q.tiles_max = l.tiles;
-    q.kblocks = (l.T * G::KS / 8 + 255) / 256;
+    q.kblocks = (l.T * G::KS / 8 + kPrepChunks - 1) / kPrepChunks;
     q.adapter = a.adapter;
     q.ranks = a.ranks;
     q.A = static_cast<const __nv_bfloat16*>(a.A);
@@ -980,7 +1068,7 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
     q.t = reinterpret_cast<float*>(ws + l.t);
     q.n_adapters = a.n_adapters;
     q.r = a.r;
-    const long long blocks = (long long)q.tiles_max * q.kblocks + (a.adapter ? (long long)a.R * ((a.r + 7) / 8) : 0);
+    const long long blocks = (long long)q.tiles_max * q.kblocks + (a.adapter ? (long long)a.R * (a.r / (kPrepThreads / 32)) : 0);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
