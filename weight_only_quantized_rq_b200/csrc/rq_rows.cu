@@ -64,13 +64,14 @@ template <int FMT>
 struct Geo {
     static constexpr int KS = is_w8(FMT) || FMT == kFmtW6G16 ? 128 : 256;         // K per stage
     static constexpr int RB = FMT == kFmtW4G64 ? 128 : is_w8(FMT) ? 128 : FMT == kFmtW6G16 ? 96 : sb_record(FMT);
-    static constexpr int XB = KS * 16 + (is_w8(FMT) ? 0 : 256);                   // bytes of one 8-row tile's stage
+    // Activations of one 8-row tile's stage: the fragments, then for sub-byte codes the rows' sums over
+    // the groups of GS weights, 64 bytes per group (row pairs 2t, 2t + 1 for t = 0..3, each pair twice: the
+    // four values that start a product).
+    static constexpr int GS = FMT == kFmtW4G64 ? 64 : FMT == kFmtW6G16 ? 16 : 32;
+    static constexpr int XB = KS * 16 + (is_w8(FMT) ? 0 : KS / GS * 64);
     static constexpr int SB = is_sb(FMT) ? 0 : KS / sym_group(FMT) * 2;           // scale bytes of a weight row's stage
     static constexpr bool SWZ = RB == 128;
     static constexpr int CB = (kRowsPerTile * RB + 1023) & ~1023;                 // a code slot
-    // Codes that fit a thread's registers are taken out of their slot at once, so that the slot refills
-    // while they are used (the wider codes' high-bit planes do not fit).
-    static constexpr bool EARLY = RB == 128 || FMT == kFmtW4SB32;
     static constexpr int SCRATCH = is_sb(FMT) ? 2048 : 1024;                      // shared bytes of a math warp
     // Sub-byte codes u unpack as 2^B + u (B code bits, the top of bf16's seven fraction bits); the products
     // start from -OFF sum x, so that they give sum q x (symmetric) or sum u x (superblocks).
@@ -231,15 +232,21 @@ __global__ void __launch_bounds__(kPrepThreads, 16) prep_kernel(const PrepParams
         const int c_end = p.pl.T * G::KS / 8;                                // 8-value chunks of a row, padded to whole stages
         uint8_t* out = p.xf + (size_t)tile * p.pl.T * G::XB;
         uint4 vv[kPrepUnroll];
+        float sum64 = 0.0f;
+        // -OFF times this row's sum over group gr of a stage, to its place behind the fragments
+        auto put_sum = [&](uint8_t* o, int gr, float sum) {
+            float* d = reinterpret_cast<float*>(o + G::KS * 16 + gr * 64 + (lane >> 3) * 16) + ((lane >> 2) & 1);
+            d[0] = d[2] = -G::OFF * sum;
+        };
 #pragma unroll
         for (int q = 0; q < kPrepUnroll; ++q) {
-            const int c = kb * kPrepChunks + q * (kPrepThreads / 8) + 4 * warp + (lane & 3);
+            const int c = kb * kPrepChunks + 4 * (kPrepUnroll * warp + q) + (lane & 3);
             vv[q] = make_uint4(0u, 0u, 0u, 0u);
             if (src >= 0 && 8 * c < p.pl.K) vv[q] = *reinterpret_cast<const uint4*>(p.x + (size_t)src * p.pl.K + 8 * c);
         }
 #pragma unroll
         for (int q = 0; q < kPrepUnroll; ++q) {
-            const int c = kb * kPrepChunks + q * (kPrepThreads / 8) + 4 * warp + (lane & 3);
+            const int c = kb * kPrepChunks + 4 * (kPrepUnroll * warp + q) + (lane & 3);
             if (c >= c_end) break;                       // the same for the whole warp
             const uint4 v = vv[q];
             const int st = 8 * c / G::KS, cs = c - st * (G::KS / 8);         // stage, chunk in the stage
@@ -255,7 +262,13 @@ __global__ void __launch_bounds__(kPrepThreads, 16) prep_kernel(const PrepParams
                 float s = bf16_sum8(v);                  // the row's sum over 32 weights
                 s += __shfl_xor_sync(~0u, s, 1);
                 s += __shfl_xor_sync(~0u, s, 2);
-                if ((lane & 3) == 0) *reinterpret_cast<float*>(o + G::KS * 16 + ((cs >> 2) * 8 + (lane >> 2)) * 4) = -G::OFF * s;
+                if (G::GS == 32) {
+                    if ((lane & 3) == 0) put_sum(o, cs >> 2, s);
+                } else if (q & 1) {                      // a thread's chunks q - 1 and q lie in one group of 64
+                    if ((lane & 3) == 0) put_sum(o, cs >> 3, sum64 + s);
+                } else {
+                    sum64 = s;
+                }
             } else {
                 // four-weight words unpack as the pairs (0, 2), (1, 3); lane t of a quad takes weights
                 // 4t .. 4t + 3 of each 16-weight step, two steps per 16 bytes
@@ -270,7 +283,7 @@ __global__ void __launch_bounds__(kPrepThreads, 16) prep_kernel(const PrepParams
                 if constexpr (!is_w8(FMT)) {
                     float s = bf16_sum8(v);              // over 16 weights
                     s += __shfl_xor_sync(~0u, s, 1);
-                    if ((lane & 1) == 0) *reinterpret_cast<float*>(o + G::KS * 16 + ((cs >> 1) * 8 + g8) * 4) = -G::OFF * s;
+                    if ((lane & 1) == 0) put_sum(o, cs >> 1, s);
                 }
             }
         }
@@ -379,50 +392,8 @@ __device__ __forceinline__ void unpack_bytes(uint32_t w, uint32_t (&o)[2]) {
 }
 
 // --------------------------------------------------------------- one stage
-// The scales of a thread's four weight rows for half a stage: fp16 bits, two
-// per 32-bit word, from the stage's scale block ([128 rows][SB bytes]).
-template <int FMT>
-struct Scales {
-    static constexpr int W = is_sb(FMT) ? 1 : sym_group(FMT) == 16 ? 2 : 1;
-    uint32_t w[4][W];
-};
-
-template <int FMT>
-__device__ __forceinline__ void read_scales(uint32_t ss, int wr, int half, int g, Scales<FMT>& s) {
-    constexpr int SB = Geo<FMT>::SB;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t a = ss + (uint32_t)(wr + 8 * i + g) * SB + half * (SB / 2);
-        if constexpr (SB == 16) {
-            const float2 v = lds64f_a(a);
-            s.w[i][0] = __float_as_uint(v.x);
-            s.w[i][1] = __float_as_uint(v.y);
-        } else if constexpr (SB == 8) {
-            s.w[i][0] = lds32_a(a);
-        } else if constexpr (SB == 4) {
-            s.w[i][0] = lds16_a(a);
-        }
-    }
-}
-
 __device__ __forceinline__ float half_at(uint32_t w, int h) {
     return __half2float(__ushort_as_half((uint16_t)(h ? w >> 16 : w & 0xffffu)));
-}
-
-// The 32-bit code words of a thread's four weight rows (8 mr + lane / 4 of the
-// warp's 32) in a stage: word lane % 4 of each of the stage's eight 16-byte
-// chunks.
-template <int FMT>
-__device__ __forceinline__ void take_codes(uint32_t cs, int wr, int lane, uint32_t (&cw)[8][4]) {
-    using G = Geo<FMT>;
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-#pragma unroll
-        for (int mr = 0; mr < 4; ++mr) {
-            const uint32_t r = wr + 8 * mr + g;
-            cw[c][mr] = lds32_a(G::SWZ ? cs + r * 128 + ((c ^ g) << 4) + 4 * t : cs + r * G::RB + 16 + 16 * c + 4 * t);
-        }
 }
 
 // A superblock stage's scales, each lane those of weight row wr + lane: S_j and
@@ -445,112 +416,140 @@ __device__ __forceinline__ void decode_superblock(uint32_t cs, uint32_t smin, in
     __syncwarp();
 }
 
-// One warp's share of a stage: weight rows wr .. wr + 31 over half `half` of the
-// stage's K, all live 8-row tiles. acc[m16][tile]: D fragment (weight rows
-// 16 m16 + lane / 4, + 8; activation rows 2 (lane % 4), + 1).
+__device__ __forceinline__ float lds_half(uint32_t a) { return __half2float(__ushort_as_half((uint16_t)lds16_a(a))); }
+
+// One warp's share of a stage: weight rows wr .. wr + 31, all live 8-row
+// tiles. acc[m16][tile]: D fragment (weight rows 16 m16 + lane / 4, + 8;
+// activation rows 2 (lane % 4), + 1). cs, xs, ss: code, activation and scale
+// blocks; smin: the warp's decoded superblock scales.
 template <int FMT, int NB>
-__device__ __forceinline__ void stage_math(uint32_t cs, const uint32_t (&cw)[8][4], uint32_t xs, uint32_t smin, int wr, int half,
-                                           int lane, int tiles, const Scales<FMT>& sc, float (&acc)[2][NB][4]) {
+__device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t ss, uint32_t smin, int wr, int lane, int tiles,
+                                           float (&acc)[2][NB][4]) {
     using G = Geo<FMT>;
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t xl = xs + lane * 16;
-    if constexpr (is_w8(FMT) || FMT == kFmtW6G16) {
-        constexpr bool G16 = sym_group(FMT) == 16;
-        float gsum[2][NB][4];
-        if (!G16) {
+    const uint32_t xl = xs + lane * 16, xg = xs + G::KS * 16 + t * 16;
+    const uint32_t rb = cs + (uint32_t)(wr + g) * G::RB;                 // first of the thread's weight rows, 8 apart
+    const uint32_t rs = ss + (uint32_t)(wr + g) * G::SB;
+    if constexpr (FMT == kFmtW4G64 || FMT == kFmtW8G64) {
+        // a group of 64: four steps into one sum
+        constexpr int NG = G::KS / 64;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+        for (int gr = 0; gr < NG; ++gr) {
+            uint32_t a[2][4][4];                         // [m16][step][register]
+            float s[4];
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
+            for (int mr = 0; mr < 4; ++mr) {
+                s[mr] = lds_half(rs + 8 * mr * G::SB + 2 * gr);
+                if constexpr (FMT == kFmtW4G64) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) gsum[mt][nb][i] = 0.0f;
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t o[4];
+                        unpack_nibbles<4>(lds32_a(rb + 8 * mr * G::RB + (((2 * gr + j) ^ g) << 4) + 4 * t), 0u, o);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            a[mr >> 1][2 * j + h][mr & 1] = o[2 * h];
+                            a[mr >> 1][2 * j + h][2 + (mr & 1)] = o[2 * h + 1];
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t o[2];
+                        unpack_bytes(lds32_a(rb + 8 * mr * G::RB + (((4 * gr + j) ^ g) << 4) + 4 * t), o);
+                        a[mr >> 1][j][mr & 1] = o[0];
+                        a[mr >> 1][j][2 + (mr & 1)] = o[1];
+                    }
+                }
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                if (NB > 1 && nb >= tiles) break;
+                const uint4 x0 = lds128_a(xl + nb * G::XB + (2 * gr) * 512), x1 = lds128_a(xl + nb * G::XB + (2 * gr + 1) * 512);
+                float4 c = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (FMT == kFmtW4G64) c = lds128f_a(xg + nb * G::XB + gr * 64);
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    float d[4];
+                    mma16816(d, a[mt][0], x0.x, x0.y, c.x, c.y, c.z, c.w);
+                    mma16816(d, a[mt][1], x0.z, x0.w, d[0], d[1], d[2], d[3]);
+                    mma16816(d, a[mt][2], x1.x, x1.y, d[0], d[1], d[2], d[3]);
+                    mma16816(d, a[mt][3], x1.z, x1.w, d[0], d[1], d[2], d[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[mt][nb][i] = fmaf(s[2 * mt + (i >> 1)], d[i], acc[mt][nb][i]);
+                }
+            }
         }
+    } else if constexpr (FMT == kFmtW8G16 || FMT == kFmtW6G16) {
+        // pairs of 16-weight steps, each a group of its own
 #pragma unroll
-        for (int sp = 0; sp < 2; ++sp) {                 // pairs of 16-weight steps
+        for (int sp = 0; sp < G::KS / 32; ++sp) {
             uint32_t a[2][2][4];
+            float s[2][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int mr = 0; mr < 4; ++mr) {
+                const uint32_t w = lds32_a(rs + 8 * mr * G::SB + 4 * sp);
 #pragma unroll
-                for (int mr = 0; mr < 4; ++mr) {
-                    const int st = 2 * sp + h;           // step in the half stage
+                for (int h = 0; h < 2; ++h) {
+                    const int st = 2 * sp + h;
+                    s[h][mr] = half_at(w, h);
                     uint32_t o[2];
                     if constexpr (FMT == kFmtW6G16) {
-                        const uint32_t b = cs + (uint32_t)(wr + 8 * mr + g) * G::RB + 48 * half;
-                        const uint32_t n = lds16_a(b + 8 * st + 2 * t);
+                        const uint32_t b = rb + 8 * mr * G::RB + 48 * (st >> 2);
+                        const uint32_t n = lds16_a(b + 8 * (st & 3) + 2 * t);
                         uint32_t pl;
-                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(pl) : "r"(b + 32 + 4 * st + t));
-                        const uint32_t w = n | (n << 8), hh = pl | (pl << 12);     // pairs (0, 2), (1, 3), as for the bytes
-                        o[0] = and_or(hh << 5, 0x00600060u, and_or(w << 1, 0x001E001Eu, 0x42804280u));
-                        o[1] = and_or(hh << 3, 0x00600060u, and_or(w >> 3, 0x001E001Eu, 0x42804280u));
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(pl) : "r"(b + 32 + 4 * (st & 3) + t));
+                        const uint32_t v = n | (n << 8), hh = pl | (pl << 12);     // pairs (0, 2), (1, 3), as for the bytes
+                        o[0] = and_or(hh << 5, 0x00600060u, and_or(v << 1, 0x001E001Eu, 0x42804280u));
+                        o[1] = and_or(hh << 3, 0x00600060u, and_or(v >> 3, 0x001E001Eu, 0x42804280u));
                     } else {
-                        unpack_bytes(cw[4 * half + st][mr], o);
+                        unpack_bytes(lds32_a(rb + 8 * mr * G::RB + ((st ^ g) << 4) + 4 * t), o);
                     }
                     a[mr >> 1][h][mr & 1] = o[0];
                     a[mr >> 1][h][2 + (mr & 1)] = o[1];
                 }
+            }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 if (NB > 1 && nb >= tiles) break;
-                const uint4 x = lds128_a(xl + nb * G::XB + (2 * half + sp) * 512);
+                const uint4 x = lds128_a(xl + nb * G::XB + sp * 512);
+                float4 c0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), c1 = c0;
+                if constexpr (FMT == kFmtW6G16) {
+                    c0 = lds128f_a(xg + nb * G::XB + 2 * sp * 64);
+                    c1 = lds128f_a(xg + nb * G::XB + (2 * sp + 1) * 64);
+                }
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
-                    if constexpr (G16) {
-                        float d0[4], d1[4];
-                        float2 c0 = make_float2(0.0f, 0.0f), c1 = c0;
-                        if constexpr (FMT == kFmtW6G16) {
-                            c0 = lds64f_a(xs + nb * G::XB + G::KS * 16 + (4 * half + 2 * sp) * 32 + t * 8);
-                            c1 = lds64f_a(xs + nb * G::XB + G::KS * 16 + (4 * half + 2 * sp + 1) * 32 + t * 8);
-                        }
-                        mma16816(d0, a[mt][0], x.x, x.y, c0.x, c0.y, c0.x, c0.y);
-                        mma16816(d1, a[mt][1], x.z, x.w, c1.x, c1.y, c1.x, c1.y);
+                    float d0[4], d1[4];
+                    mma16816(d0, a[mt][0], x.x, x.y, c0.x, c0.y, c0.z, c0.w);
+                    mma16816(d1, a[mt][1], x.z, x.w, c1.x, c1.y, c1.z, c1.w);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t w = sc.w[2 * mt + (i >> 1)][sp];
-                            acc[mt][nb][i] = fmaf(half_at(w, 0), d0[i], acc[mt][nb][i]);
-                            acc[mt][nb][i] = fmaf(half_at(w, 1), d1[i], acc[mt][nb][i]);
-                        }
-                    } else {
-                        float (&q)[4] = gsum[mt][nb];
-                        mma16816(q, a[mt][0], x.x, x.y, q[0], q[1], q[2], q[3]);
-                        mma16816(q, a[mt][1], x.z, x.w, q[0], q[1], q[2], q[3]);
+                    for (int i = 0; i < 4; ++i) {
+                        acc[mt][nb][i] = fmaf(s[0][2 * mt + (i >> 1)], d0[i], acc[mt][nb][i]);
+                        acc[mt][nb][i] = fmaf(s[1][2 * mt + (i >> 1)], d1[i], acc[mt][nb][i]);
                     }
                 }
             }
         }
-        if constexpr (!G16) {
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[mt][nb][i] = fmaf(half_at(sc.w[2 * mt + (i >> 1)][0], 0), gsum[mt][nb][i], acc[mt][nb][i]);
-        }
     } else {
-        // nibble formats, 32 weights at a time (a superblock group, half of a group of 64)
-#pragma unroll
-        for (int gp = 0; gp < 4; ++gp) {
-            const int gr = 4 * half + gp;
-            uint32_t a[2][2][4];                         // [m16][step][register]
+        // superblock groups of 32
+        decode_superblock<FMT>(cs, smin, wr, lane);
+#pragma unroll 2
+        for (int gr = 0; gr < 8; ++gr) {
+            uint32_t a[2][2][4];
             float2 sm2[4];
 #pragma unroll
-            for (int mr = 0; mr < 4; ++mr) {             // row 8 mr + g of the warp's 32
+            for (int mr = 0; mr < 4; ++mr) {
                 uint32_t o[4], h = 0u;
-                if constexpr (FMT == kFmtW4G64) {
-                    unpack_nibbles<4>(cw[gr][mr], 0u, o);
-                    sm2[mr].x = half_at(sc.w[mr][0], gp >> 1);
-                } else {
-                    const uint32_t rb = cs + (uint32_t)(wr + 8 * mr + g) * G::RB;
-                    if constexpr (FMT == kFmtW5SB32) {
-                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(h) : "r"(rb + 144 + 4 * gr + t));
-                        h |= h << 12;
-                    } else if constexpr (FMT == kFmtW6SB32) {
-                        h = lds16_a(rb + 144 + 8 * gr + 2 * t);
-                        h |= h << 8;
-                    }
-                    unpack_nibbles<G::B>(G::EARLY ? cw[gr][mr] : lds32_a(rb + 16 + 16 * gr + 4 * t), h, o);
-                    sm2[mr] = lds64f_a(smin + (8 * mr + g) * 64 + (((gr >> 1) ^ ((g >> 1) & 3)) << 4) + 8 * (gr & 1));
+                const uint32_t r = rb + 8 * mr * G::RB;
+                if constexpr (FMT == kFmtW5SB32) {
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(h) : "r"(r + 144 + 4 * gr + t));
+                    h |= h << 12;
+                } else if constexpr (FMT == kFmtW6SB32) {
+                    h = lds16_a(r + 144 + 8 * gr + 2 * t);
+                    h |= h << 8;
                 }
+                unpack_nibbles<G::B>(lds32_a(r + 16 + 16 * gr + 4 * t), h, o);
+                sm2[mr] = lds64f_a(smin + (8 * mr + g) * 64 + (((gr >> 1) ^ ((g >> 1) & 3)) << 4) + 8 * (gr & 1));
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     a[mr >> 1][s][mr & 1] = o[2 * s];
@@ -561,17 +560,17 @@ __device__ __forceinline__ void stage_math(uint32_t cs, const uint32_t (&cw)[8][
             for (int nb = 0; nb < NB; ++nb) {
                 if (NB > 1 && nb >= tiles) break;
                 const uint4 x = lds128_a(xl + nb * G::XB + gr * 512);
-                const float2 xc = lds64f_a(xs + nb * G::XB + G::KS * 16 + gr * 32 + t * 8);   // -OFF sum x of two rows
+                const float4 c = lds128f_a(xg + nb * G::XB + gr * 64);
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     float d[4];
-                    mma16816(d, a[mt][0], x.x, x.y, xc.x, xc.y, xc.x, xc.y);
+                    mma16816(d, a[mt][0], x.x, x.y, c.x, c.y, c.z, c.w);
                     mma16816(d, a[mt][1], x.z, x.w, d[0], d[1], d[2], d[3]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 m = sm2[2 * mt + (i >> 1)];
                         acc[mt][nb][i] = fmaf(m.x, d[i], acc[mt][nb][i]);
-                        if (is_sb(FMT)) acc[mt][nb][i] = fmaf(m.y, i & 1 ? xc.y : xc.x, acc[mt][nb][i]);
+                        acc[mt][nb][i] = fmaf(m.y, i & 1 ? c.y : c.x, acc[mt][nb][i]);
                     }
                 }
             }
@@ -826,7 +825,8 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
     const uint32_t sm = smem_u32(scratch);
     int cslot = 0, cwrap = 0, xslot = 0, xwrap = 0, left = n;
     auto wait = [&](uint64_t* bar, int wrap) {
-        return __all_sync(~0u, mbar_wait_bounded(bar, (uint32_t)wrap & 1u, kStatusTmaWait, 0u, p.wait_ns));
+        return __all_sync(~0u, mbar_try_wait(bar, (uint32_t)wrap & 1u)) ||
+               __all_sync(~0u, mbar_wait_bounded(bar, (uint32_t)wrap & 1u, kStatusTmaWait, 0u, p.wait_ns));
     };
     grid_dep_wait();                                      // counters and adapter terms come from prep_kernel
     for (int u = 0; left > 0; ++u) {
@@ -853,26 +853,15 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[mt][nb][i] = 0.0f;
+#pragma unroll 1
         for (int k = d.k0; k < d.k1; ++k) {
             if (!wait(&cfull[cslot], cwrap)) return;
             const uint32_t cs = base + cslot * G::CB, xs = xbase + xslot * p.xslot;
-            uint32_t cw[8][4];
-            if constexpr (is_sb(FMT)) decode_superblock<FMT>(cs, sm, wr, lane);
-            if constexpr (G::EARLY) {
-                take_codes<FMT>(cs, wr, lane, cw);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&cempty[cslot]);
-            }
             if (k > d.k0 && !wait(&xfull[xslot], xwrap)) return;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                Scales<FMT> sc;
-                read_scales<FMT>(xs + kSOff, wr, half, lane >> 2, sc);
-                stage_math<FMT, NB>(cs, cw, xs, sm, wr, half, lane, tiles, sc, acc);
-            }
+            stage_math<FMT, NB>(cs, xs, xs + kSOff, sm, wr, lane, tiles, acc);
             __syncwarp();
             if (lane == 0) {
-                if (!G::EARLY) mbar_arrive(&cempty[cslot]);
+                mbar_arrive(&cempty[cslot]);
                 mbar_arrive(&xempty[xslot]);
             }
             if (++cslot == ring) { cslot = 0; ++cwrap; }
