@@ -316,46 +316,53 @@ def rq_dequant(w: Packed, out: torch.Tensor | None = None, stream=None) -> torch
 
 
 # ------------------------------------- products that depend on the row --
-def _want(t: torch.Tensor, name: str, dtype, shape, device) -> None:
-    """Checks one tensor argument: dtype, shape (None: any size), a dense
-    layout, and that it lies on the call's GPU."""
+def _refuse(t, name: str, dtype, shape, device) -> None:
+    """Raises the ValueError that says what is wrong with a tensor argument."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise ValueError(f"{name} must be a {dtype} tensor")
-    if t.dim() != len(shape) or any(w is not None and int(s) != w for s, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in shape)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-class _On:
-    """Makes `device` current, and `stream` (or the device's current stream)
-    the one that a call and its temporary workspace use."""
-
-    def __init__(self, device: torch.device, stream):
-        if device.type != "cuda":
-            raise ValueError("the tensors must be on a CUDA device")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        other = torch.cuda.current_device() != device.index
-        self._cm = torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device) if other else None
-        self._device = device
-
-    def __enter__(self) -> ctypes.c_void_p:
-        if self._cm is not None:
-            self._cm.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream(self._device).cuda_stream)
-
-    def __exit__(self, *exc):
-        if self._cm is not None:
-            self._cm.__exit__(*exc)
+def _want(t, name: str, dtype, shape, device) -> int:
+    """The address of a dense tensor of this dtype and shape on this device;
+    anything else is refused."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        _refuse(t, name, dtype, shape, device)
+    return t.data_ptr()
 
 
-def _workspace(bytes_: int, device) -> torch.Tensor:
-    # from PyTorch's caching allocator, on the call's stream: freed to it on
-    # return, so calls on other streams and captured graphs get their own
-    return torch.empty(bytes_, dtype=torch.uint8, device=device)
+def _rows(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dim() == 0:
+        raise ValueError(f"{name} must be a tensor with rows")
+    return t.shape[0]
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _here(device: torch.device, stream) -> int:
+    """The current stream of `device` if it is the current device and no other
+    stream is asked for, else -1 (see _there)."""
+    if stream is None and device.type == "cuda" and torch.cuda.current_device() == device.index:
+        return _raw_stream(device.index)
+    return -1
+
+
+def _there(device: torch.device, stream):
+    """A context in which `device` is current, with `stream` (or the device's
+    current stream) as the stream of the call and of its temporary memory."""
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
 class GroupedExperts:
@@ -369,6 +376,7 @@ class GroupedExperts:
         self.w, self.E, self.N, self.K, self.max_rows = w, E, w.N // E, w.K, int(max_rows)
         self.device = w.codes.device
         self._desc = w.desc()
+        self._call = _lib().rq_wgemm_grouped
         self._bytes = int(_lib().rq_grouped_workspace_size(w.fmt, self.max_rows, w.K, self.N, E))
         if not self._bytes:
             raise RqError(RQ_ERR_UNSUPPORTED_SHAPE, "rq_grouped_workspace_size")
@@ -381,30 +389,32 @@ class GroupedExperts:
         that of in_rows, else of out_rows, else of x. y is [*, N] fp32 or bf16;
         without one a zeroed [rows, N] tensor of out_dtype is made. act: None
         or "relu2" (max(v, 0)^2)."""
-        dev = self.device
-        _want(x, "x", torch.bfloat16, (None, self.K), dev)
-        _want(offsets, "offsets", torch.int32, (self.E + 1,), dev)
-        R = int((in_rows if in_rows is not None else out_rows if out_rows is not None else x).shape[0])
-        if in_rows is not None:
-            _want(in_rows, "in_rows", torch.int32, (R,), dev)
-        if out_rows is not None:
-            _want(out_rows, "out_rows", torch.int32, (R,), dev)
+        dev, N = self.device, self.N
+        T = _rows(x, "x")
+        R = T if in_rows is None and out_rows is None else _rows(out_rows if in_rows is None else in_rows, "the row indices")
+        px = _want(x, "x", torch.bfloat16, (T, self.K), dev)
+        po = _want(offsets, "offsets", torch.int32, (self.E + 1,), dev)
+        pi = 0 if in_rows is None else _want(in_rows, "in_rows", torch.int32, (R,), dev)
+        pu = 0 if out_rows is None else _want(out_rows, "out_rows", torch.int32, (R,), dev)
         if R > self.max_rows:
             raise ValueError(f"{R} rows, prepared for at most {self.max_rows}")
         if act not in ACTS:
             raise ValueError(f"unknown activation {act!r}")
-        with _On(dev, stream) as st:
-            if y is None:
-                y = torch.zeros(R, self.N, dtype=out_dtype, device=dev)
-            _want(y, "y", y.dtype, (None, self.N), dev)
-            out = _out_type(y.dtype)
-            if x.shape[0] == 0 or R == 0 or y.shape[0] == 0:
-                return y
-            ws = _workspace(self._bytes, dev)
-            g = RqGroups(self.E, R, offsets.data_ptr(), None if in_rows is None else in_rows.data_ptr(),
-                         None if out_rows is None else out_rows.data_ptr())
-            _check(_lib().rq_wgemm_grouped(_ptr(x), x.shape[0], self.K, self.N, self._desc, g, _ptr(y), y.shape[0],
-                                           ACTS[act], out, _ptr(ws), self._bytes, st), "rq_wgemm_grouped")
+        st = _here(dev, stream)
+        if st < 0:
+            with _there(dev, stream):
+                return self(x, offsets, in_rows, out_rows, y, act, out_dtype)
+        if y is None:
+            y = torch.zeros(R, N, dtype=out_dtype, device=dev)
+        Ty = _rows(y, "y")
+        out = _out_type(y.dtype)
+        py = _want(y, "y", y.dtype, (Ty, N), dev)
+        if T and R and Ty:
+            # temporary memory from PyTorch's caching allocator on the call's stream: calls on other streams and
+            # captured graphs get their own
+            ws = torch.empty(self._bytes, dtype=torch.uint8, device=dev)
+            _check(self._call(px, T, self.K, N, self._desc, RqGroups(self.E, R, po, pi, pu), py, Ty, ACTS[act], out,
+                              ws.data_ptr(), self._bytes, st), "rq_wgemm_grouped")
         return y
 
 
@@ -412,8 +422,8 @@ def rq_wgemm_grouped(x: torch.Tensor, w: Packed, offsets: torch.Tensor, in_rows=
                      out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """Packed products grouped by expert: offsets int32 [E + 1], w a Packed of
     E * N rows. See GroupedExperts, which keeps what repeated calls share."""
-    R = max(1, int((in_rows if in_rows is not None else out_rows if out_rows is not None else x).shape[0]))
-    return GroupedExperts(w, int(offsets.shape[0]) - 1, R)(x, offsets, in_rows, out_rows, y, act, out_dtype, stream)
+    R = max(1, _rows(in_rows if in_rows is not None else out_rows if out_rows is not None else x, "x"))
+    return GroupedExperts(w, _rows(offsets, "offsets") - 1, R)(x, offsets, in_rows, out_rows, y, act, out_dtype, stream)
 
 
 class LoraProjection:
@@ -425,18 +435,16 @@ class LoraProjection:
     def __init__(self, w: Packed, A: torch.Tensor, B: torch.Tensor, scales: torch.Tensor, ranks: torch.Tensor | None = None,
                  max_rows: int = 128):
         dev = w.codes.device
-        if A.dim() != 3:
+        if not isinstance(A, torch.Tensor) or A.dim() != 3:
             raise ValueError("A must be [slots][rank][K]")
         n, r = int(A.shape[0]), int(A.shape[1])
-        _want(A, "A", torch.bfloat16, (n, r, w.K), dev)
-        _want(B, "B", torch.bfloat16, (n, w.N, r), dev)
-        _want(scales, "scales", torch.float32, (n,), dev)
-        if ranks is not None:
-            _want(ranks, "ranks", torch.int32, (n,), dev)
+        self._lora = RqLora(n, r, _want(A, "A", torch.bfloat16, (n, r, w.K), dev), _want(B, "B", torch.bfloat16, (n, w.N, r), dev),
+                            _want(scales, "scales", torch.float32, (n,), dev),
+                            None if ranks is None else _want(ranks, "ranks", torch.int32, (n,), dev))
         self.w, self.max_rows, self.device = w, int(max_rows), dev
         self._keep = (A, B, scales, ranks)
         self._desc = w.desc()
-        self._lora = RqLora(n, r, A.data_ptr(), B.data_ptr(), scales.data_ptr(), None if ranks is None else ranks.data_ptr())
+        self._call = _lib().rq_wgemm_lora
         self._bytes = int(_lib().rq_lora_workspace_size(w.fmt, self.max_rows, w.K, w.N, r))
         if not self._bytes:
             raise RqError(RQ_ERR_UNSUPPORTED_SHAPE, "rq_lora_workspace_size")
@@ -445,22 +453,23 @@ class LoraProjection:
                  out_dtype=torch.float32, stream=None) -> torch.Tensor:
         """y[m] = x[m] @ w_hat.T + scales[a] * (x[m] @ A[a].T) @ B[a].T with
         a = row_adapter[m] (int32 [M]; a row whose a is no slot has none)."""
-        dev, w = self.device, self.w
-        _want(x, "x", torch.bfloat16, (None, w.K), dev)
-        M = int(x.shape[0])
-        _want(row_adapter, "row_adapter", torch.int32, (M,), dev)
+        dev, N, K = self.device, self.w.N, self.w.K
+        M = _rows(x, "x")
+        px = _want(x, "x", torch.bfloat16, (M, K), dev)
+        pr = _want(row_adapter, "row_adapter", torch.int32, (M,), dev)
         if M > self.max_rows:
             raise ValueError(f"{M} rows, prepared for at most {self.max_rows}")
-        with _On(dev, stream) as st:
-            if y is None:
-                y = torch.empty(M, w.N, dtype=out_dtype, device=dev)
-            _want(y, "y", y.dtype, (M, w.N), dev)
-            out = _out_type(y.dtype)
-            if M == 0:
-                return y
-            ws = _workspace(self._bytes, dev)
-            _check(_lib().rq_wgemm_lora(_ptr(x), M, w.K, w.N, self._desc, self._lora, _ptr(row_adapter), _ptr(y), out,
-                                        _ptr(ws), self._bytes, st), "rq_wgemm_lora")
+        st = _here(dev, stream)
+        if st < 0:
+            with _there(dev, stream):
+                return self(x, row_adapter, y, out_dtype)
+        if y is None:
+            y = torch.empty(M, N, dtype=out_dtype, device=dev)
+        out = _out_type(y.dtype)
+        py = _want(y, "y", y.dtype, (M, N), dev)
+        if M:
+            ws = torch.empty(self._bytes, dtype=torch.uint8, device=dev)
+            _check(self._call(px, M, K, N, self._desc, self._lora, pr, py, out, ws.data_ptr(), self._bytes, st), "rq_wgemm_lora")
         return y
 
 
@@ -468,7 +477,7 @@ def rq_wgemm_lora(x: torch.Tensor, w: Packed, A: torch.Tensor, B: torch.Tensor, 
                   row_adapter: torch.Tensor, ranks=None, y=None, out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """A packed product with a low-rank adapter per row; see LoraProjection,
     which keeps what repeated calls share."""
-    return LoraProjection(w, A, B, scales, ranks, max(1, int(x.shape[0])))(x, row_adapter, y, out_dtype, stream)
+    return LoraProjection(w, A, B, scales, ranks, max(1, _rows(x, "x")))(x, row_adapter, y, out_dtype, stream)
 
 
 @dataclass
@@ -487,36 +496,41 @@ class TopkRouter:
 
     def __init__(self, E: int, k: int, renorm: bool = False):
         self.E, self.k, self.renorm = int(E), int(k), bool(renorm)
-        if not _lib().rq_route_workspace_size(1, self.E, self.k):
+        self._call, self._size = _lib().rq_route_topk, _lib().rq_route_workspace_size
+        if not self._size(1, self.E, self.k):
             raise ValueError("need 1 <= E <= 1024 and 1 <= k <= min(E, 16)")
 
     def __call__(self, logits: torch.Tensor, stream=None) -> Routing:
-        T, k, E, dev = int(logits.shape[0]), self.k, self.E, logits.device
+        T, k, E, dev = _rows(logits, "logits"), self.k, self.E, logits.device
         kind = _out_type(logits.dtype)
-        _want(logits, "logits", logits.dtype, (None, E), dev)
-        with _On(dev, stream) as st:
-            if T == 0:
-                z = torch.empty(0, dtype=torch.int32, device=dev)
-                return Routing(z.view(0, k), z.float().view(0, k), torch.zeros(E + 1, dtype=torch.int32, device=dev), z, z)
-            size = int(_lib().rq_route_workspace_size(T, E, k))
-            if not size:
-                raise RqError(RQ_ERR_INVALID_ARG, "rq_route_workspace_size")
-            # one buffer for the outputs, each at a multiple of 16 bytes, and one for the workspace
-            P, Q = (T * k + 3) & ~3, (E + 4) & ~3
-            b = torch.empty(4 * P + Q, dtype=torch.int32, device=dev)
-            r = Routing(b[:T * k].view(T, k), b[P:P + T * k].view(torch.float32).view(T, k), b[4 * P:4 * P + E + 1],
-                        b[2 * P:2 * P + T * k], b[3 * P:3 * P + T * k])
-            ws = _workspace(size, dev)
-            p = b.data_ptr()
-            out = RqRouting(p, p + 4 * P, p + 16 * P, p + 8 * P, p + 12 * P)
-            _check(_lib().rq_route_topk(_ptr(logits), kind, T, E, k, int(self.renorm), out, _ptr(ws), size, st),
-                   "rq_route_topk")
-        return r
+        pl = _want(logits, "logits", logits.dtype, (T, E), dev)
+        st = _here(dev, stream)
+        if st < 0:
+            with _there(dev, stream):
+                return self(logits)
+        n = T * k
+        if T == 0:
+            z = torch.empty(0, dtype=torch.int32, device=dev)
+            return Routing(z.view(0, k), z.float().view(0, k), torch.zeros(E + 1, dtype=torch.int32, device=dev), z, z)
+        size = self._size(T, E, k)
+        if not size:
+            raise RqError(RQ_ERR_INVALID_ARG, "rq_route_workspace_size")
+        # one buffer for the outputs and the workspace, each at a multiple of 16 bytes
+        P, Q = (n + 3) & ~3, (E + 4) & ~3
+        b = torch.empty(4 * P + Q + size // 4, dtype=torch.int32, device=dev)
+        p = b.data_ptr()
+        out = RqRouting(p, p + 4 * P, p + 16 * P, p + 8 * P, p + 12 * P)
+        _check(self._call(pl, kind, T, E, k, int(self.renorm), out, p + 16 * P + 4 * Q, size, st), "rq_route_topk")
+        pair, one = (k, 1), (1,)
+        return Routing(b.as_strided((T, k), pair, 0), b.view(torch.float32).as_strided((T, k), pair, P),
+                       b.as_strided((E + 1,), one, 4 * P), b.as_strided((n,), one, 2 * P), b.as_strided((n,), one, 3 * P))
 
 
 def rq_route_topk(logits: torch.Tensor, k: int, renorm: bool = False, stream=None) -> Routing:
     """The k largest of each token's logits with their softmax weights, and the
     chosen pairs grouped by expert; see include/rq.h."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a [T][E] tensor")
     return TopkRouter(int(logits.shape[1]), k, renorm)(logits, stream)
 
 
@@ -524,19 +538,23 @@ def rq_route_combine(y: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, 
                      out_dtype=None, stream=None) -> torch.Tensor:
     """out[t] = sum_j weights[t][j] * y[t k + j] over the j with ids[t][j] >= 0
     (y [T k][N], fp32 or bf16; out of out_dtype, by default y's)."""
+    if not isinstance(y, torch.Tensor) or y.dim() != 2 or not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("y must be [T k][N] and ids [T][k]")
     dev = y.device
-    T, k, N = int(ids.shape[0]), int(ids.shape[1]), int(y.shape[1])
+    (T, k), N = ids.shape, y.shape[1]
     kind = _out_type(y.dtype)
-    _want(y, "y", y.dtype, (T * k, N), dev)
-    _want(ids, "ids", torch.int32, (T, k), dev)
-    _want(weights, "weights", torch.float32, (T, k), dev)
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty(T, N, dtype=y.dtype if out_dtype is None else out_dtype, device=dev)
-        _want(out, "out", out.dtype, (T, N), dev)
-        if T:
-            _check(_lib().rq_route_combine(_ptr(y), kind, _ptr(ids), _ptr(weights), T, N, k, _ptr(out),
-                                           _out_type(out.dtype), st), "rq_route_combine")
+    py = _want(y, "y", y.dtype, (T * k, N), dev)
+    pi = _want(ids, "ids", torch.int32, (T, k), dev)
+    pw = _want(weights, "weights", torch.float32, (T, k), dev)
+    st = _here(dev, stream)
+    if st < 0:
+        with _there(dev, stream):
+            return rq_route_combine(y, ids, weights, out, out_dtype)
+    if out is None:
+        out = torch.empty(T, N, dtype=y.dtype if out_dtype is None else out_dtype, device=dev)
+    po = _want(out, "out", out.dtype, (T, N), dev)
+    if T:
+        _check(_lib().rq_route_combine(py, kind, pi, pw, T, N, k, po, _out_type(out.dtype), st), "rq_route_combine")
     return out
 
 
