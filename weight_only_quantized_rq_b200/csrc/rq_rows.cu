@@ -288,29 +288,34 @@ __global__ void __launch_bounds__(kPrepThreads, 16) prep_kernel(const PrepParams
             }
         }
     } else {
-        // t[m][j] = s_a A_a[j] . x[m]: one warp per (m, j)
-        const int per = p.r / (kPrepThreads / 32);
-        const int b = blockIdx.x - nx, m = b / per, j = (b % per) * (kPrepThreads / 32) + warp;
+        // t[m][j] = s_a A_a[j] . x[m]: a warp takes two ranks of a row, which share its x
+        const int per = p.r / (2 * (kPrepThreads / 32));
+        const int b = blockIdx.x - nx, m = b / per, j = 2 * ((b - m * per) * (kPrepThreads / 32) + warp);
         const int a = p.adapter[m];
         if (a < 0 || a >= p.n_adapters) return;
         if (p.ranks && j >= p.ranks[a]) return;
         const uint4* x = reinterpret_cast<const uint4*>(p.x + (size_t)m * p.pl.K);
         const uint4* w = reinterpret_cast<const uint4*>(p.A + ((size_t)a * p.r + j) * p.pl.K);
+        const int nc = p.pl.K / 8;
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll 2
-        for (int c = lane; c < p.pl.K / 8; c += 32) {
-            const uint4 u = x[c], v = w[c];
-            const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+        for (int c = lane; c < nc; c += 32) {
+            const uint4 u = x[c], v0 = __ldg(w + c), v1 = __ldg(w + nc + c);
+            const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, a0[4] = {v0.x, v0.y, v0.z, v0.w}, a1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s0 = fmaf(bf16lo_f32(uu[i]), bf16lo_f32(vv[i]), s0);
-                s1 = fmaf(bf16hi_f32(uu[i]), bf16hi_f32(vv[i]), s1);
+                s0 = fmaf(bf16lo_f32(uu[i]), bf16lo_f32(a0[i]), s0);
+                s1 = fmaf(bf16lo_f32(uu[i]), bf16lo_f32(a1[i]), s1);
+                s0 = fmaf(bf16hi_f32(uu[i]), bf16hi_f32(a0[i]), s0);
+                s1 = fmaf(bf16hi_f32(uu[i]), bf16hi_f32(a1[i]), s1);
             }
         }
-        float s = s0 + s1;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-        if (lane == 0) p.t[(size_t)m * p.r + j] = s * p.alpha[a];
+        for (int o = 16; o; o >>= 1) {
+            s0 += __shfl_xor_sync(~0u, s0, o);
+            s1 += __shfl_xor_sync(~0u, s1, o);
+        }
+        if (lane < 2) p.t[(size_t)m * p.r + j + lane] = (lane ? s1 : s0) * p.alpha[a];   // one past the rank is not read
     }
 }
 
@@ -319,6 +324,9 @@ __device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap* map, 
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(p), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void bulk_x(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
@@ -605,28 +613,69 @@ __device__ __forceinline__ Work get_work(const Plan& pl, const Groups& g, long l
     return w;
 }
 
-// The adapter's term for weight rows n .. n + 7 of row m: adapter a, of which
-// `rank` counts.
-__device__ __forceinline__ void add_adapter(const RowsParams& p, int m, int a, int rank, int n, float (&v)[8]) {
-    const float* t = p.t + (size_t)m * p.r;
-    const __nv_bfloat16* B = p.B + ((size_t)a * p.pl.N + n) * p.r;
-    const int rows = min(8, p.pl.N - n);
-    for (int j = 0; j < rank; j += 8) {
-        uint4 b[8];
+// fp32 pair -> bf16x2 (nearest even), lo in the low half.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// Adds the adapters' term over ranks 32 c .. 32 c + 31 to one 8-row tile's
+// sums: for each adapter among the tile's rows D += B_a t^T, with t zero for
+// the other rows. t is split into three bf16 parts (24 bits), so that nothing
+// of it is lost to the tensor core's operand type. Lane 4 g + q holds ranks
+// 8 q .. 8 q + 7 of the chunk: of weight rows n + 8 i (i = 0..3) and of
+// activation row g.
+__device__ __forceinline__ void add_adapters(const RowsParams& p, const Desc& d, int tile, int c, int n, int lane,
+                                             float (&acc0)[4], float (&acc1)[4]) {
+    const int i = 8 * tile + (lane >> 2), m = d.row0 + i, j0 = 32 * c + 8 * (lane & 3);
+    int a = -1, rank = 0;
+    if (i < d.rows) {
+        a = p.adapter[m];
+        if (a >= 0 && a < p.n_adapters) rank = p.ranks ? min(p.ranks[a], p.r) : p.r;
+        if (rank <= 32 * c) a = -1;
+    }
+    uint32_t t[3][4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) b[q] = __ldg(reinterpret_cast<const uint4*>(B + (size_t)min(q, rows - 1) * p.r + j));
-        const float4 t0 = *reinterpret_cast<const float4*>(t + j), t1 = *reinterpret_cast<const float4*>(t + j + 4);
-        const float tv[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+    for (int q = 0; q < 4; ++q) {
+        float2 v = make_float2(0.0f, 0.0f);
+        if (a >= 0 && j0 + 2 * q < rank) {
+            v = *reinterpret_cast<const float2*>(p.t + (size_t)m * p.r + j0 + 2 * q);
+            if (j0 + 2 * q + 1 >= rank) v.y = 0.0f;
+        }
+        t[0][q] = pack2(v.x, v.y);
+        v.x -= bf16lo_f32(t[0][q]);
+        v.y -= bf16hi_f32(t[0][q]);
+        t[1][q] = pack2(v.x, v.y);
+        v.x -= bf16lo_f32(t[1][q]);
+        v.y -= bf16hi_f32(t[1][q]);
+        t[2][q] = pack2(v.x, v.y);
+    }
+    unsigned todo = __ballot_sync(~0u, a >= 0);
+    while (todo) {
+        const int src = __ffs(todo) - 1, aa = __shfl_sync(~0u, a, src), rk = __shfl_sync(~0u, rank, src);
+        const bool same = a == aa;
+        todo &= ~__ballot_sync(~0u, same);
+        uint4 b[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const uint32_t bb[4] = {b[q].x, b[q].y, b[q].z, b[q].w};
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float w = i & 1 ? bf16hi_f32(bb[i >> 1]) : bf16lo_f32(bb[i >> 1]);
-                if (j + i < rank) s = fmaf(tv[i], w, s);                 // past the rank the slot may hold anything
+        for (int q = 0; q < 4; ++q) {
+            b[q] = make_uint4(0u, 0u, 0u, 0u);
+            if (j0 < rk) b[q] = __ldg(reinterpret_cast<const uint4*>(p.B + ((size_t)aa * p.pl.N + min(n + 8 * q, p.pl.N - 1)) * p.r + j0));
+            const int keep = rk - j0;                    // past the rank the slot may hold anything
+            if (keep < 8) {
+                const auto cut = [&](uint32_t w, int k) { return k + 1 < keep ? w : k < keep ? w & 0xffffu : 0u; };
+                b[q] = make_uint4(cut(b[q].x, 0), cut(b[q].y, 2), cut(b[q].z, 4), cut(b[q].w, 6));
             }
-            v[q] += s;
+        }
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+            const uint32_t t0 = same ? t[s][0] : 0u, t1 = same ? t[s][1] : 0u, t2 = same ? t[s][2] : 0u, t3 = same ? t[s][3] : 0u;
+            const uint32_t a0[4] = {b[0].x, b[1].x, b[0].y, b[1].y}, a1[4] = {b[2].x, b[3].x, b[2].y, b[3].y};
+            const uint32_t a2[4] = {b[0].z, b[1].z, b[0].w, b[1].w}, a3[4] = {b[2].z, b[3].z, b[2].w, b[3].w};
+            mma16816(acc0, a0, t0, t1, acc0[0], acc0[1], acc0[2], acc0[3]);
+            mma16816(acc1, a1, t0, t1, acc1[0], acc1[1], acc1[2], acc1[3]);
+            mma16816(acc0, a2, t2, t3, acc0[0], acc0[1], acc0[2], acc0[3]);
+            mma16816(acc1, a3, t2, t3, acc1[0], acc1[1], acc1[2], acc1[3]);
         }
     }
 }
@@ -768,6 +817,11 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
                 mbar_arrive_expect_tx(&xfull[xslot], (uint32_t)(tiles * G::XB));
             }
             __syncwarp();
+            if (p.adapter && k == 0) {                                   // the adapters' B rows into L2, by the unit's first CTA
+                const int a = lane < w.rows ? p.adapter[w.row0 + lane] : -1;
+                if (a >= 0 && a < p.n_adapters && (lane == 0 || p.adapter[w.row0 + lane - 1] != a))
+                    prefetch_l2_bulk(p.B + ((size_t)a * p.pl.N + w.n0) * p.r, (uint32_t)(min(kRowsPerTile, p.pl.N - w.n0) * p.r * 2));
+            }
             if (lane < tiles)
                 bulk_x(xs + lane * G::XB, p.xf + ((size_t)(w.tile0 + lane) * T + k) * G::XB, G::XB, &xfull[xslot]);
             if constexpr (!is_sb(FMT)) {
@@ -833,18 +887,11 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
         if (!wait(&xfull[xslot], xwrap)) return;
         const Desc d = desc[u % kDescs];
         const int tiles = (d.rows + 7) / 8;
-        // this lane's rows of y, and their adapters, for the end
-        int out[NB], ad[NB], rk[NB];
+        int out[NB];                                      // this lane's rows of y, for the end
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             const int i = 8 * nb + (lane >> 2), m = d.row0 + i;
             out[nb] = i >= d.rows ? -1 : p.out_rows ? p.out_rows[m] : m;
-            ad[nb] = -1;
-            rk[nb] = 0;
-            if (p.adapter && i < d.rows) {
-                ad[nb] = p.adapter[m];
-                if (ad[nb] >= 0 && ad[nb] < p.n_adapters) rk[nb] = p.ranks ? min(p.ranks[ad[nb]], p.r) : p.r;
-            }
         }
         float acc[2][NB][4];
 #pragma unroll
@@ -869,7 +916,19 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
         }
         left -= d.k1 - d.k0;
 
-        if (d.first != d.last) {
+        const int parts = d.last - d.first + 1;
+        if (p.adapter) {
+            // the parts of a unit share its (tile, 32 ranks) pairs
+            const int chunks = (p.r + 31) / 32, me = (int)blockIdx.x - d.first;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                if (nb >= tiles) break;
+                for (int c = 0; c < chunks; ++c)
+                    if (parts == 1 || (c * tiles + nb) % parts == me)
+                        add_adapters(p, d, nb, c, d.n0 + wr + (lane >> 2), lane, acc[0][nb], acc[1][nb]);
+            }
+        }
+        if (parts > 1) {
             // a part of a unit: CTA c's part lies in slot 2c (it began in an earlier CTA) or 2c + 1
             constexpr int kPart = kMathWarps * 2 * NB * 32;              // float4 per slot
             float4* part = reinterpret_cast<float4*>(p.part) + warp * (2 * NB * 32) + lane;
@@ -887,7 +946,7 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
             unsigned old = 0;
             if (lane == 0) old = atomicAdd(&p.count[d.first * kMathWarps + warp], 1u);
             old = __shfl_sync(~0u, old, 0);
-            if (old != (unsigned)(d.last - d.first)) continue;           // not the last to arrive
+            if (old != (unsigned)(parts - 1)) continue;           // not the last to arrive
             __threadfence();
             constexpr int kAhead = NB == 1 ? 4 : NB == 2 ? 2 : 1;        // parts read together
             for (int c0 = d.first; c0 <= d.last; c0 += kAhead) {
@@ -935,7 +994,6 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
             const float4* f = reinterpret_cast<const float4*>(scratch) + (lane >> 2) * 8;
             const float4 f0 = f[(2 * (lane & 3)) ^ (lane >> 2)], f1 = f[(2 * (lane & 3) + 1) ^ (lane >> 2)];
             float v[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-            if (rk[nb] > 0) add_adapter(p, d.row0 + 8 * nb + (lane >> 2), ad[nb], rk[nb], nn, v);
             if (p.act) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -1057,7 +1115,7 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
     q.t = reinterpret_cast<float*>(ws + l.t);
     q.n_adapters = a.n_adapters;
     q.r = a.r;
-    const long long blocks = (long long)q.tiles_max * q.kblocks + (a.adapter ? (long long)a.R * (a.r / (kPrepThreads / 32)) : 0);
+    const long long blocks = (long long)q.tiles_max * q.kblocks + (a.adapter ? (long long)a.R * (a.r / (2 * (kPrepThreads / 32))) : 0);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
