@@ -155,6 +155,29 @@ def test_grouped_long(orc, fmt, sizes):
     run_grouped(orc, fmt, 512, 264, sizes, act="relu2", dtype=torch.bfloat16, seed=9)
 
 
+@pytest.mark.parametrize("fmt,K", [("w4g64", 64), ("w4g64", 320), ("w4g64", 4096), ("w8g16", 64), ("w8g16", 192), ("w8g64", 448),
+                                   ("w6g16", 64), ("w6g16", 832), ("w4sb32", 256), ("w5sb32", 768), ("w6sb32", 512)])
+@pytest.mark.parametrize("sizes,N", [([40, 33], 72), ([24], 1), ([25, 200, 0], 129), ([300, 129], 130)])
+def test_grouped_many_rows(orc, fmt, K, sizes, N):
+    """Groups long enough for the tensor-memory kernel: few tiles (units cut among CTAs), odd widths, K with a ragged end."""
+    run_grouped(orc, fmt, K, N, sizes, gather=True, tail=3, dtype=torch.bfloat16, seed=14)
+
+
+def test_grouped_many_rows_extremes(orc):
+    """Rows of very different sizes, tiny, huge, zero and not finite, beside one another in a tile."""
+    w, What = random_packed(orc, "w8g16", 2 * 136, 256, 15)
+    x = rows_of(60, 256, 15)
+    x *= (2.0 ** torch.linspace(-100, 100, 60)).to(torch.bfloat16).to(DEV)[:, None]
+    x[7] = 0.0
+    x[11, 3], x[40, 255] = float("inf"), float("nan")
+    off = torch.tensor([0, 27, 60], dtype=torch.int32, device=DEV)
+    y = rq.rq_wgemm_grouped(x, w, off, out_dtype=torch.bfloat16)
+    good = [i for i in range(60) if i not in (11, 40)]
+    ref = grouped_ref(x, What, 2, [0, 27, 60], None)
+    check(y[good], torch.stack([ref[i][0] for i in good]), torch.stack([ref[i][1] for i in good]), 256)
+    assert not torch.isfinite(y[[11, 40]]).any()
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_grouped_relu2(orc, dtype):
     run_grouped(orc, "w4g64", 512, 96, [5, 20, 0, 2], act="relu2", dtype=dtype, seed=10)

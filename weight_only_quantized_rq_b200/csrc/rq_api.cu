@@ -183,10 +183,20 @@ int rq_wgemm_batch(const rq_wgemm_item* items, int count, int M, void* stream) {
 // y; experts; adapter rank).
 constexpr int kMaxRows = 1 << 20, kMaxExperts = 1024, kMaxRank = 256;
 
+// Groups of this many rows on average go to the tensor-memory kernel.
+constexpr int kWideRows = 24;
+static bool wide_rows(int R, int E) { return R >= kWideRows * E; }
+
+static size_t grouped_bytes(int fmt, int R, int K, int N, int E) {
+    const size_t a = rq::rows_workspace(fmt, R, K, N, E, 0), b = wide_rows(R, E) ? rq::wide_workspace(R, K, E) : 0;
+    return a > b ? a : b;
+}
+
 size_t rq_grouped_workspace_size(int fmt, int R, int K, int N, int E) {
     if (E < 1 || E > kMaxExperts || N < 1 || N > (1 << 24) / E || R < 1 || R > kMaxRows) return 0;
     if (shape_status(fmt, K, E * N) != RQ_OK) return 0;
-    return rq::rows_workspace(fmt, R, K, N, E, 0);
+    // enough for any smaller R too: the paths' needs grow with R but for the step between them
+    return grouped_bytes(fmt, R, K, N, E);
 }
 
 int rq_wgemm_grouped(const void* x, int T, int K, int N, const rq_packed* w, const rq_groups* g, void* y, int Ty, int act,
@@ -201,12 +211,13 @@ int rq_wgemm_grouped(const void* x, int T, int K, int N, const rq_packed* w, con
     if (!aligned16(x) || !aligned16(y) || !aligned16(workspace) || !aligned16(g->offsets) ||
         (g->in_rows && !aligned16(g->in_rows)) || (g->out_rows && !aligned16(g->out_rows)))
         return RQ_ERR_MISALIGNED;
-    if (workspace_bytes < rq::rows_workspace(w->fmt, g->R, K, N, g->E, 0)) return RQ_ERR_INVALID_ARG;
+    if (workspace_bytes < grouped_bytes(w->fmt, g->R, K, N, g->E)) return RQ_ERR_INVALID_ARG;
     rq::RowsArgs a = {};
     a.fmt = w->fmt; a.T = T; a.K = K; a.N = N; a.E = g->E; a.R = g->R; a.Ty = Ty;
     a.x = x; a.codes = w->codes; a.scales = w->scales;
     a.offsets = g->offsets; a.in_rows = g->in_rows; a.out_rows = g->out_rows;
     a.y = y; a.ybf16 = out_type == RQ_OUT_BF16; a.act = act; a.ws = workspace;
+    if (a.ybf16 && wide_rows(g->R, g->E)) return cuda_status(rq::launch_wide(a, static_cast<cudaStream_t>(stream)));
     return cuda_status(rq::launch_rows(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -312,13 +323,14 @@ int rq_last_cuda_error(void) { return t_last_cuda; }
 int rq_device_status(void* stream, int* word) {
     if (!word) return RQ_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    unsigned a = 0, b = 0, c = 0, d = 0, r = 0;
+    unsigned a = 0, b = 0, c = 0, d = 0, r = 0, v = 0;
     int s = cuda_status(rq::status_pack(st, &a));
     if (s == RQ_OK) s = cuda_status(rq::status_gemv(st, &b));
     if (s == RQ_OK) s = cuda_status(rq::status_tc(st, &c));
     if (s == RQ_OK) s = cuda_status(rq::status_gptq(st, &d));
     if (s == RQ_OK) s = cuda_status(rq::status_rows(st, &r));
-    const unsigned w = a | b | c | d | r;
+    if (s == RQ_OK) s = cuda_status(rq::status_wide(st, &v));
+    const unsigned w = a | b | c | d | r | v;
     *word = (int)w;
     if (s != RQ_OK) return s;
     if (w & ~(unsigned)rq::kStatusNotSpd) return RQ_ERR_DEVICE_TIMEOUT;

@@ -128,6 +128,10 @@ struct RowsArgs {
 size_t rows_workspace(int fmt, int R, int K, int N, int E, int rank);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st);
 
+// The grouped products for groups of many rows, bf16 results (rq_wide.cu).
+size_t wide_workspace(int R, int K, int E);
+cudaError_t launch_wide(const RowsArgs& a, cudaStream_t st);
+
 // Expert routing (rq_route.cu).
 struct RouteArgs {
     const void* logits;        // fp32 or bf16 [T][E]
@@ -161,6 +165,7 @@ cudaError_t status_gptq(cudaStream_t st, unsigned* word);
 cudaError_t status_gemv(cudaStream_t st, unsigned* word);
 cudaError_t status_tc(cudaStream_t st, unsigned* word);
 cudaError_t status_rows(cudaStream_t st, unsigned* word);
+cudaError_t status_wide(cudaStream_t st, unsigned* word);
 
 int sm_count();   // multiprocessors of the current device
 

@@ -47,6 +47,7 @@
 
 #include "rq_device.cuh"
 #include "rq_internal.h"
+#include "rq_tc.cuh"
 
 namespace rq {
 namespace {
@@ -320,11 +321,6 @@ __global__ void __launch_bounds__(kPrepThreads, 16) prep_kernel(const PrepParams
 }
 
 // ------------------------------------------------------------ PTX wrappers
-__device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar)) : "memory");
-}
 __device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(p), "r"(bytes) : "memory");
 }
@@ -780,7 +776,7 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
         auto codes = [&](const Cursor& c, int slot) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(&cfull[slot], (uint32_t)(kRowsPerTile * G::RB));
-                tma_codes(base + slot * G::CB, &p.cmap, c.k * G::RB, c.w.e * p.pl.N + c.w.n0, &cfull[slot]);
+                tma_2d(base + slot * G::CB, &p.cmap, c.k * G::RB, c.w.e * p.pl.N + c.w.n0, &cfull[slot]);
             }
         };
         Cursor cc, cx;
@@ -1008,25 +1004,9 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
 }
 
 // ------------------------------------------------------------------ host
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-    static EncodeTiled fn = nullptr;
-    static int tried = 0;
-    if (!__atomic_load_n(&tried, __ATOMIC_ACQUIRE)) {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiled>(f);
-        __atomic_store_n(&tried, 1, __ATOMIC_RELEASE);
-    }
-    return fn;
-}
-
 constexpr int kMaxCtas = 768;          // CTAs of a launch at most
+
+// CTAs of a launch at most
 
 // 8-row tiles per unit: as many as an even split of the rows fills, since a
 // group with more rows than a unit holds streams its weights once per unit.

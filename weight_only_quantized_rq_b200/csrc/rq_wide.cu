@@ -1,0 +1,748 @@
+// rq_wide.cu -- the grouped products for groups of many rows (prompts), on the
+// 5th-generation tensor cores: y[i] = act(x[in(i)] W_e^T) with bf16 results.
+//
+// lay_rows_kernel gathers the rows into group order as fp16 under a power of
+// two per row (the largest value in [2^14, 2^15); bf16 values are exact there
+// down to 2^-31 of the row's largest), in the order in which the codes unpack.
+// wide_kernel multiplies:
+//   * A unit is 128 weight rows x K x up to MC activation rows of one expert.
+//     tcgen05.mma takes the weights from tensor memory (A) and the activations
+//     from shared memory (B); the fp32 sums stay in tensor memory until the
+//     unit's end.
+//   * Sixteen warps unpack: a thread owns one weight row of the tile (its
+//     tensor-memory lane) and 64 weights of every fourth 64-K atom. A weight is
+//     q s (or S u - M) rounded once to fp16 (2^-12 relative, an eighth of the
+//     result's own rounding to bf16); fp16 instead of bf16 for both operands
+//     buys that. |w_hat| above 65504 overflows.
+//   * Bound by arithmetic where groups are long: per 64-K atom the tensor
+//     cores need 2 MC cycles, the unpacking about 110 issue slots per warp
+//     scheduler, and shared memory is filled with 128 MC bytes of activations
+//     and 128 rows of codes.
+//   * Units are cut where an even share of the work (rows x K) ends, so every
+//     CTA (one per SM) has the same; a cut unit's parts are summed through the
+//     workspace in K order by whichever CTA arrives last.
+// Roles: 16 unpacking warps (they also move the sums out), one warp that
+// issues the MMAs, one thread that issues the tensor copies.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "rq_device.cuh"
+#include "rq_internal.h"
+#include "rq_tc.cuh"
+
+namespace rq {
+namespace {
+
+constexpr int kWorkers = 16;
+constexpr int kGroups = 4;              // warps 4 g .. 4 g + 3 take atoms g, g + 4, ...
+constexpr int kWideThreads = 32 * (kWorkers + 2);
+constexpr int kMaxX = 8;                // activation slots at most
+constexpr int kCodeSlots = 2;           // even: a slot's stages always go to the same warps
+constexpr int kDescs = 8;
+constexpr size_t kWideSmem = 226 * 1024;
+constexpr int kWideMaxCtas = 256;
+
+template <int FMT>
+struct Wide {
+    static constexpr int KS = is_w8(FMT) || FMT == kFmtW6G16 ? 128 : 256;         // K per code slot
+    static constexpr int RB = FMT == kFmtW4G64 || is_w8(FMT) ? 128 : FMT == kFmtW6G16 ? 96 : sb_record(FMT);
+    static constexpr int CB = (kTcRows * RB + 1023) & ~1023;
+    static constexpr int ATOMS = KS / 64;
+    // order of a row's values within 8 (1: 0 4 1 5 2 6 3 7) or 4 (2: 0 2 1 3)
+    static constexpr int ORDER = is_sb(FMT) ? 0 : is_w8(FMT) ? 2 : 1;
+};
+
+struct WidePlan {
+    const int* offsets;
+    int E, R, N, K, T, MC;
+};
+
+struct WideParams {
+    CUtensorMap cmap;                   // codes: uint8 [E N][row bytes], box [128][RB]
+    CUtensorMap xmap;                   // rows: fp16 [R][K] viewed as [K / 64][R][64], box [1][32][64]
+    WidePlan pl;
+    const uint8_t* scales;
+    unsigned long long total_rows;
+    uint32_t srb;
+    const float* rscale;                // [R] inverse of a row's power of two
+    float* part;                        // partial tiles, two per CTA
+    unsigned* count;                    // stages summed of a cut unit, by its first CTA and warp
+    const int* out_rows;
+    void* y;
+    int Ty, act;
+    int xslots;
+    unsigned long long wait_ns;
+    int test_flags;
+};
+
+// ------------------------------------------------------------------- rows
+constexpr int kLayThreads = 256;
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// One warp per row: the largest exponent, then the row under its power of two.
+template <int ORDER>
+__global__ void __launch_bounds__(kLayThreads) lay_rows_kernel(const __nv_bfloat16* x, const int* in_rows, int rows_x, int R, int K,
+                                                             uint4* out, float* rscale, unsigned* count, int n_count) {
+    const int lane = threadIdx.x & 31;
+    grid_dep_wait();
+    grid_dep_launch();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < n_count; i += kLayThreads) count[i] = 0u;
+    const int row = blockIdx.x * (kLayThreads / 32) + (threadIdx.x >> 5);
+    if (row >= R) return;
+    int src = in_rows ? in_rows[row] : row;
+    if (src < 0 || src >= rows_x) src = -1;
+    const uint4* p = reinterpret_cast<const uint4*>(x + (size_t)(src < 0 ? 0 : src) * K);
+    const int nc = K / 8;
+    uint32_t top = 0u;
+    if (src >= 0) {
+#pragma unroll 4
+        for (int c = lane; c < nc; c += 32) {
+            const uint4 v = p[c];
+            const uint32_t m = 0x7fff7fffu;
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m)));
+        }
+    }
+    top = max(top & 0xffffu, top >> 16);
+    top = __reduce_max_sync(~0u, top);
+    const int ex = (int)(top >> 7);                      // biased exponent of the largest value; 255: not finite
+    int sh = 0;
+    if (ex < 255 && top) sh = max(-126, min(126, 141 - ex));
+    const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
+    if (lane == 0) rscale[row] = __uint_as_float((uint32_t)(127 - sh) << 23);
+    uint4* o = out + (size_t)row * nc;
+#pragma unroll 2
+    for (int c = lane; c < nc; c += 32) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (src >= 0) v = p[c];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = half2_bits(bf16lo_f32(w[i]) * f, bf16hi_f32(w[i]) * f);
+        if (ORDER == 1) o[c] = make_uint4(prmt(h[0], h[2], 0x5410u), prmt(h[0], h[2], 0x7632u), prmt(h[1], h[3], 0x5410u), prmt(h[1], h[3], 0x7632u));
+        else if (ORDER == 2) o[c] = make_uint4(prmt(h[0], h[1], 0x5410u), prmt(h[0], h[1], 0x7632u), prmt(h[2], h[3], 0x5410u), prmt(h[2], h[3], 0x7632u));
+        else o[c] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+}
+
+// ------------------------------------------------------------------ groups
+// Per expert: first row, and the cost of all K stages before it. An expert's
+// rows are cut into equal chunks (a multiple of 16 rows, at most MC).
+struct WGroups {
+    long long* cost;   // [E + 1]
+    int* row;          // [E + 1]
+};
+__host__ __device__ inline size_t wgroups_bytes(int E) { return round16((size_t)(E + 1) * 12); }
+
+__device__ __forceinline__ int chunk_rows(int m, int MC) {
+    const int c = (m + MC - 1) / MC;
+    return c ? ((m + c - 1) / c + 15) & ~15 : 16;
+}
+// Cost of a stage: the rows that the tensor cores multiply, at least what
+// unpacking takes.
+__device__ __forceinline__ int stage_cost(int rows) { return max(rows, 96); }
+
+__device__ __forceinline__ void scan_wide(const WidePlan& pl, WGroups g, int lane) {
+    const int tiles_n = (pl.N + kTcRows - 1) / kTcRows;
+    int top = 0;
+    long long base = 0;
+    for (int e0 = 0; e0 <= pl.E; e0 += 32) {
+        const int e = e0 + lane;
+        int v = e <= pl.E ? min(max(pl.offsets[e], 0), pl.R) : 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(~0u, v, o);
+            if (lane >= o) v = max(v, w);
+        }
+        v = max(v, top);
+        const int prev = __shfl_up_sync(~0u, v, 1);
+        const int m = lane == 0 ? (e0 ? v - top : 0) : v - prev;       // rows of group e - 1
+        const int rc = chunk_rows(m, pl.MC);
+        long long c = (long long)((m + rc - 1) / rc) * tiles_n * pl.T * stage_cost(rc);
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long b = __shfl_up_sync(~0u, c, o);
+            if (lane >= o) c += b;
+        }
+        if (e <= pl.E) {
+            g.row[e] = v;
+            g.cost[e] = base + c;
+        }
+        top = __shfl_sync(~0u, v, 31);
+        base += __shfl_sync(~0u, c, 31);
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ int last_at_most(const long long* a, int E, long long v) {
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a[mid] <= v) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// A stretch of a unit in one CTA.
+struct __align__(16) WDesc {
+    int done;          // no more work
+    int row0, rows;    // rows of the call
+    int n0, wrow;      // first weight row within the expert, and in the plane
+    int k0, k1;        // stages
+    int first, last;   // CTAs that share the unit
+    int cost;          // of a stage
+    long long pos;     // cost position of the unit's first stage
+};
+
+__device__ __forceinline__ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// ------------------------------------------------------------------ unpack
+__device__ __forceinline__ uint32_t h2(uint16_t v) { return (uint32_t)v * 0x10001u; }
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) { uint32_t d; asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b)); return d; }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) { uint32_t d; asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b)); return d; }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+// (v & m) | c
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t m, uint32_t c) { return lop_mask_or(v, m, c); }
+__device__ __forceinline__ uint4 lds4(uint32_t a) { return lds128_a(a); }
+
+// 64 weights of the thread's row in an atom -> 32 fp16 pairs. cs: the row's
+// bytes of the slot; at: atom of the slot; sc: its scale words (two fp16
+// each); sw: swizzle of 16-byte chunks (row % 8, or 0).
+template <int FMT>
+__device__ __forceinline__ void unpack_atom(uint32_t cs, int at, int sw, const uint32_t (&sc)[2], uint32_t (&o)[32]) {
+    if constexpr (FMT == kFmtW4G64) {
+        // (1024 + u) - 1032 and (1024 + 16 u) / 16 - 72 give q exactly; q s is rounded once
+        const uint4 c0 = lds4(cs + (((2 * at) ^ sw) << 4)), c1 = lds4(cs + (((2 * at + 1) ^ sw) << 4));
+        const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        const uint32_t s = h2((uint16_t)(sc[0] & 0xffffu));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t v = w[i] >> 8;
+            o[4 * i + 0] = hmul2(hadd2(and_or(w[i], 0x000F000Fu, 0x64006400u), 0xE408E408u), s);
+            o[4 * i + 1] = hmul2(hfma2(and_or(w[i], 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u), s);
+            o[4 * i + 2] = hmul2(hadd2(and_or(v, 0x000F000Fu, 0x64006400u), 0xE408E408u), s);
+            o[4 * i + 3] = hmul2(hfma2(and_or(v, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u), s);
+        }
+    } else if constexpr (is_w8(FMT)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint4 v = lds4(cs + (((4 * at + c) ^ sw) << 4));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t s = FMT == kFmtW8G64 ? h2((uint16_t)(sc[0] & 0xffffu)) : h2((uint16_t)(c & 1 ? sc[c >> 1] >> 16 : sc[c >> 1] & 0xffffu));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[8 * c + 2 * i] = hmul2(hadd2(and_or(w[i], 0x00FF00FFu, 0x64006400u), 0xE480E480u), s);        // - 1152
+                o[8 * c + 2 * i + 1] = hmul2(hadd2(and_or(w[i] >> 8, 0x00FF00FFu, 0x64006400u), 0xE480E480u), s);
+            }
+        }
+    } else if constexpr (FMT == kFmtW6G16) {
+        const uint4 c0 = lds4(cs + 48 * at), c1 = lds4(cs + 48 * at + 16), pl = lds4(cs + 48 * at + 32);
+        const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w}, p[4] = {pl.x, pl.y, pl.z, pl.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t ph = (p[i >> 1] >> (16 * (i & 1))) & 0xffffu, h = ph | (ph << 8);
+            const uint32_t s = h2((uint16_t)((i >> 1) & 1 ? sc[i >> 2] >> 16 : sc[i >> 2] & 0xffffu));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t hs = q < 2 ? h << (4 - 2 * q) : h >> (2 * q - 4);
+                const uint32_t u = and_or(hs, 0x00300030u, and_or(w[i] >> (4 * q), 0x000F000Fu, 0x64006400u));
+                o[4 * i + q] = hmul2(hadd2(u, 0xE420E420u), s);                                                // - 1056
+            }
+        }
+    } else {
+        // S u - M in fp32, S = d sc and M = dmin m exact, then one rounding
+        const uint4 hd = lds4(cs);
+        const float d = __half2float(__ushort_as_half((uint16_t)(hd.x & 0xffffu)));
+        const float dm = __half2float(__ushort_as_half((uint16_t)(hd.x >> 16)));
+#pragma unroll
+        for (int gl = 0; gl < 2; ++gl) {
+            const int j = 2 * at + gl;
+            const float S = __fmul_rn(d, (float)sb_field(hd.y, hd.z, hd.w, 0, j));
+            const float c = __fmaf_rn(-128.0f, S, -__fmul_rn(dm, (float)sb_field(hd.y, hd.z, hd.w, 1, j)));
+            const uint4 cw = lds4(cs + 16 + 16 * j);
+            const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
+            uint32_t pl[2] = {0u, 0u};
+            if constexpr (FMT == kFmtW5SB32) pl[0] = lds32_a(cs + 144 + 4 * j);
+            if constexpr (FMT == kFmtW6SB32) {
+                pl[0] = lds32_a(cs + 144 + 8 * j);
+                pl[1] = lds32_a(cs + 148 + 8 * j);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t lo = w[i] & 0x0F0F0F0Fu, hi = (w[i] >> 4) & 0x0F0F0F0Fu;        // weights 0 2 4 6 / 1 3 5 7
+                if constexpr (FMT == kFmtW5SB32) {
+                    const uint32_t pb = pl[0] >> (8 * i);                                 // bit k of weight k to bit 4 of its byte
+                    lo |= ((pb & 0x55u) * 0x00410410u) & 0x10101010u;
+                    hi |= (((pb >> 1) & 0x55u) * 0x00410410u) & 0x10101010u;
+                } else if constexpr (FMT == kFmtW6SB32) {
+                    const uint32_t pb = (pl[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+                    const uint32_t e = pb & 0x3333u, f = (pb >> 2) & 0x3333u;
+                    lo |= prmt(e << 4, e, 0x5140u) & 0x30303030u;
+                    hi |= prmt(f << 4, f, 0x5140u) & 0x30303030u;
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float a = __uint_as_float(prmt(lo, kW4Magic, 0x7044u + 0x100u * q));   // 128 + u
+                    const float b = __uint_as_float(prmt(hi, kW4Magic, 0x7044u + 0x100u * q));
+                    o[16 * gl + 4 * i + q] = half2_bits(__fmaf_rn(a, S, c), __fmaf_rn(b, S, c));
+                }
+            }
+        }
+    }
+}
+
+// Scale words of the row's atom (64 weights from K 64 a on).
+template <int FMT>
+__device__ __forceinline__ void atom_scales(const uint8_t* row, int a, int K, uint32_t (&sc)[2]) {
+    sc[0] = sc[1] = 0u;
+    if constexpr (!is_sb(FMT)) {
+        if (64 * a >= K) return;
+        if constexpr (sym_group(FMT) == 16) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + 8 * a));
+            sc[0] = v.x;
+            sc[1] = v.y;
+        } else {
+            sc[0] = __ldg(reinterpret_cast<const uint16_t*>(row) + a);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- product
+template <int FMT, int MC>
+__global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_constant__ WideParams p) {
+    using G = Wide<FMT>;
+    constexpr int NA = (512 - MC) / 32 / 4 * 4 > 12 ? 12 : (512 - MC) / 32 / 4 * 4;   // A slots, 32 columns each, after the sums
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int NX = p.xslots;
+    uint8_t* at = smem + kCodeSlots * G::CB + (size_t)NX * MC * 128;
+    WDesc* desc = reinterpret_cast<WDesc*>(at);
+    at += kDescs * sizeof(WDesc);
+    uint64_t* cfull = reinterpret_cast<uint64_t*>(at);
+    uint64_t* cempty = cfull + kCodeSlots;
+    uint64_t* xfull = cempty + kCodeSlots;
+    uint64_t* xempty = xfull + kMaxX;
+    uint64_t* afull = xempty + kMaxX;
+    uint64_t* aempty = afull + 12;
+    uint64_t* ufull = aempty + 12;
+    uint64_t* dfull = ufull + kDescs;
+    uint64_t* dempty = dfull + 1;
+    uint64_t* mdone = dempty + 1;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(mdone + 1);
+    at += (2 * kCodeSlots + 2 * kMaxX + 24 + kDescs + 4) * 8;
+    WGroups g;
+    g.cost = reinterpret_cast<long long*>(at);
+    g.row = reinterpret_cast<int*>(g.cost + p.pl.E + 1);
+
+    if (tid == 0) {
+        for (int s = 0; s < kCodeSlots; ++s) {
+            mbar_init(&cfull[s], 1);
+            mbar_init(&cempty[s], kWorkers / kGroups * G::ATOMS);
+        }
+        for (int s = 0; s < NX; ++s) {
+            mbar_init(&xfull[s], 1);
+            mbar_init(&xempty[s], 1);
+        }
+        for (int s = 0; s < NA; ++s) {
+            mbar_init(&afull[s], kWorkers / kGroups);
+            mbar_init(&aempty[s], 1);
+        }
+        for (int s = 0; s < kDescs; ++s) mbar_init(&ufull[s], 1);
+        mbar_init(dfull, 1);
+        mbar_init(dempty, kWorkers);
+        mbar_init(mdone, 1);
+        fence_mbar_init();
+    }
+    if (warp == kWorkers) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(tslot)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (warp == kWorkers + 1) {
+        scan_wide(p.pl, g, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    grid_dep_launch();
+
+    const int T = p.pl.T;
+    const long long W = g.cost[p.pl.E];
+    const uint32_t cbase = smem_u32(smem), xbase = cbase + kCodeSlots * G::CB;
+    auto wait = [&](uint64_t* bar, int phase, unsigned flag) {
+        return __all_sync(~0u, mbar_try_wait(bar, (uint32_t)phase & 1u)) ||
+               __all_sync(~0u, mbar_wait_bounded(bar, (uint32_t)phase & 1u, flag, 0u, p.wait_ns));
+    };
+
+    if (warp == kWorkers + 1) {
+        // ------------------------------------------- work and tensor copies
+        if (lane == 0) {
+            const long long Gc = gridDim.x;
+            const long long P0 = ceil_div(blockIdx.x * W, Gc), P1 = ceil_div((blockIdx.x + 1) * W, Gc);
+            int u = 0, cs = 0, xs = 0, cwrap = 0, xwrap = 0, cissued = 0, xissued = 0;
+            bool ok = !(p.test_flags & kTestNoCopies), waited = false;
+            int e = 0, m = 0, rc = 0, chunks = 0;
+            long long w = 1, st = 0, stages = 0;         // expert e: cost of a stage, next stage, stages
+            auto enter = [&](int expert) {
+                e = expert;
+                m = g.row[e + 1] - g.row[e];
+                rc = chunk_rows(m, p.pl.MC);
+                chunks = (m + rc - 1) / rc;
+                w = stage_cost(rc);
+                stages = (g.cost[e + 1] - g.cost[e]) / w;
+            };
+            if (P0 < P1) {
+                enter(last_at_most(g.cost, p.pl.E, P0));
+                st = ceil_div(P0 - g.cost[e], w);
+            }
+            while (P0 < P1) {
+                while (st >= stages && e + 1 < p.pl.E) {             // to the next expert with rows
+                    enter(e + 1);
+                    st = 0;
+                }
+                const long long pos = g.cost[e] + st * w;
+                if (st >= stages || pos >= P1 || !ok) break;
+                const long long unit = st / T;
+                const int nt = (int)(unit / chunks), c = (int)(unit - (long long)nt * chunks);
+                WDesc d;
+                d.done = 0;
+                d.row0 = g.row[e] + c * rc;
+                d.rows = min(rc, m - c * rc);
+                d.n0 = nt * kTcRows;
+                d.wrow = e * p.pl.N + d.n0;
+                d.k0 = (int)(st - unit * T);
+                d.k1 = (int)min((long long)T, d.k0 + ceil_div(P1 - pos, w));
+                d.cost = (int)w;
+                d.pos = g.cost[e] + unit * T * w;
+                d.first = d.k0 > 0 ? (int)(d.pos * Gc / W) : (int)blockIdx.x;
+                d.last = d.k1 < T ? (int)((d.pos + (T - 1) * w) * Gc / W) : (int)blockIdx.x;
+                desc[u % kDescs] = d;
+                mbar_arrive(&ufull[u % kDescs]);
+                ++u;
+                if constexpr (!is_sb(FMT)) {             // the tile's scales into L2
+                    const unsigned long long b0 = (unsigned long long)d.wrow * p.srb & ~15ull;
+                    const unsigned long long b1 = (min((unsigned long long)d.wrow + kTcRows, p.total_rows) * p.srb + 15) & ~15ull;
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(p.scales + b0), "r"((uint32_t)(b1 - b0)) : "memory");
+                }
+                const int boxes = (((d.rows + 15) & ~15) + 31) / 32;
+                for (int k = d.k0; k < d.k1 && ok; ++k) {
+                    if (cwrap && !mbar_wait_bounded(&cempty[cs], (uint32_t)(cwrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&cfull[cs], (uint32_t)(kTcRows * G::RB));
+                    tma_2d(cbase + cs * G::CB, &p.cmap, k * G::RB, d.wrow, &cfull[cs]);
+                    ++cissued;
+                    if (++cs == kCodeSlots) { cs = 0; ++cwrap; }
+                    if (!waited) {
+                        grid_dep_wait();                 // the rows come from lay_rows_kernel
+                        asm volatile("fence.proxy.async.global;" ::: "memory");
+                        waited = true;
+                    }
+                    for (int a = 0; a < G::ATOMS; ++a) {
+                        if (xwrap && !mbar_wait_bounded(&xempty[xs], (uint32_t)(xwrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns)) { ok = false; break; }
+                        mbar_arrive_expect_tx(&xfull[xs], (uint32_t)boxes * 4096u);
+                        for (int b = 0; b < boxes; ++b)
+                            tma_3d(xbase + xs * (MC * 128) + b * 4096, &p.xmap, 0, d.row0 + 32 * b, k * G::ATOMS + a, &xfull[xs]);
+                        ++xissued;
+                        if (++xs == NX) { xs = 0; ++xwrap; }
+                    }
+                }
+                st = unit * T + d.k1;
+            }
+            if (!waited) grid_dep_wait();                // no kernel after this one runs beside lay_rows_kernel
+            if (ok || (p.test_flags & kTestNoCopies) == 0) {
+                desc[u % kDescs].done = 1;
+                mbar_arrive(&ufull[u % kDescs]);
+            }
+            // copies in flight (a warp gave up) land before the CTA leaves
+            for (int q = 0; q < kCodeSlots && q < cissued; ++q)
+                mbar_wait_bounded(&cfull[q], (uint32_t)(cissued / kCodeSlots + (q < cissued % kCodeSlots ? 1 : 0) - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
+            for (int q = 0; q < NX && q < xissued; ++q)
+                mbar_wait_bounded(&xfull[q], (uint32_t)(xissued / NX + (q < xissued % NX ? 1 : 0) - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
+        }
+        __syncwarp();
+    } else if (warp == kWorkers) {
+        // ------------------------------------------------------- MMA issue
+        int xs = 0, xwrap = 0, as = 0, awrap = 0;
+        bool ok = true;
+        for (int u = 0; ok; ++u) {
+            if (!wait(&ufull[u % kDescs], u / kDescs, kStatusTmaWait)) break;
+            const WDesc d = desc[u % kDescs];
+            if (d.done) break;
+            if (u && !wait(dempty, u - 1, kStatusMmaWait)) break;
+            tc_fence_after();
+            const int np = (d.rows + 15) & ~15;
+            const uint32_t idesc = (1u << 4) | ((uint32_t)(np >> 3) << 17) | ((uint32_t)(kTcRows >> 4) << 24);   // fp16, fp32 sums
+            const int n = (d.k1 - d.k0) * G::ATOMS;
+            for (int i = 0; i < n; ++i) {
+                if (!wait(&xfull[xs], xwrap, kStatusTmaWait) || !wait(&afull[as], awrap, kStatusTmaWait)) { ok = false; break; }
+                tc_fence_after();
+                mma_atom(tmem, tmem + MC + 32u * as, sw128_desc(xbase + xs * (MC * 128)), idesc, i ? 1u : 0u);
+                mma_commit(&xempty[xs]);
+                mma_commit(&aempty[as]);
+                if (++xs == NX) { xs = 0; ++xwrap; }
+                if (++as == NA) { as = 0; ++awrap; }
+            }
+            if (ok) mma_commit(dfull);
+        }
+        mma_commit(mdone);
+        wait(mdone, 0, kStatusMmaWait);                  // no MMA in flight at teardown
+    } else {
+        // ------------------------------------------- unpack, then the sums
+        const int q = warp & 3, gi = warp >> 2, r = 32 * q + lane;
+        const uint32_t tl = (uint32_t)(32 * q) << 16;
+        int i0 = 0, c0 = 0;                              // atoms and code slots before the current unit
+        bool waited = false;
+        for (int u = 0;; ++u) {
+            if (!wait(&ufull[u % kDescs], u / kDescs, kStatusTmaWait)) break;
+            const WDesc d = desc[u % kDescs];
+            if (d.done) break;
+            const int n = (d.k1 - d.k0) * G::ATOMS;
+            const uint8_t* srow = p.scales + min((unsigned long long)d.wrow + r, p.total_rows - 1) * p.srb;
+            int a = (gi - i0) & (kGroups - 1);
+            uint32_t sc[2], nx[2];
+            atom_scales<FMT>(srow, d.k0 * G::ATOMS + a, p.pl.K, nx);
+            bool ok = true;
+            for (; a < n; a += kGroups) {
+                sc[0] = nx[0];
+                sc[1] = nx[1];
+                if (a + kGroups < n) atom_scales<FMT>(srow, d.k0 * G::ATOMS + a + kGroups, p.pl.K, nx);
+                const int ai = i0 + a, as = ai % NA, use = ai / NA, ci = c0 + a / G::ATOMS;
+                if (!wait(&cfull[ci % kCodeSlots], ci / kCodeSlots, kStatusTmaWait)) { ok = false; break; }
+                uint32_t o[32];
+                unpack_atom<FMT>(cbase + (ci % kCodeSlots) * G::CB + r * G::RB, a % G::ATOMS, G::RB == 128 ? r & 7 : 0, sc, o);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cempty[ci % kCodeSlots]);
+                if (use && !wait(&aempty[as], use - 1, kStatusMmaWait)) { ok = false; break; }
+                tc_fence_after();
+                tmem_st32(tmem + tl + MC + 32u * as, o);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&afull[as]);
+            }
+            i0 += n;
+            c0 += d.k1 - d.k0;
+            if (!ok || !wait(dfull, u, kStatusMmaWait)) break;
+            tc_fence_after();
+            // sums: this warp's 32 weight rows, 16 activation rows at a time
+            const int blocks = (d.rows + 15) / 16;
+            const bool cut = d.first != d.last || d.k0 > 0 || d.k1 < T;
+            if (!waited) {
+                grid_dep_wait();                         // counters and powers of two come from lay_rows_kernel
+                waited = true;
+            }
+            constexpr size_t kPart = (size_t)MC * kTcRows;
+            bool store = true;
+            if (cut) {
+                float* mine = p.part + (2 * (size_t)blockIdx.x + (d.k0 == 0)) * kPart + r;
+                for (int b = gi; b < blocks; b += kGroups) {
+                    float v[16];
+                    tmem_ld16(tmem + tl + 16u * b, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) __stcg(mine + (size_t)(16 * b + j) * kTcRows, v[j]);
+                }
+                __threadfence();
+                __syncwarp();
+                unsigned old = 0;
+                if (lane == 0) old = atomicAdd(&p.count[d.first * kWorkers + warp], (unsigned)(d.k1 - d.k0));
+                old = __shfl_sync(~0u, old, 0);
+                store = old + (unsigned)(d.k1 - d.k0) == (unsigned)T;    // the last part: all stages are summed
+                if (store) __threadfence();
+            }
+            for (int b = gi; store && b < blocks; b += kGroups) {
+                float v[16];
+                if (!cut) {
+                    tmem_ld16(tmem + tl + 16u * b, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+                    for (int c = d.first; c <= d.last; ++c) {
+                        // CTA c's stages of the unit, if it has any
+                        const long long q0 = ceil_div((long long)c * W, gridDim.x) - d.pos, q1 = ceil_div(((long long)c + 1) * W, gridDim.x) - d.pos;
+                        const long long k0 = q0 <= 0 ? 0 : ceil_div(q0, d.cost), k1 = q1 <= 0 ? 0 : ceil_div(q1, d.cost);
+                        if (k0 >= k1 || k0 >= T) continue;
+                        const float* f = p.part + (2 * (size_t)c + (k0 == 0)) * kPart + r;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] += __ldcg(f + (size_t)(16 * b + j) * kTcRows);
+                    }
+                }
+                const int nn = d.n0 + r, N = p.pl.N;
+                int orow[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int i = 16 * b + j, m = d.row0 + i;
+                    orow[j] = i >= d.rows ? -1 : p.out_rows ? __ldg(p.out_rows + m) : m;
+                    const float sc1 = i < d.rows ? __ldcg(p.rscale + m) : 0.0f;
+                    v[j] *= sc1;
+                    if (p.act) {
+                        v[j] = v[j] > 0.0f || v[j] != v[j] ? v[j] : 0.0f;
+                        v[j] *= v[j];
+                    }
+                }
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y);
+                if ((N & 1) == 0) {
+                    // lanes in pairs: the even one stores columns n, n + 1 of row j, the odd one those of row j + 1
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float give = lane & 1 ? v[j] : v[j + 1];
+                        const float got = __shfl_xor_sync(~0u, give, 1);
+                        const __nv_bfloat162 h = lane & 1 ? __floats2bfloat162_rn(got, v[j + 1]) : __floats2bfloat162_rn(v[j], got);
+                        const int o = lane & 1 ? orow[j + 1] : orow[j];
+                        if (o >= 0 && o < p.Ty && nn < N)
+                            *reinterpret_cast<__nv_bfloat162*>(y + (size_t)o * N + (nn & ~1)) = h;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (orow[j] >= 0 && orow[j] < p.Ty && nn < N) y[(size_t)orow[j] * N + nn] = __float2bfloat16_rn(v[j]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dempty);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWorkers) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ host
+struct WLayout { size_t xg, rscale, part, count, total; };
+
+WLayout wide_layout(int R, int K, int MC) {
+    WLayout l;
+    l.xg = 0;
+    l.rscale = (size_t)R * K * 2;
+    l.part = l.rscale + round16((size_t)R * 4);
+    l.count = l.part + (size_t)2 * kWideMaxCtas * MC * kTcRows * 4;
+    l.total = l.count + kWideMaxCtas * kWorkers * 4;
+    return l;
+}
+
+// Activation rows of a unit at most.
+int wide_mc(int R, int E) { return (R + E - 1) / E > 128 ? 256 : 128; }
+
+template <int FMT, int MC>
+cudaError_t launch_wide_mc(const RowsArgs& a, WideParams& p, cudaStream_t st) {
+    using G = Wide<FMT>;
+    const size_t fixed = kCodeSlots * G::CB + kDescs * sizeof(WDesc) + (2 * kCodeSlots + 2 * kMaxX + 24 + kDescs + 4) * 8 + wgroups_bytes(a.E);
+    p.xslots = (int)((kWideSmem - fixed) / (MC * 128));
+    if (p.xslots > kMaxX) p.xslots = kMaxX;
+    if (p.xslots < 2) return cudaErrorInvalidValue;
+    auto kern = wide_kernel<FMT, MC>;
+    static unsigned long long attr_done = 0ull;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWideSmem);
+        if (e != cudaSuccess) return e;
+        __atomic_fetch_or(&attr_done, bit, __ATOMIC_RELEASE);
+    }
+    const int sms = sm_count();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms < kWideMaxCtas ? sms : kWideMaxCtas));
+    cfg.blockDim = dim3(kWideThreads);
+    cfg.dynamicSmemBytes = fixed + (size_t)p.xslots * MC * 128;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int FMT>
+cudaError_t launch_wide_fmt(const RowsArgs& a, cudaStream_t st) {
+    using G = Wide<FMT>;
+    const EncodeTiled enc = encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const int MC = wide_mc(a.R, a.E);
+    const WLayout l = wide_layout(a.R, a.K, MC);
+    uint8_t* ws = static_cast<uint8_t*>(a.ws);
+    unsigned* count = reinterpret_cast<unsigned*>(ws + l.count);
+    float* rscale = reinterpret_cast<float*>(ws + l.rscale);
+
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.R + kLayThreads / 32 - 1) / (kLayThreads / 32)));
+    cfg.blockDim = dim3(kLayThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, lay_rows_kernel<G::ORDER>, static_cast<const __nv_bfloat16*>(a.x), a.in_rows, a.T, a.R, a.K,
+                                       reinterpret_cast<uint4*>(ws + l.xg), rscale, count, kWideMaxCtas * kWorkers);
+    if (e != cudaSuccess) return e;
+
+    WideParams p = {};
+    const uint64_t crb = code_row_bytes(FMT, a.K), rows = (uint64_t)a.E * a.N;
+    const cuuint64_t cd[2] = {crb, rows}, cst[1] = {crb};
+    const cuuint32_t cb[2] = {(cuuint32_t)G::RB, (cuuint32_t)kTcRows}, ones[3] = {1, 1, 1};
+    const cuuint64_t xd[3] = {64, (cuuint64_t)a.R, (cuuint64_t)(a.K / 64)}, xst[2] = {(cuuint64_t)a.K * 2, 128};
+    const cuuint32_t xb[3] = {64, 32, 1};
+    if (enc(&p.cmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(a.codes), cd, cst, cb, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            G::RB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        enc(&p.xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, ws + l.xg, xd, xst, xb, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    p.pl = {a.offsets, a.E, a.R, a.N, a.K, (a.K + G::KS - 1) / G::KS, MC};
+    p.scales = static_cast<const uint8_t*>(a.scales);
+    p.total_rows = rows;
+    p.srb = (uint32_t)scale_row_bytes(FMT, a.K);
+    p.rscale = rscale;
+    p.part = reinterpret_cast<float*>(ws + l.part);
+    p.count = count;
+    p.out_rows = a.out_rows;
+    p.y = a.y;
+    p.Ty = a.Ty;
+    p.act = a.act;
+    p.wait_ns = wait_limit_ns();
+    p.test_flags = test_flags();
+    return MC == 256 ? launch_wide_mc<FMT, 256>(a, p, st) : launch_wide_mc<FMT, 128>(a, p, st);
+}
+
+}  // namespace
+
+size_t wide_workspace(int R, int K, int E) { return wide_layout(R, K, wide_mc(R, E)).total; }
+
+cudaError_t launch_wide(const RowsArgs& a, cudaStream_t st) {
+    switch (a.fmt) {
+        case kFmtW4G64: return launch_wide_fmt<kFmtW4G64>(a, st);
+        case kFmtW8G16: return launch_wide_fmt<kFmtW8G16>(a, st);
+        case kFmtW8G64: return launch_wide_fmt<kFmtW8G64>(a, st);
+        case kFmtW6G16: return launch_wide_fmt<kFmtW6G16>(a, st);
+        case kFmtW4SB32: return launch_wide_fmt<kFmtW4SB32>(a, st);
+        case kFmtW5SB32: return launch_wide_fmt<kFmtW5SB32>(a, st);
+        default: return launch_wide_fmt<kFmtW6SB32>(a, st);
+    }
+}
+
+cudaError_t status_wide(cudaStream_t st, unsigned* word) {
+    unsigned v = 0, z = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_status, &z, sizeof(z), 0, cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    *word = v;
+    return e;
+}
+
+}  // namespace rq
