@@ -22,7 +22,7 @@
 //     CTA (one per SM) has the same; a cut unit's parts are summed through the
 //     workspace in K order by whichever CTA arrives last.
 // Roles: 16 unpacking warps (they also move the sums out), one warp that
-// issues the MMAs, one thread that issues the tensor copies.
+// issues the MMAs, one thread that copies codes and one that copies rows.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -38,12 +38,14 @@ namespace {
 
 constexpr int kWorkers = 16;
 constexpr int kGroups = 4;              // warps 4 g .. 4 g + 3 take atoms g, g + 4, ...
-constexpr int kWideThreads = 32 * (kWorkers + 2);
+constexpr int kWideThreads = 32 * (kWorkers + 3);
 constexpr int kMaxX = 8;                // activation slots at most
-constexpr int kCodeSlots = 2;           // even: a slot's stages always go to the same warps
+// Code slots: an even number, so that a slot's stages always go to the same warps.
+__host__ __device__ constexpr int code_slots(int mc) { return mc == 256 ? 2 : 4; }
 constexpr int kDescs = 8;
 constexpr size_t kWideSmem = 226 * 1024;
 constexpr int kWideMaxCtas = 256;
+constexpr int kBarBytes = (2 * 4 + 2 * kMaxX + 2 * 4 + kDescs + 2 * 2 + 2) * 8;
 
 template <int FMT>
 struct Wide {
@@ -179,16 +181,6 @@ __device__ __forceinline__ void scan_wide(const WidePlan& pl, WGroups g, int lan
     __syncwarp();
 }
 
-__device__ __forceinline__ int last_at_most(const long long* a, int E, long long v) {
-    int lo = 0, hi = E - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a[mid] <= v) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
 // A stretch of a unit in one CTA.
 struct __align__(16) WDesc {
     int done;          // no more work
@@ -201,6 +193,65 @@ struct __align__(16) WDesc {
 };
 
 __device__ __forceinline__ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// Walks a CTA's stretches: cost positions [ceil(b W / G), ceil((b + 1) W / G)).
+struct Walk {
+    const WidePlan& pl;
+    const WGroups& g;
+    long long W, Gc, P1, w, st, stages;                  // w: cost of a stage of expert e, st: its next stage
+    int e, m, rc, chunks;
+    bool live;
+
+    __device__ __forceinline__ Walk(const WidePlan& plan, const WGroups& groups) : pl(plan), g(groups) {
+        W = g.cost[pl.E];
+        Gc = gridDim.x;
+        const long long P0 = ceil_div(blockIdx.x * W, Gc);
+        P1 = ceil_div((blockIdx.x + 1) * W, Gc);
+        live = P0 < P1;
+        if (!live) return;
+        int lo = 0, hi = pl.E - 1;                       // last expert whose first position is at most P0
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (g.cost[mid] <= P0) lo = mid;
+            else hi = mid - 1;
+        }
+        enter(lo);
+        st = ceil_div(P0 - g.cost[e], w);
+    }
+    __device__ __forceinline__ void enter(int expert) {
+        e = expert;
+        m = g.row[e + 1] - g.row[e];
+        rc = chunk_rows(m, pl.MC);
+        chunks = (m + rc - 1) / rc;
+        w = stage_cost(rc);
+        stages = (g.cost[e + 1] - g.cost[e]) / w;
+    }
+    __device__ __forceinline__ bool next(WDesc& d) {
+        if (!live) return false;
+        while (st >= stages && e + 1 < pl.E) {           // to the next expert with rows
+            enter(e + 1);
+            st = 0;
+        }
+        const long long pos = g.cost[e] + st * w;
+        if (st >= stages || pos >= P1) return live = false;
+        const int T = pl.T;
+        const long long unit = st / T;
+        const int nt = (int)(unit / chunks), c = (int)(unit - (long long)nt * chunks);
+        d.done = 0;
+        d.row0 = g.row[e] + c * rc;
+        d.rows = min(rc, m - c * rc);
+        d.n0 = nt * kTcRows;
+        d.wrow = e * pl.N + d.n0;
+        d.k0 = (int)(st - unit * T);
+        d.k1 = (int)min((long long)T, d.k0 + ceil_div(P1 - pos, w));
+        d.cost = (int)w;
+        d.pos = g.cost[e] + unit * T * w;
+        d.first = d.k0 > 0 ? (int)(d.pos * Gc / W) : (int)blockIdx.x;
+        d.last = d.k1 < T ? (int)((d.pos + (T - 1) * w) * Gc / W) : (int)blockIdx.x;
+        st = unit * T + d.k1;
+        return true;
+    }
+};
 
 // ------------------------------------------------------------------ unpack
 __device__ __forceinline__ uint32_t h2(uint16_t v) { return (uint32_t)v * 0x10001u; }
@@ -321,25 +372,30 @@ __device__ __forceinline__ void atom_scales(const uint8_t* row, int a, int K, ui
 template <int FMT, int MC>
 __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_constant__ WideParams p) {
     using G = Wide<FMT>;
-    constexpr int NA = (512 - MC) / 32 / 4 * 4 > 12 ? 12 : (512 - MC) / 32 / 4 * 4;   // A slots, 32 columns each, after the sums
+    constexpr int ND = MC == 256 ? 1 : 2;                                // buffers of sums
+    constexpr uint32_t A0 = ND * MC;                                     // A slots of 128 K (64 columns) behind them
+    constexpr int NA = (512 - (int)A0) / 64;                             // 4: even, as the code slots
+    constexpr int kCodeSlots = code_slots(MC);
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int NX = p.xslots;
     uint8_t* at = smem + kCodeSlots * G::CB + (size_t)NX * MC * 128;
     WDesc* desc = reinterpret_cast<WDesc*>(at);
     at += kDescs * sizeof(WDesc);
+    float2* rowinfo = reinterpret_cast<float2*>(at) + (warp & (kWorkers - 1)) * (MC / kGroups);   // (row of y, scale) per warp
+    at += kWorkers * (MC / kGroups) * 8;
     uint64_t* cfull = reinterpret_cast<uint64_t*>(at);
     uint64_t* cempty = cfull + kCodeSlots;
     uint64_t* xfull = cempty + kCodeSlots;
     uint64_t* xempty = xfull + kMaxX;
     uint64_t* afull = xempty + kMaxX;
-    uint64_t* aempty = afull + 12;
-    uint64_t* ufull = aempty + 12;
+    uint64_t* aempty = afull + NA;
+    uint64_t* ufull = aempty + NA;
     uint64_t* dfull = ufull + kDescs;
-    uint64_t* dempty = dfull + 1;
-    uint64_t* mdone = dempty + 1;
+    uint64_t* dempty = dfull + ND;
+    uint64_t* mdone = dempty + ND;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(mdone + 1);
-    at += (2 * kCodeSlots + 2 * kMaxX + 24 + kDescs + 4) * 8;
+    at += kBarBytes;
     WGroups g;
     g.cost = reinterpret_cast<long long*>(at);
     g.row = reinterpret_cast<int*>(g.cost + p.pl.E + 1);
@@ -354,12 +410,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             mbar_init(&xempty[s], 1);
         }
         for (int s = 0; s < NA; ++s) {
-            mbar_init(&afull[s], kWorkers / kGroups);
+            mbar_init(&afull[s], 2 * kWorkers / kGroups);
             mbar_init(&aempty[s], 1);
         }
         for (int s = 0; s < kDescs; ++s) mbar_init(&ufull[s], 1);
-        mbar_init(dfull, 1);
-        mbar_init(dempty, kWorkers);
+        for (int s = 0; s < ND; ++s) {
+            mbar_init(&dfull[s], 1);
+            mbar_init(&dempty[s], kWorkers);
+        }
         mbar_init(mdone, 1);
         fence_mbar_init();
     }
@@ -377,7 +435,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     grid_dep_launch();
 
     const int T = p.pl.T;
-    const long long W = g.cost[p.pl.E];
     const uint32_t cbase = smem_u32(smem), xbase = cbase + kCodeSlots * G::CB;
     auto wait = [&](uint64_t* bar, int phase, unsigned flag) {
         return __all_sync(~0u, mbar_try_wait(bar, (uint32_t)phase & 1u)) ||
@@ -385,88 +442,59 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     };
 
     if (warp == kWorkers + 1) {
-        // ------------------------------------------- work and tensor copies
+        // ------------------------------------------------ work and its rows
         if (lane == 0) {
-            const long long Gc = gridDim.x;
-            const long long P0 = ceil_div(blockIdx.x * W, Gc), P1 = ceil_div((blockIdx.x + 1) * W, Gc);
-            int u = 0, cs = 0, xs = 0, cwrap = 0, xwrap = 0, cissued = 0, xissued = 0;
-            bool ok = !(p.test_flags & kTestNoCopies), waited = false;
-            int e = 0, m = 0, rc = 0, chunks = 0;
-            long long w = 1, st = 0, stages = 0;         // expert e: cost of a stage, next stage, stages
-            auto enter = [&](int expert) {
-                e = expert;
-                m = g.row[e + 1] - g.row[e];
-                rc = chunk_rows(m, p.pl.MC);
-                chunks = (m + rc - 1) / rc;
-                w = stage_cost(rc);
-                stages = (g.cost[e + 1] - g.cost[e]) / w;
-            };
-            if (P0 < P1) {
-                enter(last_at_most(g.cost, p.pl.E, P0));
-                st = ceil_div(P0 - g.cost[e], w);
-            }
-            while (P0 < P1) {
-                while (st >= stages && e + 1 < p.pl.E) {             // to the next expert with rows
-                    enter(e + 1);
-                    st = 0;
-                }
-                const long long pos = g.cost[e] + st * w;
-                if (st >= stages || pos >= P1 || !ok) break;
-                const long long unit = st / T;
-                const int nt = (int)(unit / chunks), c = (int)(unit - (long long)nt * chunks);
-                WDesc d;
-                d.done = 0;
-                d.row0 = g.row[e] + c * rc;
-                d.rows = min(rc, m - c * rc);
-                d.n0 = nt * kTcRows;
-                d.wrow = e * p.pl.N + d.n0;
-                d.k0 = (int)(st - unit * T);
-                d.k1 = (int)min((long long)T, d.k0 + ceil_div(P1 - pos, w));
-                d.cost = (int)w;
-                d.pos = g.cost[e] + unit * T * w;
-                d.first = d.k0 > 0 ? (int)(d.pos * Gc / W) : (int)blockIdx.x;
-                d.last = d.k1 < T ? (int)((d.pos + (T - 1) * w) * Gc / W) : (int)blockIdx.x;
+            grid_dep_wait();                             // the rows come from lay_rows_kernel
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            Walk walk(p.pl, g);
+            WDesc d;
+            int u = 0, xs = 0, xwrap = 0, issued = 0;
+            bool ok = !(p.test_flags & kTestNoCopies);
+            for (; ok && walk.next(d); ++u) {
                 desc[u % kDescs] = d;
                 mbar_arrive(&ufull[u % kDescs]);
-                ++u;
+                const int boxes = (((d.rows + 15) & ~15) + 31) / 32;
+                for (int a = d.k0 * G::ATOMS; ok && a < d.k1 * G::ATOMS; ++a) {
+                    if (xwrap && !mbar_wait_bounded(&xempty[xs], (uint32_t)(xwrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&xfull[xs], (uint32_t)boxes * 4096u);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_3d(xbase + xs * (MC * 128) + b * 4096, &p.xmap, 0, d.row0 + 32 * b, a, &xfull[xs]);
+                    ++issued;
+                    if (++xs == NX) { xs = 0; ++xwrap; }
+                }
+            }
+            if (!(p.test_flags & kTestNoCopies)) {
+                desc[u % kDescs].done = 1;
+                mbar_arrive(&ufull[u % kDescs]);
+            }
+            // copies in flight (a warp gave up) land before the CTA leaves
+            for (int q = 0; q < NX && q < issued; ++q)
+                mbar_wait_bounded(&xfull[q], (uint32_t)(issued / NX + (q < issued % NX ? 1 : 0) - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
+        }
+        __syncwarp();
+    } else if (warp == kWorkers + 2) {
+        // ------------------------------------------------------------ codes
+        if (lane == 0 && !(p.test_flags & kTestNoCopies)) {
+            Walk walk(p.pl, g);
+            WDesc d;
+            int cs = 0, cwrap = 0, issued = 0;
+            bool ok = true;
+            while (ok && walk.next(d)) {
                 if constexpr (!is_sb(FMT)) {             // the tile's scales into L2
                     const unsigned long long b0 = (unsigned long long)d.wrow * p.srb & ~15ull;
                     const unsigned long long b1 = (min((unsigned long long)d.wrow + kTcRows, p.total_rows) * p.srb + 15) & ~15ull;
                     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(p.scales + b0), "r"((uint32_t)(b1 - b0)) : "memory");
                 }
-                const int boxes = (((d.rows + 15) & ~15) + 31) / 32;
-                for (int k = d.k0; k < d.k1 && ok; ++k) {
+                for (int k = d.k0; k < d.k1; ++k) {
                     if (cwrap && !mbar_wait_bounded(&cempty[cs], (uint32_t)(cwrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns)) { ok = false; break; }
                     mbar_arrive_expect_tx(&cfull[cs], (uint32_t)(kTcRows * G::RB));
                     tma_2d(cbase + cs * G::CB, &p.cmap, k * G::RB, d.wrow, &cfull[cs]);
-                    ++cissued;
+                    ++issued;
                     if (++cs == kCodeSlots) { cs = 0; ++cwrap; }
-                    if (!waited) {
-                        grid_dep_wait();                 // the rows come from lay_rows_kernel
-                        asm volatile("fence.proxy.async.global;" ::: "memory");
-                        waited = true;
-                    }
-                    for (int a = 0; a < G::ATOMS; ++a) {
-                        if (xwrap && !mbar_wait_bounded(&xempty[xs], (uint32_t)(xwrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns)) { ok = false; break; }
-                        mbar_arrive_expect_tx(&xfull[xs], (uint32_t)boxes * 4096u);
-                        for (int b = 0; b < boxes; ++b)
-                            tma_3d(xbase + xs * (MC * 128) + b * 4096, &p.xmap, 0, d.row0 + 32 * b, k * G::ATOMS + a, &xfull[xs]);
-                        ++xissued;
-                        if (++xs == NX) { xs = 0; ++xwrap; }
-                    }
                 }
-                st = unit * T + d.k1;
             }
-            if (!waited) grid_dep_wait();                // no kernel after this one runs beside lay_rows_kernel
-            if (ok || (p.test_flags & kTestNoCopies) == 0) {
-                desc[u % kDescs].done = 1;
-                mbar_arrive(&ufull[u % kDescs]);
-            }
-            // copies in flight (a warp gave up) land before the CTA leaves
-            for (int q = 0; q < kCodeSlots && q < cissued; ++q)
-                mbar_wait_bounded(&cfull[q], (uint32_t)(cissued / kCodeSlots + (q < cissued % kCodeSlots ? 1 : 0) - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
-            for (int q = 0; q < NX && q < xissued; ++q)
-                mbar_wait_bounded(&xfull[q], (uint32_t)(xissued / NX + (q < xissued % NX ? 1 : 0) - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
+            for (int q = 0; q < kCodeSlots && q < issued; ++q)
+                mbar_wait_bounded(&cfull[q], (uint32_t)(issued / kCodeSlots + (q < issued % kCodeSlots ? 1 : 0) - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
         }
         __syncwarp();
     } else if (warp == kWorkers) {
@@ -477,21 +505,26 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             if (!wait(&ufull[u % kDescs], u / kDescs, kStatusTmaWait)) break;
             const WDesc d = desc[u % kDescs];
             if (d.done) break;
-            if (u && !wait(dempty, u - 1, kStatusMmaWait)) break;
+            const int db = u % ND;
+            if (u >= ND && !wait(&dempty[db], u / ND - 1, kStatusMmaWait)) break;
             tc_fence_after();
             const int np = (d.rows + 15) & ~15;
             const uint32_t idesc = (1u << 4) | ((uint32_t)(np >> 3) << 17) | ((uint32_t)(kTcRows >> 4) << 24);   // fp16, fp32 sums
-            const int n = (d.k1 - d.k0) * G::ATOMS;
-            for (int i = 0; i < n; ++i) {
-                if (!wait(&xfull[xs], xwrap, kStatusTmaWait) || !wait(&afull[as], awrap, kStatusTmaWait)) { ok = false; break; }
-                tc_fence_after();
-                mma_atom(tmem, tmem + MC + 32u * as, sw128_desc(xbase + xs * (MC * 128)), idesc, i ? 1u : 0u);
-                mma_commit(&xempty[xs]);
+            const int n = (d.k1 - d.k0) * (G::ATOMS / 2);
+            for (int i = 0; ok && i < n; ++i) {
+                if (!wait(&afull[as], awrap, kStatusTmaWait)) { ok = false; break; }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!wait(&xfull[xs], xwrap, kStatusTmaWait)) { ok = false; break; }
+                    tc_fence_after();
+                    mma_atom(tmem + db * MC, tmem + A0 + 64u * as + 32u * h, sw128_desc(xbase + xs * (MC * 128)), idesc, (i | h) ? 1u : 0u);
+                    mma_commit(&xempty[xs]);
+                    if (++xs == NX) { xs = 0; ++xwrap; }
+                }
                 mma_commit(&aempty[as]);
-                if (++xs == NX) { xs = 0; ++xwrap; }
                 if (++as == NA) { as = 0; ++awrap; }
             }
-            if (ok) mma_commit(dfull);
+            if (ok) mma_commit(&dfull[db]);
         }
         mma_commit(mdone);
         wait(mdone, 0, kStatusMmaWait);                  // no MMA in flight at teardown
@@ -501,6 +534,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
         const uint32_t tl = (uint32_t)(32 * q) << 16;
         int i0 = 0, c0 = 0;                              // atoms and code slots before the current unit
         bool waited = false;
+        const long long W = g.cost[p.pl.E];
         for (int u = 0;; ++u) {
             if (!wait(&ufull[u % kDescs], u / kDescs, kStatusTmaWait)) break;
             const WDesc d = desc[u % kDescs];
@@ -515,7 +549,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                 sc[0] = nx[0];
                 sc[1] = nx[1];
                 if (a + kGroups < n) atom_scales<FMT>(srow, d.k0 * G::ATOMS + a + kGroups, p.pl.K, nx);
-                const int ai = i0 + a, as = ai % NA, use = ai / NA, ci = c0 + a / G::ATOMS;
+                const int ai = i0 + a, as = (ai >> 1) % NA, use = (ai >> 1) / NA, ci = c0 + a / G::ATOMS;
                 if (!wait(&cfull[ci % kCodeSlots], ci / kCodeSlots, kStatusTmaWait)) { ok = false; break; }
                 uint32_t o[32];
                 unpack_atom<FMT>(cbase + (ci % kCodeSlots) * G::CB + r * G::RB, a % G::ATOMS, G::RB == 128 ? r & 7 : 0, sc, o);
@@ -523,7 +557,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                 if (lane == 0) mbar_arrive(&cempty[ci % kCodeSlots]);
                 if (use && !wait(&aempty[as], use - 1, kStatusMmaWait)) { ok = false; break; }
                 tc_fence_after();
-                tmem_st32(tmem + tl + MC + 32u * as, o);
+                tmem_st32(tmem + tl + A0 + 64u * as + 32u * (ai & 1), o);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -531,22 +565,38 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             }
             i0 += n;
             c0 += d.k1 - d.k0;
-            if (!ok || !wait(dfull, u, kStatusMmaWait)) break;
-            tc_fence_after();
-            // sums: this warp's 32 weight rows, 16 activation rows at a time
-            const int blocks = (d.rows + 15) / 16;
-            const bool cut = d.first != d.last || d.k0 > 0 || d.k1 < T;
+            if (!ok) break;
             if (!waited) {
                 grid_dep_wait();                         // counters and powers of two come from lay_rows_kernel
                 waited = true;
             }
+            // this warp's activation rows, 16 of every 64: row of y (negative: none) and scale
+            const int blocks = (d.rows + 15) / 16;
+            for (int b = gi, x = 0; b < blocks; b += 2 * kGroups, x += 32) {
+                const int i = 16 * (b + (lane >> 4) * kGroups) + (lane & 15), m = d.row0 + i;
+                int o = -1;
+                float f = 0.0f;
+                if (i < d.rows) {
+                    o = p.out_rows ? __ldg(p.out_rows + m) : m;
+                    if (o >= p.Ty) o = -1;
+                    f = __ldcg(p.rscale + m);
+                }
+                if (x + lane < MC / kGroups) rowinfo[x + lane] = make_float2(__int_as_float(o), f);
+            }
+            __syncwarp();
+            const int db = u % ND;
+            if (!wait(&dfull[db], u / ND, kStatusMmaWait)) break;
+            tc_fence_after();
+            // sums: this warp's 32 weight rows, 16 activation rows at a time
+            const uint32_t dcol = tmem + tl + db * MC;
+            const bool cut = d.first != d.last || d.k0 > 0 || d.k1 < T;
             constexpr size_t kPart = (size_t)MC * kTcRows;
             bool store = true;
             if (cut) {
                 float* mine = p.part + (2 * (size_t)blockIdx.x + (d.k0 == 0)) * kPart + r;
                 for (int b = gi; b < blocks; b += kGroups) {
                     float v[16];
-                    tmem_ld16(tmem + tl + 16u * b, v);
+                    tmem_ld16(dcol + 16u * b, v);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) __stcg(mine + (size_t)(16 * b + j) * kTcRows, v[j]);
                 }
@@ -561,7 +611,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             for (int b = gi; store && b < blocks; b += kGroups) {
                 float v[16];
                 if (!cut) {
-                    tmem_ld16(tmem + tl + 16u * b, v);
+                    tmem_ld16(dcol + 16u * b, v);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] = 0.0f;
@@ -577,13 +627,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                 }
                 const int nn = d.n0 + r, N = p.pl.N;
                 int orow[16];
+                const float4* info = reinterpret_cast<const float4*>(rowinfo + (b / kGroups) * 16);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int i = 16 * b + j, m = d.row0 + i;
-                    orow[j] = i >= d.rows ? -1 : p.out_rows ? __ldg(p.out_rows + m) : m;
-                    const float sc1 = i < d.rows ? __ldcg(p.rscale + m) : 0.0f;
-                    v[j] *= sc1;
-                    if (p.act) {
+                for (int j = 0; j < 16; j += 2) {
+                    const float4 f = info[j / 2];
+                    orow[j] = __float_as_int(f.x);
+                    orow[j + 1] = __float_as_int(f.z);
+                    v[j] *= f.y;
+                    v[j + 1] *= f.w;
+                }
+                if (p.act) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
                         v[j] = v[j] > 0.0f || v[j] != v[j] ? v[j] : 0.0f;
                         v[j] *= v[j];
                     }
@@ -597,18 +652,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                         const float got = __shfl_xor_sync(~0u, give, 1);
                         const __nv_bfloat162 h = lane & 1 ? __floats2bfloat162_rn(got, v[j + 1]) : __floats2bfloat162_rn(v[j], got);
                         const int o = lane & 1 ? orow[j + 1] : orow[j];
-                        if (o >= 0 && o < p.Ty && nn < N)
+                        if (o >= 0 && nn < N)
                             *reinterpret_cast<__nv_bfloat162*>(y + (size_t)o * N + (nn & ~1)) = h;
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        if (orow[j] >= 0 && orow[j] < p.Ty && nn < N) y[(size_t)orow[j] * N + nn] = __float2bfloat16_rn(v[j]);
+                        if (orow[j] >= 0 && nn < N) y[(size_t)orow[j] * N + nn] = __float2bfloat16_rn(v[j]);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(dempty);
+            if (lane == 0) mbar_arrive(&dempty[db]);
         }
     }
     __syncwarp();
@@ -639,7 +694,7 @@ int wide_mc(int R, int E) { return (R + E - 1) / E > 128 ? 256 : 128; }
 template <int FMT, int MC>
 cudaError_t launch_wide_mc(const RowsArgs& a, WideParams& p, cudaStream_t st) {
     using G = Wide<FMT>;
-    const size_t fixed = kCodeSlots * G::CB + kDescs * sizeof(WDesc) + (2 * kCodeSlots + 2 * kMaxX + 24 + kDescs + 4) * 8 + wgroups_bytes(a.E);
+    const size_t fixed = code_slots(MC) * G::CB + kDescs * sizeof(WDesc) + kWorkers * (MC / kGroups) * 8 + kBarBytes + wgroups_bytes(a.E);
     p.xslots = (int)((kWideSmem - fixed) / (MC * 128));
     if (p.xslots > kMaxX) p.xslots = kMaxX;
     if (p.xslots < 2) return cudaErrorInvalidValue;
