@@ -5,19 +5,18 @@
 // two per row (the largest value in [2^14, 2^15); bf16 values are exact there
 // down to 2^-31 of the row's largest), in the order in which the codes unpack.
 // wide_kernel multiplies:
-//   * A unit is 128 weight rows x K x up to MC activation rows of one expert.
-//     tcgen05.mma takes the weights from tensor memory (A) and the activations
-//     from shared memory (B); the fp32 sums stay in tensor memory until the
-//     unit's end.
-//   * Sixteen warps unpack: a thread owns one weight row of the tile (its
-//     tensor-memory lane) and 64 weights of every fourth 64-K atom. A weight is
-//     q s (or S u - M) rounded once to fp16 (2^-12 relative, an eighth of the
-//     result's own rounding to bf16); fp16 instead of bf16 for both operands
-//     buys that. |w_hat| above 65504 overflows.
-//   * Bound by arithmetic where groups are long: per 64-K atom the tensor
-//     cores need 2 MC cycles, the unpacking about 110 issue slots per warp
-//     scheduler, and shared memory is filled with 128 MC bytes of activations
-//     and 128 rows of codes.
+//   * A unit is 256 weight rows x K x up to MC activation rows of one expert:
+//     two tiles of 128 weight rows that share the activations. tcgen05.mma takes
+//     the weights from tensor memory (A) and the activations from shared memory
+//     (B); the fp32 sums stay in tensor memory until the unit's end. Two tiles
+//     of weights and 128 rows beat one tile and 256 rows (the same sums): the
+//     weights are the narrow operand, so a CTA fetches 24 instead of 36 KB per
+//     64 K, and it was the fetching that bound it.
+//   * Sixteen warps unpack: a thread owns one weight row of a tile (its
+//     tensor-memory lane) and half of its K. A weight is q s (or S u - M)
+//     rounded once to fp16 (2^-12 relative, an eighth of the result's own
+//     rounding to bf16); fp16 instead of bf16 for both operands buys that.
+//     |w_hat| above 65504 overflows.
 //   * Units are cut where an even share of the work (rows x K) ends, so every
 //     CTA (one per SM) has the same; a cut unit's parts are summed through the
 //     workspace in K order by whichever CTA arrives last.
@@ -37,22 +36,24 @@ namespace rq {
 namespace {
 
 constexpr int kWorkers = 16;
-constexpr int kGroups = 4;              // warps 4 g .. 4 g + 3 take atoms g, g + 4, ...
+constexpr int kTiles = 2;               // weight tiles of a unit; warps 8 t .. 8 t + 7 unpack tile t, four of them
+                                        // the first 64 of each 128 K, four the others
+constexpr int kUnitRows = kTiles * kTcRows;
 constexpr int kWideThreads = 32 * (kWorkers + 3);
-constexpr int kMaxX = 8;                // activation slots at most
-// Code slots: an even number, so that a slot's stages always go to the same warps.
-__host__ __device__ constexpr int code_slots(int mc) { return mc == 256 ? 2 : 4; }
+constexpr int kMaxX = 6;                // activation slots at most (128 K each)
+constexpr int kCodeSlots = 2;
 constexpr int kDescs = 8;
 constexpr size_t kWideSmem = 226 * 1024;
 constexpr int kWideMaxCtas = 256;
-constexpr int kBarBytes = (2 * 4 + 2 * kMaxX + 2 * 4 + kDescs + 2 * 2 + 2) * 8;
+constexpr int kA = 4;                   // A slots: 128 K of one tile, 64 columns
+constexpr int kBarBytes = (2 * kCodeSlots + 2 * kMaxX + 2 * kA + kDescs + 2 * 2 + 2) * 8;
 
 template <int FMT>
 struct Wide {
     static constexpr int KS = is_w8(FMT) || FMT == kFmtW6G16 ? 128 : 256;         // K per code slot
     static constexpr int RB = FMT == kFmtW4G64 || is_w8(FMT) ? 128 : FMT == kFmtW6G16 ? 96 : sb_record(FMT);
-    static constexpr int CB = (kTcRows * RB + 1023) & ~1023;
-    static constexpr int ATOMS = KS / 64;
+    static constexpr int CB = (kUnitRows * RB + 1023) & ~1023;
+    static constexpr int PAIRS = KS / 128;                                        // 128-K steps of a stage
     // order of a row's values within 8 (1: 0 4 1 5 2 6 3 7) or 4 (2: 0 2 1 3)
     static constexpr int ORDER = is_sb(FMT) ? 0 : is_w8(FMT) ? 2 : 1;
 };
@@ -63,7 +64,7 @@ struct WidePlan {
 };
 
 struct WideParams {
-    CUtensorMap cmap;                   // codes: uint8 [E N][row bytes], box [128][RB]
+    CUtensorMap cmap;                   // codes: uint8 [E N][row bytes], box [256][RB]
     CUtensorMap xmap;                   // rows: fp16 [R][K] viewed as [K / 64][R][64], box [1][32][64]
     WidePlan pl;
     const uint8_t* scales;
@@ -152,7 +153,7 @@ __device__ __forceinline__ int chunk_rows(int m, int MC) {
 __device__ __forceinline__ int stage_cost(int rows) { return max(rows, 96); }
 
 __device__ __forceinline__ void scan_wide(const WidePlan& pl, WGroups g, int lane) {
-    const int tiles_n = (pl.N + kTcRows - 1) / kTcRows;
+    const int tiles_n = (pl.N + kUnitRows - 1) / kUnitRows;
     int top = 0;
     long long base = 0;
     for (int e0 = 0; e0 <= pl.E; e0 += 32) {
@@ -240,7 +241,7 @@ struct Walk {
         d.done = 0;
         d.row0 = g.row[e] + c * rc;
         d.rows = min(rc, m - c * rc);
-        d.n0 = nt * kTcRows;
+        d.n0 = nt * kUnitRows;
         d.wrow = e * pl.N + d.n0;
         d.k0 = (int)(st - unit * T);
         d.k1 = (int)min((long long)T, d.k0 + ceil_div(P1 - pos, w));
@@ -372,25 +373,24 @@ __device__ __forceinline__ void atom_scales(const uint8_t* row, int a, int K, ui
 template <int FMT, int MC>
 __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_constant__ WideParams p) {
     using G = Wide<FMT>;
-    constexpr int ND = MC == 256 ? 1 : 2;                                // buffers of sums
-    constexpr uint32_t A0 = ND * MC;                                     // A slots of 128 K (64 columns) behind them
-    constexpr int NA = (512 - (int)A0) / 64;                             // 4: even, as the code slots
-    constexpr int kCodeSlots = code_slots(MC);
+    constexpr int ND = MC == 64 ? 2 : 1;                                 // buffers of sums
+    constexpr uint32_t A0 = ND * kTiles * MC;                            // the A slots lie behind them
+    static_assert(A0 + 64 * kA <= 512, "tensor memory");
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int NX = p.xslots;
-    uint8_t* at = smem + kCodeSlots * G::CB + (size_t)NX * MC * 128;
+    uint8_t* at = smem + kCodeSlots * G::CB + (size_t)NX * MC * 256;
     WDesc* desc = reinterpret_cast<WDesc*>(at);
     at += kDescs * sizeof(WDesc);
-    float2* rowinfo = reinterpret_cast<float2*>(at) + (warp & (kWorkers - 1)) * (MC / kGroups);   // (row of y, scale) per warp
-    at += kWorkers * (MC / kGroups) * 8;
+    float2* rowinfo = reinterpret_cast<float2*>(at) + (warp & (kWorkers - 1)) * (MC / 2);   // (row of y, scale) per warp
+    at += kWorkers * (MC / 2) * 8;
     uint64_t* cfull = reinterpret_cast<uint64_t*>(at);
     uint64_t* cempty = cfull + kCodeSlots;
     uint64_t* xfull = cempty + kCodeSlots;
     uint64_t* xempty = xfull + kMaxX;
     uint64_t* afull = xempty + kMaxX;
-    uint64_t* aempty = afull + NA;
-    uint64_t* ufull = aempty + NA;
+    uint64_t* aempty = afull + kA;
+    uint64_t* ufull = aempty + kA;
     uint64_t* dfull = ufull + kDescs;
     uint64_t* dempty = dfull + ND;
     uint64_t* mdone = dempty + ND;
@@ -403,14 +403,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     if (tid == 0) {
         for (int s = 0; s < kCodeSlots; ++s) {
             mbar_init(&cfull[s], 1);
-            mbar_init(&cempty[s], kWorkers / kGroups * G::ATOMS);
+            mbar_init(&cempty[s], kWorkers);
         }
         for (int s = 0; s < NX; ++s) {
             mbar_init(&xfull[s], 1);
             mbar_init(&xempty[s], 1);
         }
-        for (int s = 0; s < NA; ++s) {
-            mbar_init(&afull[s], 2 * kWorkers / kGroups);
+        for (int s = 0; s < kA; ++s) {
+            mbar_init(&afull[s], kWorkers / kTiles);
             mbar_init(&aempty[s], 1);
         }
         for (int s = 0; s < kDescs; ++s) mbar_init(&ufull[s], 1);
@@ -454,11 +454,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                 desc[u % kDescs] = d;
                 mbar_arrive(&ufull[u % kDescs]);
                 const int boxes = (((d.rows + 15) & ~15) + 31) / 32;
-                for (int a = d.k0 * G::ATOMS; ok && a < d.k1 * G::ATOMS; ++a) {
+                for (int a = d.k0 * G::PAIRS; ok && a < d.k1 * G::PAIRS; ++a) {
                     if (xwrap && !mbar_wait_bounded(&xempty[xs], (uint32_t)(xwrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&xfull[xs], (uint32_t)boxes * 4096u);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_3d(xbase + xs * (MC * 128) + b * 4096, &p.xmap, 0, d.row0 + 32 * b, a, &xfull[xs]);
+                    mbar_arrive_expect_tx(&xfull[xs], (uint32_t)boxes * 8192u);
+                    for (int h = 0; h < 2; ++h)
+                        for (int b = 0; b < boxes; ++b)
+                            tma_3d(xbase + xs * (MC * 256) + h * (MC * 128) + b * 4096, &p.xmap, 0, d.row0 + 32 * b, 2 * a + h, &xfull[xs]);
                     ++issued;
                     if (++xs == NX) { xs = 0; ++xwrap; }
                 }
@@ -482,12 +483,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             while (ok && walk.next(d)) {
                 if constexpr (!is_sb(FMT)) {             // the tile's scales into L2
                     const unsigned long long b0 = (unsigned long long)d.wrow * p.srb & ~15ull;
-                    const unsigned long long b1 = (min((unsigned long long)d.wrow + kTcRows, p.total_rows) * p.srb + 15) & ~15ull;
+                    const unsigned long long b1 = (min((unsigned long long)d.wrow + kUnitRows, p.total_rows) * p.srb + 15) & ~15ull;
                     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(p.scales + b0), "r"((uint32_t)(b1 - b0)) : "memory");
                 }
                 for (int k = d.k0; k < d.k1; ++k) {
                     if (cwrap && !mbar_wait_bounded(&cempty[cs], (uint32_t)(cwrap - 1) & 1u, kStatusSlotWait, 32u, p.wait_ns)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&cfull[cs], (uint32_t)(kTcRows * G::RB));
+                    mbar_arrive_expect_tx(&cfull[cs], (uint32_t)(kUnitRows * G::RB));
                     tma_2d(cbase + cs * G::CB, &p.cmap, k * G::RB, d.wrow, &cfull[cs]);
                     ++issued;
                     if (++cs == kCodeSlots) { cs = 0; ++cwrap; }
@@ -510,19 +511,22 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             tc_fence_after();
             const int np = (d.rows + 15) & ~15;
             const uint32_t idesc = (1u << 4) | ((uint32_t)(np >> 3) << 17) | ((uint32_t)(kTcRows >> 4) << 24);   // fp16, fp32 sums
-            const int n = (d.k1 - d.k0) * (G::ATOMS / 2);
+            const int n = (d.k1 - d.k0) * G::PAIRS;
             for (int i = 0; ok && i < n; ++i) {
-                if (!wait(&afull[as], awrap, kStatusTmaWait)) { ok = false; break; }
+                if (!wait(&xfull[xs], xwrap, kStatusTmaWait)) { ok = false; break; }
+                const uint64_t xd = sw128_desc(xbase + xs * (MC * 256));
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!wait(&xfull[xs], xwrap, kStatusTmaWait)) { ok = false; break; }
+                for (int t = 0; t < kTiles; ++t) {
+                    if (!wait(&afull[as], awrap, kStatusTmaWait)) { ok = false; break; }
                     tc_fence_after();
-                    mma_atom(tmem + db * MC, tmem + A0 + 64u * as + 32u * h, sw128_desc(xbase + xs * (MC * 128)), idesc, (i | h) ? 1u : 0u);
-                    mma_commit(&xempty[xs]);
-                    if (++xs == NX) { xs = 0; ++xwrap; }
+                    const uint32_t dc = tmem + (db * kTiles + t) * MC, ac = tmem + A0 + 64u * as;
+                    mma_atom(dc, ac, xd, idesc, i ? 1u : 0u);
+                    mma_atom(dc, ac + 32u, xd + (uint64_t)(MC * 128 >> 4), idesc, 1u);
+                    mma_commit(&aempty[as]);
+                    if (++as == kA) { as = 0; ++awrap; }
                 }
-                mma_commit(&aempty[as]);
-                if (++as == NA) { as = 0; ++awrap; }
+                mma_commit(&xempty[xs]);
+                if (++xs == NX) { xs = 0; ++xwrap; }
             }
             if (ok) mma_commit(&dfull[db]);
         }
@@ -530,50 +534,55 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
         wait(mdone, 0, kStatusMmaWait);                  // no MMA in flight at teardown
     } else {
         // ------------------------------------------- unpack, then the sums
-        const int q = warp & 3, gi = warp >> 2, r = 32 * q + lane;
+        const int q = warp & 3, tile = warp >> 3, h = (warp >> 2) & 1, r = 32 * q + lane, rr = kTcRows * tile + r;
         const uint32_t tl = (uint32_t)(32 * q) << 16;
-        int i0 = 0, c0 = 0;                              // atoms and code slots before the current unit
+        int cs = 0, cwrap = 0, as = tile, awrap = 0;     // this tile's A slots: tile, tile + 2
         bool waited = false;
         const long long W = g.cost[p.pl.E];
         for (int u = 0;; ++u) {
             if (!wait(&ufull[u % kDescs], u / kDescs, kStatusTmaWait)) break;
             const WDesc d = desc[u % kDescs];
             if (d.done) break;
-            const int n = (d.k1 - d.k0) * G::ATOMS;
-            const uint8_t* srow = p.scales + min((unsigned long long)d.wrow + r, p.total_rows - 1) * p.srb;
-            int a = (gi - i0) & (kGroups - 1);
+            const uint8_t* srow = p.scales + min((unsigned long long)d.wrow + rr, p.total_rows - 1) * p.srb;
             uint32_t sc[2], nx[2];
-            atom_scales<FMT>(srow, d.k0 * G::ATOMS + a, p.pl.K, nx);
+            const int a1 = d.k1 * 2 * G::PAIRS;
+            atom_scales<FMT>(srow, d.k0 * 2 * G::PAIRS + h, p.pl.K, nx);
             bool ok = true;
-            for (; a < n; a += kGroups) {
-                sc[0] = nx[0];
-                sc[1] = nx[1];
-                if (a + kGroups < n) atom_scales<FMT>(srow, d.k0 * G::ATOMS + a + kGroups, p.pl.K, nx);
-                const int ai = i0 + a, as = (ai >> 1) % NA, use = (ai >> 1) / NA, ci = c0 + a / G::ATOMS;
-                if (!wait(&cfull[ci % kCodeSlots], ci / kCodeSlots, kStatusTmaWait)) { ok = false; break; }
-                uint32_t o[32];
-                unpack_atom<FMT>(cbase + (ci % kCodeSlots) * G::CB + r * G::RB, a % G::ATOMS, G::RB == 128 ? r & 7 : 0, sc, o);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&cempty[ci % kCodeSlots]);
-                if (use && !wait(&aempty[as], use - 1, kStatusMmaWait)) { ok = false; break; }
-                tc_fence_after();
-                tmem_st32(tmem + tl + A0 + 64u * as + 32u * (ai & 1), o);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&afull[as]);
+            for (int k = d.k0; ok && k < d.k1; ++k) {
+                if (!wait(&cfull[cs], cwrap, kStatusTmaWait)) { ok = false; break; }
+#pragma unroll
+                for (int i = 0; i < G::PAIRS; ++i) {
+                    const int a = (k * G::PAIRS + i) * 2 + h;            // 64-K atom of the row
+                    sc[0] = nx[0];
+                    sc[1] = nx[1];
+                    if (a + 2 < a1) atom_scales<FMT>(srow, a + 2, p.pl.K, nx);
+                    uint32_t o[32];
+                    unpack_atom<FMT>(cbase + cs * G::CB + rr * G::RB, 2 * i + h, G::RB == 128 ? r & 7 : 0, sc, o);
+                    if (i == G::PAIRS - 1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&cempty[cs]);
+                    }
+                    if (awrap && !wait(&aempty[as], awrap - 1, kStatusMmaWait)) { ok = false; break; }
+                    tc_fence_after();
+                    tmem_st32(tmem + tl + A0 + 64u * as + 32u * h, o);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&afull[as]);
+                    as += kTiles;
+                    if (as >= kA) { as = tile; ++awrap; }
+                }
+                if (++cs == kCodeSlots) { cs = 0; ++cwrap; }
             }
-            i0 += n;
-            c0 += d.k1 - d.k0;
             if (!ok) break;
             if (!waited) {
                 grid_dep_wait();                         // counters and powers of two come from lay_rows_kernel
                 waited = true;
             }
-            // this warp's activation rows, 16 of every 64: row of y (negative: none) and scale
+            // this warp's activation rows, 16 of every 32: row of y (negative: none) and scale
             const int blocks = (d.rows + 15) / 16;
-            for (int b = gi, x = 0; b < blocks; b += 2 * kGroups, x += 32) {
-                const int i = 16 * (b + (lane >> 4) * kGroups) + (lane & 15), m = d.row0 + i;
+            for (int b = h, x = 0; b < blocks; b += 4, x += 32) {
+                const int i = 16 * (b + (lane >> 4) * 2) + (lane & 15), m = d.row0 + i;
                 int o = -1;
                 float f = 0.0f;
                 if (i < d.rows) {
@@ -581,24 +590,24 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                     if (o >= p.Ty) o = -1;
                     f = __ldcg(p.rscale + m);
                 }
-                if (x + lane < MC / kGroups) rowinfo[x + lane] = make_float2(__int_as_float(o), f);
+                if (x + lane < MC / 2) rowinfo[x + lane] = make_float2(__int_as_float(o), f);
             }
             __syncwarp();
             const int db = u % ND;
             if (!wait(&dfull[db], u / ND, kStatusMmaWait)) break;
             tc_fence_after();
             // sums: this warp's 32 weight rows, 16 activation rows at a time
-            const uint32_t dcol = tmem + tl + db * MC;
+            const uint32_t dcol = tmem + tl + (db * kTiles + tile) * MC;
             const bool cut = d.first != d.last || d.k0 > 0 || d.k1 < T;
-            constexpr size_t kPart = (size_t)MC * kTcRows;
+            constexpr size_t kPart = (size_t)MC * kUnitRows;
             bool store = true;
             if (cut) {
-                float* mine = p.part + (2 * (size_t)blockIdx.x + (d.k0 == 0)) * kPart + r;
-                for (int b = gi; b < blocks; b += kGroups) {
+                float* mine = p.part + (2 * (size_t)blockIdx.x + (d.k0 == 0)) * kPart + rr;
+                for (int b = h; b < blocks; b += 2) {
                     float v[16];
                     tmem_ld16(dcol + 16u * b, v);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) __stcg(mine + (size_t)(16 * b + j) * kTcRows, v[j]);
+                    for (int j = 0; j < 16; ++j) __stcg(mine + (size_t)(16 * b + j) * kUnitRows, v[j]);
                 }
                 __threadfence();
                 __syncwarp();
@@ -608,7 +617,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                 store = old + (unsigned)(d.k1 - d.k0) == (unsigned)T;    // the last part: all stages are summed
                 if (store) __threadfence();
             }
-            for (int b = gi; store && b < blocks; b += kGroups) {
+            for (int b = h; store && b < blocks; b += 2) {
                 float v[16];
                 if (!cut) {
                     tmem_ld16(dcol + 16u * b, v);
@@ -620,14 +629,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                         const long long q0 = ceil_div((long long)c * W, gridDim.x) - d.pos, q1 = ceil_div(((long long)c + 1) * W, gridDim.x) - d.pos;
                         const long long k0 = q0 <= 0 ? 0 : ceil_div(q0, d.cost), k1 = q1 <= 0 ? 0 : ceil_div(q1, d.cost);
                         if (k0 >= k1 || k0 >= T) continue;
-                        const float* f = p.part + (2 * (size_t)c + (k0 == 0)) * kPart + r;
+                        const float* f = p.part + (2 * (size_t)c + (k0 == 0)) * kPart + rr;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] += __ldcg(f + (size_t)(16 * b + j) * kTcRows);
+                        for (int j = 0; j < 16; ++j) v[j] += __ldcg(f + (size_t)(16 * b + j) * kUnitRows);
                     }
                 }
-                const int nn = d.n0 + r, N = p.pl.N;
+                const int nn = d.n0 + rr, N = p.pl.N;
                 int orow[16];
-                const float4* info = reinterpret_cast<const float4*>(rowinfo + (b / kGroups) * 16);
+                const float4* info = reinterpret_cast<const float4*>(rowinfo + (b >> 1) * 16);
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
                     const float4 f = info[j / 2];
@@ -683,19 +692,19 @@ WLayout wide_layout(int R, int K, int MC) {
     l.xg = 0;
     l.rscale = (size_t)R * K * 2;
     l.part = l.rscale + round16((size_t)R * 4);
-    l.count = l.part + (size_t)2 * kWideMaxCtas * MC * kTcRows * 4;
+    l.count = l.part + (size_t)2 * kWideMaxCtas * MC * kUnitRows * 4;
     l.total = l.count + kWideMaxCtas * kWorkers * 4;
     return l;
 }
 
 // Activation rows of a unit at most.
-int wide_mc(int R, int E) { return (R + E - 1) / E > 128 ? 256 : 128; }
+int wide_mc(int R, int E) { return (R + E - 1) / E > 64 ? 128 : 64; }
 
 template <int FMT, int MC>
 cudaError_t launch_wide_mc(const RowsArgs& a, WideParams& p, cudaStream_t st) {
     using G = Wide<FMT>;
-    const size_t fixed = code_slots(MC) * G::CB + kDescs * sizeof(WDesc) + kWorkers * (MC / kGroups) * 8 + kBarBytes + wgroups_bytes(a.E);
-    p.xslots = (int)((kWideSmem - fixed) / (MC * 128));
+    const size_t fixed = kCodeSlots * G::CB + kDescs * sizeof(WDesc) + kWorkers * (MC / 2) * 8 + kBarBytes + wgroups_bytes(a.E);
+    p.xslots = (int)((kWideSmem - fixed) / (MC * 256));
     if (p.xslots > kMaxX) p.xslots = kMaxX;
     if (p.xslots < 2) return cudaErrorInvalidValue;
     auto kern = wide_kernel<FMT, MC>;
@@ -713,7 +722,7 @@ cudaError_t launch_wide_mc(const RowsArgs& a, WideParams& p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms < kWideMaxCtas ? sms : kWideMaxCtas));
     cfg.blockDim = dim3(kWideThreads);
-    cfg.dynamicSmemBytes = fixed + (size_t)p.xslots * MC * 128;
+    cfg.dynamicSmemBytes = fixed + (size_t)p.xslots * MC * 256;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -750,7 +759,7 @@ cudaError_t launch_wide_fmt(const RowsArgs& a, cudaStream_t st) {
     WideParams p = {};
     const uint64_t crb = code_row_bytes(FMT, a.K), rows = (uint64_t)a.E * a.N;
     const cuuint64_t cd[2] = {crb, rows}, cst[1] = {crb};
-    const cuuint32_t cb[2] = {(cuuint32_t)G::RB, (cuuint32_t)kTcRows}, ones[3] = {1, 1, 1};
+    const cuuint32_t cb[2] = {(cuuint32_t)G::RB, (cuuint32_t)kUnitRows}, ones[3] = {1, 1, 1};
     const cuuint64_t xd[3] = {64, (cuuint64_t)a.R, (cuuint64_t)(a.K / 64)}, xst[2] = {(cuuint64_t)a.K * 2, 128};
     const cuuint32_t xb[3] = {64, 32, 1};
     if (enc(&p.cmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(a.codes), cd, cst, cb, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -772,7 +781,7 @@ cudaError_t launch_wide_fmt(const RowsArgs& a, cudaStream_t st) {
     p.act = a.act;
     p.wait_ns = wait_limit_ns();
     p.test_flags = test_flags();
-    return MC == 256 ? launch_wide_mc<FMT, 256>(a, p, st) : launch_wide_mc<FMT, 128>(a, p, st);
+    return MC == 128 ? launch_wide_mc<FMT, 128>(a, p, st) : launch_wide_mc<FMT, 64>(a, p, st);
 }
 
 }  // namespace
