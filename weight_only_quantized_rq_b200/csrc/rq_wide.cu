@@ -20,8 +20,10 @@
 //   * Units are cut where an even share of the work (rows x K) ends, so every
 //     CTA (one per SM) has the same; a cut unit's parts are summed through the
 //     workspace in K order by whichever CTA arrives last.
-// Roles: 16 unpacking warps (they also move the sums out), one warp that
-// issues the MMAs, one thread that copies codes and one that copies rows.
+// Roles: 16 unpacking warps (they also move the sums out), a warp per weight
+// tile that issues its MMAs (one warp alone issued for 380 of the 256 cycles
+// that the products of an atom take), one thread that copies codes and one
+// that copies rows.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -39,14 +41,14 @@ constexpr int kWorkers = 16;
 constexpr int kTiles = 2;               // weight tiles of a unit; warps 8 t .. 8 t + 7 unpack tile t, four of them
                                         // the first 64 of each 128 K, four the others
 constexpr int kUnitRows = kTiles * kTcRows;
-constexpr int kWideThreads = 32 * (kWorkers + 3);
+constexpr int kWideThreads = 32 * (kWorkers + 4);
 constexpr int kMaxX = 6;                // activation slots at most (128 K each)
 constexpr int kCodeSlots = 2;
 constexpr int kDescs = 8;
 constexpr size_t kWideSmem = 226 * 1024;
 constexpr int kWideMaxCtas = 256;
 constexpr int kA = 4;                   // A slots: 128 K of one tile, 64 columns
-constexpr int kBarBytes = (2 * kCodeSlots + 2 * kMaxX + 2 * kA + kDescs + 2 * 2 + 2) * 8;
+constexpr int kBarBytes = (2 * kCodeSlots + 2 * kMaxX + 2 * kA + kDescs + 4 * 2 + 3) * 8;
 
 template <int FMT>
 struct Wide {
@@ -392,9 +394,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     uint64_t* aempty = afull + kA;
     uint64_t* ufull = aempty + kA;
     uint64_t* dfull = ufull + kDescs;
-    uint64_t* dempty = dfull + ND;
-    uint64_t* mdone = dempty + ND;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(mdone + 1);
+    uint64_t* dempty = dfull + ND * kTiles;
+    uint64_t* mdone = dempty + ND * kTiles;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(mdone + kTiles);
     at += kBarBytes;
     WGroups g;
     g.cost = reinterpret_cast<long long*>(at);
@@ -407,18 +409,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
         }
         for (int s = 0; s < NX; ++s) {
             mbar_init(&xfull[s], 1);
-            mbar_init(&xempty[s], 1);
+            mbar_init(&xempty[s], kTiles);
         }
         for (int s = 0; s < kA; ++s) {
             mbar_init(&afull[s], kWorkers / kTiles);
             mbar_init(&aempty[s], 1);
         }
         for (int s = 0; s < kDescs; ++s) mbar_init(&ufull[s], 1);
-        for (int s = 0; s < ND; ++s) {
+        for (int s = 0; s < ND * kTiles; ++s) {
             mbar_init(&dfull[s], 1);
-            mbar_init(&dempty[s], kWorkers);
+            mbar_init(&dempty[s], kWorkers / kTiles);
         }
-        mbar_init(mdone, 1);
+        for (int s = 0; s < kTiles; ++s) mbar_init(&mdone[s], 1);
         fence_mbar_init();
     }
     if (warp == kWorkers) {
@@ -498,40 +500,39 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                 mbar_wait_bounded(&cfull[q], (uint32_t)(issued / kCodeSlots + (q < issued % kCodeSlots ? 1 : 0) - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
         }
         __syncwarp();
-    } else if (warp == kWorkers) {
+    } else if (warp >= kWorkers) {
         // ------------------------------------------------------- MMA issue
-        int xs = 0, xwrap = 0, as = 0, awrap = 0;
+        const int t = warp == kWorkers ? 0 : 1;
+        int xs = 0, xwrap = 0, as = t, awrap = 0;        // the tile's A slots: t, t + 2
         bool ok = true;
         for (int u = 0; ok; ++u) {
             if (!wait(&ufull[u % kDescs], u / kDescs, kStatusTmaWait)) break;
             const WDesc d = desc[u % kDescs];
             if (d.done) break;
             const int db = u % ND;
-            if (u >= ND && !wait(&dempty[db], u / ND - 1, kStatusMmaWait)) break;
+            if (u >= ND && !wait(&dempty[db * kTiles + t], u / ND - 1, kStatusMmaWait)) break;
             tc_fence_after();
             const int np = (d.rows + 15) & ~15;
             const uint32_t idesc = (1u << 4) | ((uint32_t)(np >> 3) << 17) | ((uint32_t)(kTcRows >> 4) << 24);   // fp16, fp32 sums
+            const uint32_t dc = tmem + (db * kTiles + t) * MC;
             const int n = (d.k1 - d.k0) * G::PAIRS;
-            for (int i = 0; ok && i < n; ++i) {
-                if (!wait(&xfull[xs], xwrap, kStatusTmaWait)) { ok = false; break; }
+            for (int i = 0; i < n; ++i) {
+                if (!wait(&xfull[xs], xwrap, kStatusTmaWait) || !wait(&afull[as], awrap, kStatusTmaWait)) { ok = false; break; }
+                tc_fence_after();
                 const uint64_t xd = sw128_desc(xbase + xs * (MC * 256));
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    if (!wait(&afull[as], awrap, kStatusTmaWait)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t dc = tmem + (db * kTiles + t) * MC, ac = tmem + A0 + 64u * as;
-                    mma_atom(dc, ac, xd, idesc, i ? 1u : 0u);
-                    mma_atom(dc, ac + 32u, xd + (uint64_t)(MC * 128 >> 4), idesc, 1u);
-                    mma_commit(&aempty[as]);
-                    if (++as == kA) { as = 0; ++awrap; }
-                }
+                const uint32_t ac = tmem + A0 + 64u * as;
+                mma_atom(dc, ac, xd, idesc, i ? 1u : 0u);
+                mma_atom(dc, ac + 32u, xd + (uint64_t)(MC * 128 >> 4), idesc, 1u);
+                mma_commit(&aempty[as]);
                 mma_commit(&xempty[xs]);
+                as += kTiles;
+                if (as >= kA) { as = t; ++awrap; }
                 if (++xs == NX) { xs = 0; ++xwrap; }
             }
-            if (ok) mma_commit(&dfull[db]);
+            if (ok) mma_commit(&dfull[db * kTiles + t]);
         }
-        mma_commit(mdone);
-        wait(mdone, 0, kStatusMmaWait);                  // no MMA in flight at teardown
+        mma_commit(&mdone[t]);
+        wait(&mdone[t], 0, kStatusMmaWait);              // no MMA in flight at teardown
     } else {
         // ------------------------------------------- unpack, then the sums
         const int q = warp & 3, tile = warp >> 3, h = (warp >> 2) & 1, r = 32 * q + lane, rr = kTcRows * tile + r;
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             }
             __syncwarp();
             const int db = u % ND;
-            if (!wait(&dfull[db], u / ND, kStatusMmaWait)) break;
+            if (!wait(&dfull[db * kTiles + tile], u / ND, kStatusMmaWait)) break;
             tc_fence_after();
             // sums: this warp's 32 weight rows, 16 activation rows at a time
             const uint32_t dcol = tmem + tl + (db * kTiles + tile) * MC;
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&dempty[db]);
+            if (lane == 0) mbar_arrive(&dempty[db * kTiles + tile]);
         }
     }
     __syncwarp();
