@@ -271,6 +271,19 @@ def test_lora_rows_and_ranks(orc, M, r):
     run_lora(orc, "w4g64", M, 256, 136, 7, r, seed=22)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [9, 32, 70, 129])
+def test_lora_many_rows(orc, fmt, M):
+    """bf16 results above the few rows whose adapters the product itself does, on either product kernel."""
+    run_lora(orc, fmt, M, 512, 200, 5, 40, ranks=[40, 0, 13, 33, 8], dtype=torch.bfloat16, seed=27)
+
+
+def test_lora_rounds_of_rows(orc):
+    """More rows than one round of launches takes."""
+    for dtype in (torch.float32, torch.bfloat16):
+        run_lora(orc, "w4g64", 2050, 128, 72, 9, 16, dtype=dtype, seed=28)
+
+
 @pytest.mark.parametrize("K,N", [(64, 1), (192, 129), (4096, 96), (8192, 40)])
 @pytest.mark.parametrize("fmt", ["w4g64", "w8g16"])
 def test_lora_widths(orc, fmt, K, N):

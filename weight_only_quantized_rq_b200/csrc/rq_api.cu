@@ -183,12 +183,8 @@ int rq_wgemm_batch(const rq_wgemm_item* items, int count, int M, void* stream) {
 // y; experts; adapter rank).
 constexpr int kMaxRows = 1 << 20, kMaxExperts = 1024, kMaxRank = 256;
 
-// Groups of this many rows on average go to the tensor-memory kernel.
-constexpr int kWideRows = 24;
-static bool wide_rows(int R, int E) { return R >= kWideRows * E; }
-
-static size_t grouped_bytes(int fmt, int R, int K, int N, int E) {
-    const size_t a = rq::rows_workspace(fmt, R, K, N, E, 0), b = wide_rows(R, E) ? rq::wide_workspace(R, K, E) : 0;
+static size_t grouped_bytes(int fmt, int R, int K, int E) {
+    const size_t a = rq::rows_workspace(fmt, R, K, E), b = rq::wide_rows(R, E) ? rq::wide_workspace(R, K, E) : 0;
     return a > b ? a : b;
 }
 
@@ -196,7 +192,7 @@ size_t rq_grouped_workspace_size(int fmt, int R, int K, int N, int E) {
     if (E < 1 || E > kMaxExperts || N < 1 || N > (1 << 24) / E || R < 1 || R > kMaxRows) return 0;
     if (shape_status(fmt, K, E * N) != RQ_OK) return 0;
     // enough for any smaller R too: the paths' needs grow with R but for the step between them
-    return grouped_bytes(fmt, R, K, N, E);
+    return grouped_bytes(fmt, R, K, E);
 }
 
 int rq_wgemm_grouped(const void* x, int T, int K, int N, const rq_packed* w, const rq_groups* g, void* y, int Ty, int act,
@@ -211,20 +207,20 @@ int rq_wgemm_grouped(const void* x, int T, int K, int N, const rq_packed* w, con
     if (!aligned16(x) || !aligned16(y) || !aligned16(workspace) || !aligned16(g->offsets) ||
         (g->in_rows && !aligned16(g->in_rows)) || (g->out_rows && !aligned16(g->out_rows)))
         return RQ_ERR_MISALIGNED;
-    if (workspace_bytes < grouped_bytes(w->fmt, g->R, K, N, g->E)) return RQ_ERR_INVALID_ARG;
+    if (workspace_bytes < grouped_bytes(w->fmt, g->R, K, g->E)) return RQ_ERR_INVALID_ARG;
     rq::RowsArgs a = {};
     a.fmt = w->fmt; a.T = T; a.K = K; a.N = N; a.E = g->E; a.R = g->R; a.Ty = Ty;
     a.x = x; a.codes = w->codes; a.scales = w->scales;
     a.offsets = g->offsets; a.in_rows = g->in_rows; a.out_rows = g->out_rows;
     a.y = y; a.ybf16 = out_type == RQ_OUT_BF16; a.act = act; a.ws = workspace;
-    if (a.ybf16 && wide_rows(g->R, g->E)) return cuda_status(rq::launch_wide(a, static_cast<cudaStream_t>(stream)));
+    if (a.ybf16 && rq::wide_rows(g->R, g->E)) return cuda_status(rq::launch_wide(a, static_cast<cudaStream_t>(stream)));
     return cuda_status(rq::launch_rows(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t rq_lora_workspace_size(int fmt, int M, int K, int N, int rank) {
     if (M < 1 || M > kMaxRows || rank < 8 || rank > kMaxRank || rank % 8 != 0) return 0;
     if (shape_status(fmt, K, N) != RQ_OK) return 0;
-    return rq::rows_workspace(fmt, M, K, N, 1, rank);
+    return rq::lora_workspace(fmt, M, K, N, rank);
 }
 
 int rq_wgemm_lora(const void* x, int M, int K, int N, const rq_packed* w, const rq_lora* ad, const int* row_adapter, void* y,
@@ -239,14 +235,14 @@ int rq_wgemm_lora(const void* x, int M, int K, int N, const rq_packed* w, const 
     if (!aligned16(x) || !aligned16(y) || !aligned16(workspace) || !aligned16(row_adapter) || !aligned16(ad->A) ||
         !aligned16(ad->B) || !aligned16(ad->scales) || (ad->ranks && !aligned16(ad->ranks)))
         return RQ_ERR_MISALIGNED;
-    if (workspace_bytes < rq::rows_workspace(w->fmt, M, K, N, 1, ad->rank)) return RQ_ERR_INVALID_ARG;
+    if (workspace_bytes < rq::lora_workspace(w->fmt, M, K, N, ad->rank)) return RQ_ERR_INVALID_ARG;
     rq::RowsArgs a = {};
     a.fmt = w->fmt; a.T = M; a.K = K; a.N = N; a.E = 1; a.R = M; a.Ty = M;
     a.x = x; a.codes = w->codes; a.scales = w->scales;
     a.y = y; a.ybf16 = out_type == RQ_OUT_BF16; a.ws = workspace;
-    a.adapter = row_adapter; a.A = ad->A; a.B = ad->B; a.alpha = ad->scales; a.ranks = ad->ranks;
-    a.n_adapters = ad->n; a.r = ad->rank;
-    return cuda_status(rq::launch_rows(a, static_cast<cudaStream_t>(stream)));
+    a.ad = {row_adapter, ad->ranks, static_cast<const __nv_bfloat16*>(ad->A), static_cast<const __nv_bfloat16*>(ad->B), ad->scales, nullptr,
+            ad->n, ad->rank, N, K};
+    return cuda_status(rq::launch_lora(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t rq_route_workspace_size(int T, int E, int k) {

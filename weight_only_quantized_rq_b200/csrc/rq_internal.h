@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace rq {
@@ -103,6 +104,18 @@ constexpr int kTcMinM = 3;
 bool tc_supported(int fmt, int M);
 cudaError_t launch_tc(const WgemmArgs* a, int count, cudaStream_t st);
 
+// The adapters of a call (device pointers): row m uses slot row[m], if there is
+// one, with the first ranks[slot] of its r ranks (ranks NULL: all).
+struct Adapters {
+    const int* row;
+    const int* ranks;
+    const __nv_bfloat16* A;    // [n][r][K]
+    const __nv_bfloat16* B;    // [n][N][r]
+    const float* alpha;        // [n]
+    float* t;                  // [rows][r]: alpha A x
+    int n, r, N, K;
+};
+
 // Products whose weights depend on the activation row (rq_rows.cu): E packed
 // matrices of N rows each in one plane, rows [offsets[e], offsets[e + 1]) of
 // the call multiplied by matrix e (offsets NULL: E = 1, every row); and one
@@ -117,20 +130,24 @@ struct RowsArgs {
     const int* out_rows;       // [R] row of y, or NULL: row i
     void* y;                   // [Ty][N]
     int ybf16, act;            // act 1: max(v, 0)^2
-    const int* adapter;        // [R] adapter of each row, or NULL
-    const void* A;             // bf16 [n_adapters][r][K]
-    const void* B;             // bf16 [n_adapters][N][r]
-    const float* alpha;        // [n_adapters]
-    const int* ranks;          // [n_adapters] or NULL: all r
-    int n_adapters, r;
+    Adapters ad;               // ad.row NULL: none
+    const int* order;          // rows in adapter order, and the adapters' term [R][ldz], made beside the product
+    const float* z;            // (NULL: the product makes it)
+    int ldz;
     void* ws;
 };
-size_t rows_workspace(int fmt, int R, int K, int N, int E, int rank);
+size_t rows_workspace(int fmt, int R, int K, int E);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st);
 
 // The grouped products for groups of many rows, bf16 results (rq_wide.cu).
+inline bool wide_rows(int R, int E) { return R >= 32 * E; }
 size_t wide_workspace(int R, int K, int E);
 cudaError_t launch_wide(const RowsArgs& a, cudaStream_t st);
+
+// The product with an adapter per row, either way (rq_lora.cu).
+size_t lora_workspace(int fmt, int R, int K, int N, int rank);
+cudaError_t launch_lora(const RowsArgs& a, cudaStream_t st);
+cudaError_t launch_expand(const Adapters& ad, const int* order, int R, float* z, int ldz, cudaStream_t st);
 
 // Expert routing (rq_route.cu).
 struct RouteArgs {

@@ -1,0 +1,146 @@
+// rq_lora.cu -- a low-rank adapter per row beside a shared packed product:
+// y[m] = x[m] W^T + s_a B_a (A_a x[m]), a = row_adapter[m].
+//
+// Up to eight rows the product's own kernels do it (rq_rows.cu): two launches.
+// Above, the adapters' term is made beside the product and added in its
+// epilogue, in fp32 before the one rounding:
+//   shrink_kernel  t = s_a A_a x (a warp per row and two ranks; bound by reading
+//                  the A of every adapter in use), and the rows' order by adapter
+//   expand_kernel  z = B_a t for eight rows x 128 weight rows per block, rows in
+//                  adapter order so that a block reads the B of few adapters
+// The product starts while expand runs and waits for it only at its end.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "rq_device.cuh"
+#include "rq_internal.h"
+#include "rq_rows.cuh"
+
+namespace rq {
+namespace {
+
+constexpr int kFewRows = 8;
+constexpr int kBlockRows = 1024;       // rows per round of launches
+constexpr int kShrinkThreads = 256;
+constexpr int kExpandThreads = 128;
+
+__global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const __grid_constant__ Adapters p, const __nv_bfloat16* x, int R, int* order) {
+    __shared__ int slot[kBlockRows];
+    const int tid = threadIdx.x, lane = tid & 31;
+    grid_dep_wait();
+    grid_dep_launch();                                   // all work before this call is done
+    const long long i = ((long long)blockIdx.x * kShrinkThreads + tid) >> 5;
+    const int per = p.r / 2;
+    if (blockIdx.x < gridDim.x - 1) {
+        const int m = (int)(i / per);
+        if (m < R) shrink_pair<4>(p, x, m, 2 * (int)(i - (long long)m * per), lane);
+        return;
+    }
+    // the last block: the rows' places in adapter order (rows without one last)
+    for (int m = tid; m < R; m += kShrinkThreads) {
+        const int a = p.row[m];
+        slot[m] = a >= 0 && a < p.n ? a : 0x7fffffff;
+    }
+    __syncthreads();
+    for (int m = tid; m < R; m += kShrinkThreads) {
+        const int a = slot[m];
+        int at = 0;
+        for (int q = 0; q < R; ++q) at += slot[q] < a || (slot[q] == a && q < m);
+        order[at] = m;
+    }
+}
+
+__global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_constant__ Adapters p, const int* order, int R, float* z, int ldz) {
+    __shared__ float4 scratch[kExpandThreads / 32][64];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int n0 = blockIdx.x * 128 + 32 * warp, i = 8 * blockIdx.y + (lane >> 2);
+    if (n0 >= ldz) return;
+    const int m = i < R ? order[i] : -1;
+    float acc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    for (int c = 0; 32 * c < p.r; ++c) add_adapters(p, m, c, n0 + (lane >> 2), lane, acc[0], acc[1]);
+    // [activation row][weight row], 16-byte chunks swizzled by the row
+    float* f = reinterpret_cast<float*>(scratch[warp]);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int r = 2 * (lane & 3) + (q & 1), c = 16 * mt + (lane >> 2) + 8 * (q >> 1);
+            f[r * 32 + (((c >> 2) ^ r) << 2) + (c & 3)] = acc[mt][q];
+        }
+    __syncwarp();
+    const int r = lane >> 2, n = n0 + 8 * (lane & 3);
+    if (m < 0 || n >= ldz) return;
+    float4* o = reinterpret_cast<float4*>(z + (size_t)m * ldz + n);
+    o[0] = scratch[warp][r * 8 + ((2 * (lane & 3)) ^ r)];
+    o[1] = scratch[warp][r * 8 + ((2 * (lane & 3) + 1) ^ r)];
+}
+
+template <class K, class... A>
+cudaError_t launch(K kernel, dim3 grid, int block, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+int ld_of(int N) { return (N + 7) & ~7; }
+
+struct LoraLayout { size_t t, order, z, product, total; };
+
+LoraLayout lora_layout(int fmt, int R, int K, int N, int rank) {
+    const int b = R < kBlockRows ? R : kBlockRows;
+    LoraLayout l;
+    l.t = 0;
+    l.order = round16((size_t)b * rank * 4);
+    l.z = l.order + round16((size_t)b * 4);
+    l.product = l.z + (R > kFewRows ? (size_t)b * ld_of(N) * 4 : 0);
+    const size_t narrow = rows_workspace(fmt, b, K, 1), wide = wide_rows(b, 1) ? wide_workspace(b, K, 1) : 0;
+    l.total = l.product + (narrow > wide ? narrow : wide);
+    return l;
+}
+
+}  // namespace
+
+cudaError_t launch_expand(const Adapters& ad, const int* order, int R, float* z, int ldz, cudaStream_t st) {
+    return launch(expand_kernel, dim3((unsigned)((ldz + 127) / 128), (unsigned)((R + 7) / 8)), kExpandThreads, st, ad, order, R, z, ldz);
+}
+
+size_t lora_workspace(int fmt, int R, int K, int N, int rank) { return lora_layout(fmt, R, K, N, rank).total; }
+
+cudaError_t launch_lora(const RowsArgs& a0, cudaStream_t st) {
+    const LoraLayout l = lora_layout(a0.fmt, a0.R, a0.K, a0.N, a0.ad.r);
+    uint8_t* ws = static_cast<uint8_t*>(a0.ws);
+    for (int m0 = 0; m0 < a0.R; m0 += kBlockRows) {
+        RowsArgs a = a0;
+        a.R = a.T = a.Ty = a0.R - m0 < kBlockRows ? a0.R - m0 : kBlockRows;
+        a.x = static_cast<const __nv_bfloat16*>(a0.x) + (size_t)m0 * a0.K;
+        a.y = static_cast<uint8_t*>(a0.y) + (size_t)m0 * a0.N * (a0.ybf16 ? 2 : 4);
+        a.ws = ws + l.product;
+        a.ad.row = a0.ad.row + m0;
+        a.ad.t = reinterpret_cast<float*>(ws + l.t);
+        if (a0.R > kFewRows) {
+            int* order = reinterpret_cast<int*>(ws + l.order);
+            const long long warps = (long long)a.R * (a.ad.r / 2);
+            cudaError_t e = launch(shrink_kernel, dim3((unsigned)((warps + kShrinkThreads / 32 - 1) / (kShrinkThreads / 32) + 1)), kShrinkThreads, st,
+                                   a.ad, static_cast<const __nv_bfloat16*>(a.x), a.R, order);
+            if (e != cudaSuccess) return e;
+            a.order = order;
+            a.z = reinterpret_cast<float*>(ws + l.z);
+            a.ldz = ld_of(a0.N);
+        }
+        const cudaError_t e = a.ybf16 && wide_rows(a.R, 1) ? launch_wide(a, st) : launch_rows(a, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace rq

@@ -47,6 +47,7 @@
 
 #include "rq_device.cuh"
 #include "rq_internal.h"
+#include "rq_rows.cuh"
 #include "rq_tc.cuh"
 
 namespace rq {
@@ -103,11 +104,9 @@ struct RowsParams {
     const int* out_rows;
     void* y;
     int Ty, ybf16, act;
-    const int* adapter;
-    const int* ranks;
-    const __nv_bfloat16* B;
-    const float* t;                    // [R][r]
-    int n_adapters, r;
+    Adapters ad;                       // row NULL: none; used where a unit holds one 8-row tile
+    const float* z;                    // [R][ldz] the adapters' term, or NULL
+    int ldz;
     int ring, xslot;                   // code slots; bytes of an activation slot
     unsigned long long wait_ns;
     int test_flags;
@@ -122,12 +121,8 @@ struct PrepParams {
     unsigned* count;
     int n_count;
     int tiles_max, kblocks;
-    const int* adapter;
-    const int* ranks;
-    const __nv_bfloat16* A;
-    const float* alpha;
-    float* t;
-    int n_adapters, r;
+    Adapters ad;
+    int late;                          // the kernel before this one is waited for at the end
 };
 
 // ------------------------------------------------------------------ groups
@@ -208,12 +203,12 @@ __device__ __forceinline__ float bf16_sum8(uint4 v) {
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kPrepThreads, 16) prep_kernel(const PrepParams p) {
+__global__ void __launch_bounds__(kPrepThreads, 8) prep_kernel(const PrepParams p) {
     using G = Geo<FMT>;
     extern __shared__ __align__(16) uint8_t sm[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    grid_dep_wait();
-    grid_dep_launch();                                   // the product kernel may start: all earlier work is done
+    if (!p.late) grid_dep_wait();
+    grid_dep_launch();                                   // the next kernel may start: all work before this call is done
     const int nx = p.tiles_max * p.kblocks;
     if ((int)blockIdx.x < nx) {
         if (blockIdx.x == 0)
@@ -222,7 +217,10 @@ __global__ void __launch_bounds__(kPrepThreads, 16) prep_kernel(const PrepParams
         if (warp == 0) scan_groups(p.pl, g, lane);
         __syncthreads();
         const int tile = blockIdx.x / p.kblocks, kb = blockIdx.x % p.kblocks;
-        if (tile >= g.tile[p.pl.E]) return;
+        if (tile >= g.tile[p.pl.E]) {
+            if (p.late) grid_dep_wait();
+            return;
+        }
         const int e = find_group(g.tile, p.pl.E, tile);
         const int row = g.row[e] + 8 * (tile - g.tile[e]) + (lane >> 2);     // lane = 4 (row in tile) + chunk in four
         int src = -1;
@@ -289,35 +287,11 @@ __global__ void __launch_bounds__(kPrepThreads, 16) prep_kernel(const PrepParams
             }
         }
     } else {
-        // t[m][j] = s_a A_a[j] . x[m]: a warp takes two ranks of a row, which share its x
-        const int per = p.r / (2 * (kPrepThreads / 32));
+        const int per = p.ad.r / (2 * (kPrepThreads / 32));
         const int b = blockIdx.x - nx, m = b / per, j = 2 * ((b - m * per) * (kPrepThreads / 32) + warp);
-        const int a = p.adapter[m];
-        if (a < 0 || a >= p.n_adapters) return;
-        if (p.ranks && j >= p.ranks[a]) return;
-        const uint4* x = reinterpret_cast<const uint4*>(p.x + (size_t)m * p.pl.K);
-        const uint4* w = reinterpret_cast<const uint4*>(p.A + ((size_t)a * p.r + j) * p.pl.K);
-        const int nc = p.pl.K / 8;
-        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll 2
-        for (int c = lane; c < nc; c += 32) {
-            const uint4 u = x[c], v0 = __ldg(w + c), v1 = __ldg(w + nc + c);
-            const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, a0[4] = {v0.x, v0.y, v0.z, v0.w}, a1[4] = {v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s0 = fmaf(bf16lo_f32(uu[i]), bf16lo_f32(a0[i]), s0);
-                s1 = fmaf(bf16lo_f32(uu[i]), bf16lo_f32(a1[i]), s1);
-                s0 = fmaf(bf16hi_f32(uu[i]), bf16hi_f32(a0[i]), s0);
-                s1 = fmaf(bf16hi_f32(uu[i]), bf16hi_f32(a1[i]), s1);
-            }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            s0 += __shfl_xor_sync(~0u, s0, o);
-            s1 += __shfl_xor_sync(~0u, s1, o);
-        }
-        if (lane < 2) p.t[(size_t)m * p.r + j + lane] = (lane ? s1 : s0) * p.alpha[a];   // one past the rank is not read
+        shrink_pair<4>(p.ad, p.x, m, j, lane);
     }
+    if (p.late) grid_dep_wait();                         // done means that the kernel before is done too
 }
 
 // ------------------------------------------------------------ PTX wrappers
@@ -337,15 +311,6 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool in)
 }
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
-}
-
-// D = A B + C, A 16 x 16 (row), B 16 x 8 (col), bf16 with fp32 sums.
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1,
-                                         float c2, float c3) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // (v & m) | c
@@ -609,73 +574,6 @@ __device__ __forceinline__ Work get_work(const Plan& pl, const Groups& g, long l
     return w;
 }
 
-// fp32 pair -> bf16x2 (nearest even), lo in the low half.
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
-// Adds the adapters' term over ranks 32 c .. 32 c + 31 to one 8-row tile's
-// sums: for each adapter among the tile's rows D += B_a t^T, with t zero for
-// the other rows. t is split into three bf16 parts (24 bits), so that nothing
-// of it is lost to the tensor core's operand type. Lane 4 g + q holds ranks
-// 8 q .. 8 q + 7 of the chunk: of weight rows n + 8 i (i = 0..3) and of
-// activation row g.
-__device__ __forceinline__ void add_adapters(const RowsParams& p, const Desc& d, int tile, int c, int n, int lane,
-                                             float (&acc0)[4], float (&acc1)[4]) {
-    const int i = 8 * tile + (lane >> 2), m = d.row0 + i, j0 = 32 * c + 8 * (lane & 3);
-    int a = -1, rank = 0;
-    if (i < d.rows) {
-        a = p.adapter[m];
-        if (a >= 0 && a < p.n_adapters) rank = p.ranks ? min(p.ranks[a], p.r) : p.r;
-        if (rank <= 32 * c) a = -1;
-    }
-    uint32_t t[3][4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        float2 v = make_float2(0.0f, 0.0f);
-        if (a >= 0 && j0 + 2 * q < rank) {
-            v = *reinterpret_cast<const float2*>(p.t + (size_t)m * p.r + j0 + 2 * q);
-            if (j0 + 2 * q + 1 >= rank) v.y = 0.0f;
-        }
-        t[0][q] = pack2(v.x, v.y);
-        v.x -= bf16lo_f32(t[0][q]);
-        v.y -= bf16hi_f32(t[0][q]);
-        t[1][q] = pack2(v.x, v.y);
-        v.x -= bf16lo_f32(t[1][q]);
-        v.y -= bf16hi_f32(t[1][q]);
-        t[2][q] = pack2(v.x, v.y);
-    }
-    unsigned todo = __ballot_sync(~0u, a >= 0);
-    while (todo) {
-        const int src = __ffs(todo) - 1, aa = __shfl_sync(~0u, a, src), rk = __shfl_sync(~0u, rank, src);
-        const bool same = a == aa;
-        todo &= ~__ballot_sync(~0u, same);
-        uint4 b[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            b[q] = make_uint4(0u, 0u, 0u, 0u);
-            if (j0 < rk) b[q] = __ldg(reinterpret_cast<const uint4*>(p.B + ((size_t)aa * p.pl.N + min(n + 8 * q, p.pl.N - 1)) * p.r + j0));
-            const int keep = rk - j0;                    // past the rank the slot may hold anything
-            if (keep < 8) {
-                const auto cut = [&](uint32_t w, int k) { return k + 1 < keep ? w : k < keep ? w & 0xffffu : 0u; };
-                b[q] = make_uint4(cut(b[q].x, 0), cut(b[q].y, 2), cut(b[q].z, 4), cut(b[q].w, 6));
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < 3; ++s) {
-            const uint32_t t0 = same ? t[s][0] : 0u, t1 = same ? t[s][1] : 0u, t2 = same ? t[s][2] : 0u, t3 = same ? t[s][3] : 0u;
-            const uint32_t a0[4] = {b[0].x, b[1].x, b[0].y, b[1].y}, a1[4] = {b[2].x, b[3].x, b[2].y, b[3].y};
-            const uint32_t a2[4] = {b[0].z, b[1].z, b[0].w, b[1].w}, a3[4] = {b[2].z, b[3].z, b[2].w, b[3].w};
-            mma16816(acc0, a0, t0, t1, acc0[0], acc0[1], acc0[2], acc0[3]);
-            mma16816(acc1, a1, t0, t1, acc1[0], acc1[1], acc1[2], acc1[3]);
-            mma16816(acc0, a2, t2, t3, acc0[0], acc0[1], acc0[2], acc0[3]);
-            mma16816(acc1, a3, t2, t3, acc1[0], acc1[1], acc1[2], acc1[3]);
-        }
-    }
-}
-
 // v[0..7] to columns n .. n + 7 of y's row `out`.
 __device__ __forceinline__ void store8(const RowsParams& p, int out, int n, const float (&v)[8]) {
     const int N = p.pl.N;
@@ -789,7 +687,7 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
             if (++cslot == ring) { cslot = 0; ++cwrap; }
             next(cc);
         }
-        grid_dep_wait();
+        if (!p.z) grid_dep_wait();                       // with z, the kernel before this one waited for prep_kernel
         asm volatile("fence.proxy.async.global;" ::: "memory");
         // In the order in which slots come free: a stage's activations when
         // the stage kXRing before has been used, then the codes that follow
@@ -813,10 +711,10 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
                 mbar_arrive_expect_tx(&xfull[xslot], (uint32_t)(tiles * G::XB));
             }
             __syncwarp();
-            if (p.adapter && k == 0) {                                   // the adapters' B rows into L2, by the unit's first CTA
-                const int a = lane < w.rows ? p.adapter[w.row0 + lane] : -1;
-                if (a >= 0 && a < p.n_adapters && (lane == 0 || p.adapter[w.row0 + lane - 1] != a))
-                    prefetch_l2_bulk(p.B + ((size_t)a * p.pl.N + w.n0) * p.r, (uint32_t)(min(kRowsPerTile, p.pl.N - w.n0) * p.r * 2));
+            if (NB == 1 && p.ad.row && k == 0) {                         // the adapters' B rows into L2, by the unit's first CTA
+                const int a = lane < w.rows ? p.ad.row[w.row0 + lane] : -1;
+                if (a >= 0 && a < p.ad.n && (lane == 0 || p.ad.row[w.row0 + lane - 1] != a))
+                    prefetch_l2_bulk(p.ad.B + ((size_t)a * p.pl.N + w.n0) * p.ad.r, (uint32_t)(min(kRowsPerTile, p.pl.N - w.n0) * p.ad.r * 2));
             }
             if (lane < tiles)
                 bulk_x(xs + lane * G::XB, p.xf + ((size_t)(w.tile0 + lane) * T + k) * G::XB, G::XB, &xfull[xslot]);
@@ -878,7 +776,7 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
         return __all_sync(~0u, mbar_try_wait(bar, (uint32_t)wrap & 1u)) ||
                __all_sync(~0u, mbar_wait_bounded(bar, (uint32_t)wrap & 1u, kStatusTmaWait, 0u, p.wait_ns));
     };
-    grid_dep_wait();                                      // counters and adapter terms come from prep_kernel
+    bool waited = false;
     for (int u = 0; left > 0; ++u) {
         if (!wait(&xfull[xslot], xwrap)) return;
         const Desc d = desc[u % kDescs];
@@ -913,15 +811,16 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
         left -= d.k1 - d.k0;
 
         const int parts = d.last - d.first + 1;
-        if (p.adapter) {
-            // the parts of a unit share its (tile, 32 ranks) pairs
-            const int chunks = (p.r + 31) / 32, me = (int)blockIdx.x - d.first;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                if (nb >= tiles) break;
-                for (int c = 0; c < chunks; ++c)
-                    if (parts == 1 || (c * tiles + nb) % parts == me)
-                        add_adapters(p, d, nb, c, d.n0 + wr + (lane >> 2), lane, acc[0][nb], acc[1][nb]);
+        if (!waited) {
+            grid_dep_wait();                              // counters and the adapters' terms come from the kernels before
+            waited = true;
+        }
+        if constexpr (NB == 1) {
+            if (p.ad.row) {
+                // the parts of a unit share its ranks, 32 at a time
+                const int i = lane >> 2, m = i < d.rows ? d.row0 + i : -1;
+                for (int c = (int)blockIdx.x - d.first; 32 * c < p.ad.r; c += parts)
+                    add_adapters(p.ad, m, c, d.n0 + wr + (lane >> 2), lane, acc[0][0], acc[1][0]);
             }
         }
         if (parts > 1) {
@@ -990,6 +889,12 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
             const float4* f = reinterpret_cast<const float4*>(scratch) + (lane >> 2) * 8;
             const float4 f0 = f[(2 * (lane & 3)) ^ (lane >> 2)], f1 = f[(2 * (lane & 3) + 1) ^ (lane >> 2)];
             float v[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+            if (p.z) {
+                const float4* z = reinterpret_cast<const float4*>(p.z + (size_t)(d.row0 + 8 * nb + (lane >> 2)) * p.ldz + nn);
+                const float4 z0 = __ldcg(z), z1 = __ldcg(z + 1);
+                v[0] += z0.x; v[1] += z0.y; v[2] += z0.z; v[3] += z0.w;
+                v[4] += z1.x; v[5] += z1.y; v[6] += z1.z; v[7] += z1.w;
+            }
             if (p.act) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -1015,18 +920,17 @@ int pick_nb(int R, int E) {
     return R <= 8 || per <= 3 ? 1 : per <= 12 ? 2 : 4;
 }
 
-struct Layout { size_t xf, part, count, t, total; int tiles, T; };
+struct Layout { size_t xf, part, count, total; int tiles, T; };
 
 template <int FMT>
-Layout layout(int R, int K, int E, int rank) {
+Layout layout(int R, int K, int E) {
     Layout l;
     l.T = (K + Geo<FMT>::KS - 1) / Geo<FMT>::KS;
     l.tiles = R / 8 + (E < R ? E : R);                   // sum of ceil(m_e / 8) at most
     l.xf = 0;
     l.part = round16((size_t)l.tiles * l.T * Geo<FMT>::XB);
     l.count = l.part + (size_t)2 * kMaxCtas * pick_nb(R, E) * 4096;
-    l.t = l.count + kMaxCtas * kMathWarps * 4;
-    l.total = l.t + round16((size_t)R * rank * 4);
+    l.total = l.count + kMaxCtas * kMathWarps * 4;
     return l;
 }
 
@@ -1074,7 +978,7 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
     using G = Geo<FMT>;
     const EncodeTiled enc = encoder();
     if (!enc) return cudaErrorNotSupported;
-    const Layout l = layout<FMT>(a.R, a.K, a.E, a.adapter ? a.r : 0);
+    const Layout l = layout<FMT>(a.R, a.K, a.E);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     Plan pl = {a.offsets, a.E, a.R, a.N, a.K, l.T, pick_nb(a.R, a.E)};
 
@@ -1088,14 +992,9 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
     q.n_count = kMaxCtas * kMathWarps;
     q.tiles_max = l.tiles;
     q.kblocks = (l.T * G::KS / 8 + kPrepChunks - 1) / kPrepChunks;
-    q.adapter = a.adapter;
-    q.ranks = a.ranks;
-    q.A = static_cast<const __nv_bfloat16*>(a.A);
-    q.alpha = a.alpha;
-    q.t = reinterpret_cast<float*>(ws + l.t);
-    q.n_adapters = a.n_adapters;
-    q.r = a.r;
-    const long long blocks = (long long)q.tiles_max * q.kblocks + (a.adapter ? (long long)a.R * (a.r / (2 * (kPrepThreads / 32))) : 0);
+    if (!a.z) q.ad = a.ad;                                // with z the adapters' term is made elsewhere
+    q.late = a.z != nullptr;
+    const long long blocks = (long long)q.tiles_max * q.kblocks + (q.ad.row ? (long long)a.R * (q.ad.r / (2 * (kPrepThreads / 32))) : 0);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
@@ -1109,6 +1008,10 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, prep_kernel<FMT>, q);
     if (e != cudaSuccess) return e;
+    if (a.z) {
+        e = launch_expand(a.ad, a.order, a.R, const_cast<float*>(a.z), a.ldz, st);
+        if (e != cudaSuccess) return e;
+    }
 
     RowsParams p = {};
     const uint64_t crb = code_row_bytes(FMT, a.K), rows = (uint64_t)a.E * a.N;
@@ -1130,12 +1033,9 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
     p.Ty = a.Ty;
     p.ybf16 = a.ybf16;
     p.act = a.act;
-    p.adapter = a.adapter;
-    p.ranks = a.ranks;
-    p.B = static_cast<const __nv_bfloat16*>(a.B);
-    p.t = reinterpret_cast<const float*>(ws + l.t);
-    p.n_adapters = a.n_adapters;
-    p.r = a.r;
+    p.ad = q.ad;
+    p.z = a.z;
+    p.ldz = a.ldz;
     p.wait_ns = wait_limit_ns();
     p.test_flags = test_flags();
     if (pl.NB == 1) return launch_product<FMT, 1>(p, st);
@@ -1145,15 +1045,15 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t rows_workspace(int fmt, int R, int K, int, int E, int rank) {
+size_t rows_workspace(int fmt, int R, int K, int E) {
     switch (fmt) {
-        case kFmtW4G64: return layout<kFmtW4G64>(R, K, E, rank).total;
-        case kFmtW8G16: return layout<kFmtW8G16>(R, K, E, rank).total;
-        case kFmtW8G64: return layout<kFmtW8G64>(R, K, E, rank).total;
-        case kFmtW6G16: return layout<kFmtW6G16>(R, K, E, rank).total;
-        case kFmtW4SB32: return layout<kFmtW4SB32>(R, K, E, rank).total;
-        case kFmtW5SB32: return layout<kFmtW5SB32>(R, K, E, rank).total;
-        default: return layout<kFmtW6SB32>(R, K, E, rank).total;
+        case kFmtW4G64: return layout<kFmtW4G64>(R, K, E).total;
+        case kFmtW8G16: return layout<kFmtW8G16>(R, K, E).total;
+        case kFmtW8G64: return layout<kFmtW8G64>(R, K, E).total;
+        case kFmtW6G16: return layout<kFmtW6G16>(R, K, E).total;
+        case kFmtW4SB32: return layout<kFmtW4SB32>(R, K, E).total;
+        case kFmtW5SB32: return layout<kFmtW5SB32>(R, K, E).total;
+        default: return layout<kFmtW6SB32>(R, K, E).total;
     }
 }
 

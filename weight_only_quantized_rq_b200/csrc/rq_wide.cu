@@ -32,6 +32,7 @@
 
 #include "rq_device.cuh"
 #include "rq_internal.h"
+#include "rq_rows.cuh"
 #include "rq_tc.cuh"
 
 namespace rq {
@@ -61,7 +62,7 @@ struct Wide {
 };
 
 struct WidePlan {
-    const int* offsets;
+    const int* offsets;                 // NULL: one group of all rows
     int E, R, N, K, T, MC;
 };
 
@@ -78,6 +79,8 @@ struct WideParams {
     const int* out_rows;
     void* y;
     int Ty, act;
+    const float* z;                     // [R][ldz] the adapters' term, or NULL
+    int ldz;
     int xslots;
     unsigned long long wait_ns;
     int test_flags;
@@ -94,14 +97,17 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
 // One warp per row: the largest exponent, then the row under its power of two.
 template <int ORDER>
 __global__ void __launch_bounds__(kLayThreads) lay_rows_kernel(const __nv_bfloat16* x, const int* in_rows, int rows_x, int R, int K,
-                                                             uint4* out, float* rscale, unsigned* count, int n_count) {
+                                                             uint4* out, float* rscale, unsigned* count, int n_count, int late) {
     const int lane = threadIdx.x & 31;
-    grid_dep_wait();
+    if (!late) grid_dep_wait();
     grid_dep_launch();
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < n_count; i += kLayThreads) count[i] = 0u;
     const int row = blockIdx.x * (kLayThreads / 32) + (threadIdx.x >> 5);
-    if (row >= R) return;
+    if (row >= R) {
+        if (late) grid_dep_wait();
+        return;
+    }
     int src = in_rows ? in_rows[row] : row;
     if (src < 0 || src >= rows_x) src = -1;
     const uint4* p = reinterpret_cast<const uint4*>(x + (size_t)(src < 0 ? 0 : src) * K);
@@ -135,6 +141,7 @@ __global__ void __launch_bounds__(kLayThreads) lay_rows_kernel(const __nv_bfloat
         else if (ORDER == 2) o[c] = make_uint4(prmt(h[0], h[1], 0x5410u), prmt(h[0], h[1], 0x7632u), prmt(h[2], h[3], 0x5410u), prmt(h[2], h[3], 0x7632u));
         else o[c] = make_uint4(h[0], h[1], h[2], h[3]);
     }
+    if (late) grid_dep_wait();                           // done means that the kernel before is done too
 }
 
 // ------------------------------------------------------------------ groups
@@ -160,7 +167,9 @@ __device__ __forceinline__ void scan_wide(const WidePlan& pl, WGroups g, int lan
     long long base = 0;
     for (int e0 = 0; e0 <= pl.E; e0 += 32) {
         const int e = e0 + lane;
-        int v = e <= pl.E ? min(max(pl.offsets[e], 0), pl.R) : 0;
+        int v = 0;
+        if (pl.offsets) v = e <= pl.E ? min(max(pl.offsets[e], 0), pl.R) : 0;
+        else v = e >= 1 ? pl.R : 0;                       // one group of all rows
         for (int o = 1; o < 32; o <<= 1) {
             const int w = __shfl_up_sync(~0u, v, o);
             if (lane >= o) v = max(v, w);
@@ -446,7 +455,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     if (warp == kWorkers + 1) {
         // ------------------------------------------------ work and its rows
         if (lane == 0) {
-            grid_dep_wait();                             // the rows come from lay_rows_kernel
+            if (!p.z) grid_dep_wait();                   // the rows (with z, the kernel before this one waited for them)
             asm volatile("fence.proxy.async.global;" ::: "memory");
             Walk walk(p.pl, g);
             WDesc d;
@@ -646,6 +655,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                     v[j] *= f.y;
                     v[j + 1] *= f.w;
                 }
+                if (p.z) {
+                    const float* z = p.z + (size_t)(d.row0 + 16 * b) * p.ldz + nn;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (orow[j] >= 0 && nn < N) v[j] += __ldcg(z + (size_t)j * p.ldz);
+                }
                 if (p.act) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -754,8 +769,12 @@ cudaError_t launch_wide_fmt(const RowsArgs& a, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, lay_rows_kernel<G::ORDER>, static_cast<const __nv_bfloat16*>(a.x), a.in_rows, a.T, a.R, a.K,
-                                       reinterpret_cast<uint4*>(ws + l.xg), rscale, count, kWideMaxCtas * kWorkers);
+                                       reinterpret_cast<uint4*>(ws + l.xg), rscale, count, kWideMaxCtas * kWorkers, a.z ? 1 : 0);
     if (e != cudaSuccess) return e;
+    if (a.z) {
+        e = launch_expand(a.ad, a.order, a.R, const_cast<float*>(a.z), a.ldz, st);
+        if (e != cudaSuccess) return e;
+    }
 
     WideParams p = {};
     const uint64_t crb = code_row_bytes(FMT, a.K), rows = (uint64_t)a.E * a.N;
@@ -780,6 +799,8 @@ cudaError_t launch_wide_fmt(const RowsArgs& a, cudaStream_t st) {
     p.y = a.y;
     p.Ty = a.Ty;
     p.act = a.act;
+    p.z = a.z;
+    p.ldz = a.ldz;
     p.wait_ns = wait_limit_ns();
     p.test_flags = test_flags();
     return MC == 128 ? launch_wide_mc<FMT, 128>(a, p, st) : launch_wide_mc<FMT, 64>(a, p, st);
