@@ -611,6 +611,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             const bool cut = d.first != d.last || d.k0 > 0 || d.k1 < T;
             constexpr size_t kPart = (size_t)MC * kUnitRows;
             bool store = true;
+            // which of CTAs c0 .. c0 + 31 have stages of the unit
+            auto parts_from = [&](int c0) {
+                const int c = c0 + lane;
+                const long long q0 = ceil_div((long long)c * W, gridDim.x) - d.pos, q1 = ceil_div(((long long)c + 1) * W, gridDim.x) - d.pos;
+                const long long k0 = q0 <= 0 ? 0 : ceil_div(q0, d.cost), k1 = q1 <= 0 ? 0 : ceil_div(q1, d.cost);
+                return __ballot_sync(~0u, c <= d.last && k0 < k1 && k0 < T);
+            };
+            unsigned parts0 = 0u;
             if (cut) {
                 float* mine = p.part + (2 * (size_t)blockIdx.x + (d.k0 == 0)) * kPart + rr;
                 for (int b = h; b < blocks; b += 2) {
@@ -625,7 +633,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                 if (lane == 0) old = atomicAdd(&p.count[d.first * kWorkers + warp], (unsigned)(d.k1 - d.k0));
                 old = __shfl_sync(~0u, old, 0);
                 store = old + (unsigned)(d.k1 - d.k0) == (unsigned)T;    // the last part: all stages are summed
-                if (store) __threadfence();
+                if (store) {
+                    __threadfence();
+                    parts0 = parts_from(d.first);
+                }
             }
             for (int b = h; store && b < blocks; b += 2) {
                 float v[16];
@@ -634,14 +645,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] = 0.0f;
-                    for (int c = d.first; c <= d.last; ++c) {
-                        // CTA c's stages of the unit, if it has any
-                        const long long q0 = ceil_div((long long)c * W, gridDim.x) - d.pos, q1 = ceil_div(((long long)c + 1) * W, gridDim.x) - d.pos;
-                        const long long k0 = q0 <= 0 ? 0 : ceil_div(q0, d.cost), k1 = q1 <= 0 ? 0 : ceil_div(q1, d.cost);
-                        if (k0 >= k1 || k0 >= T) continue;
-                        const float* f = p.part + (2 * (size_t)c + (k0 == 0)) * kPart + rr;
+                    for (int c0 = d.first; c0 <= d.last; c0 += 32) {
+                        unsigned todo = c0 == d.first ? parts0 : parts_from(c0);
+                        while (todo) {                   // two parts' loads at a time, added in order
+                            const int ca = __ffs(todo) - 1;
+                            todo &= todo - 1;
+                            const int cb = todo ? __ffs(todo) - 1 : -1;
+                            todo &= todo - 1;
+                            const float* fa = p.part + (2 * (size_t)(c0 + ca) + (c0 + ca == d.first)) * kPart + (size_t)(16 * b) * kUnitRows + rr;
+                            const float* fb = p.part + 2 * (size_t)(c0 + max(cb, 0)) * kPart + (size_t)(16 * b) * kUnitRows + rr;
+                            float xa[16], xb[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] += __ldcg(f + (size_t)(16 * b + j) * kUnitRows);
+                            for (int j = 0; j < 16; ++j) xa[j] = __ldcg(fa + j * kUnitRows);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) xb[j] = cb >= 0 ? __ldcg(fb + j * kUnitRows) : 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = (v[j] + xa[j]) + xb[j];
+                        }
                     }
                 }
                 const int nn = d.n0 + rr, N = p.pl.N;
