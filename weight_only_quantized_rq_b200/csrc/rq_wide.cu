@@ -150,8 +150,9 @@ __global__ void __launch_bounds__(kLayThreads) lay_rows_kernel(const __nv_bfloat
 struct WGroups {
     long long* cost;   // [E + 1]
     int* row;          // [E + 1]
+    int* ctas;         // CTAs that share the work
 };
-__host__ __device__ inline size_t wgroups_bytes(int E) { return round16((size_t)(E + 1) * 12); }
+__host__ __device__ inline size_t wgroups_bytes(int E) { return round16((size_t)(E + 1) * 12 + 4); }
 
 __device__ __forceinline__ int chunk_rows(int m, int MC) {
     const int c = (m + MC - 1) / MC;
@@ -164,7 +165,7 @@ __device__ __forceinline__ int stage_cost(int rows) { return max(rows, 96); }
 __device__ __forceinline__ void scan_wide(const WidePlan& pl, WGroups g, int lane) {
     const int tiles_n = (pl.N + kUnitRows - 1) / kUnitRows;
     int top = 0;
-    long long base = 0;
+    long long base = 0, units = 0;
     for (int e0 = 0; e0 <= pl.E; e0 += 32) {
         const int e = e0 + lane;
         int v = 0;
@@ -178,10 +179,13 @@ __device__ __forceinline__ void scan_wide(const WidePlan& pl, WGroups g, int lan
         const int prev = __shfl_up_sync(~0u, v, 1);
         const int m = lane == 0 ? (e0 ? v - top : 0) : v - prev;       // rows of group e - 1
         const int rc = chunk_rows(m, pl.MC);
-        long long c = (long long)((m + rc - 1) / rc) * tiles_n * pl.T * stage_cost(rc);
+        long long un = (long long)((m + rc - 1) / rc) * tiles_n, c = un * pl.T * stage_cost(rc);
         for (int o = 1; o < 32; o <<= 1) {
-            const long long b = __shfl_up_sync(~0u, c, o);
-            if (lane >= o) c += b;
+            const long long b = __shfl_up_sync(~0u, c, o), n = __shfl_up_sync(~0u, un, o);
+            if (lane >= o) {
+                c += b;
+                un += n;
+            }
         }
         if (e <= pl.E) {
             g.row[e] = v;
@@ -189,6 +193,15 @@ __device__ __forceinline__ void scan_wide(const WidePlan& pl, WGroups g, int lan
         }
         top = __shfl_sync(~0u, v, 31);
         base += __shfl_sync(~0u, c, 31);
+        units += __shfl_sync(~0u, un, 31);
+    }
+    // Cutting a unit into p parts takes its K loop (about 0.65 us per 128 K) down to a p-th and costs about
+    // 0.5 us per part and 2.5 more per 128 rows to sum them: p = the root of the two's ratio, where the
+    // units alone do not fill the SMs.
+    if (lane == 0) {
+        const float loop = 0.65f * (float)((pl.K + 127) / 128), part = 0.5f + 2.5f / 128.0f * (float)min(pl.MC, (top + pl.E - 1) / pl.E);
+        const long long want = units * max(1, (int)(sqrtf(loop / part) + 0.5f));
+        *g.ctas = (int)min((long long)gridDim.x, max(1ll, want));
     }
     __syncwarp();
 }
@@ -216,10 +229,10 @@ struct Walk {
 
     __device__ __forceinline__ Walk(const WidePlan& plan, const WGroups& groups) : pl(plan), g(groups) {
         W = g.cost[pl.E];
-        Gc = gridDim.x;
+        Gc = *g.ctas;
         const long long P0 = ceil_div(blockIdx.x * W, Gc);
         P1 = ceil_div((blockIdx.x + 1) * W, Gc);
-        live = P0 < P1;
+        live = blockIdx.x < Gc && P0 < P1;
         if (!live) return;
         int lo = 0, hi = pl.E - 1;                       // last expert whose first position is at most P0
         while (lo < hi) {
@@ -263,6 +276,14 @@ struct Walk {
         st = unit * T + d.k1;
         return true;
     }
+};
+
+// An activation row at the end of a unit: where it goes (NULL: nowhere), its
+// power of two as fp32, and what the stored bf16 pairs are multiplied by.
+struct __align__(16) RowInfo {
+    __nv_bfloat16* y;
+    float scale;
+    uint32_t scale2;
 };
 
 // ------------------------------------------------------------------ unpack
@@ -380,6 +401,18 @@ __device__ __forceinline__ void atom_scales(const uint8_t* row, int a, int K, ui
     }
 }
 
+// max(v, 0), NaN stays NaN
+__device__ __forceinline__ float relu_nan(float v) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(v), "f"(0.0f));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // ----------------------------------------------------------------- product
 template <int FMT, int MC>
 __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_constant__ WideParams p) {
@@ -393,8 +426,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     uint8_t* at = smem + kCodeSlots * G::CB + (size_t)NX * MC * 256;
     WDesc* desc = reinterpret_cast<WDesc*>(at);
     at += kDescs * sizeof(WDesc);
-    float2* rowinfo = reinterpret_cast<float2*>(at) + (warp & (kWorkers - 1)) * (MC / 2);   // (row of y, scale) per warp
-    at += kWorkers * (MC / 2) * 8;
+    RowInfo* rowinfo = reinterpret_cast<RowInfo*>(at) + (warp & (kWorkers - 1)) * (MC / 2);
+    at += kWorkers * (MC / 2) * sizeof(RowInfo);
     uint64_t* cfull = reinterpret_cast<uint64_t*>(at);
     uint64_t* cempty = cfull + kCodeSlots;
     uint64_t* xfull = cempty + kCodeSlots;
@@ -410,6 +443,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     WGroups g;
     g.cost = reinterpret_cast<long long*>(at);
     g.row = reinterpret_cast<int*>(g.cost + p.pl.E + 1);
+    g.ctas = g.row + p.pl.E + 1;
 
     if (tid == 0) {
         for (int s = 0; s < kCodeSlots; ++s) {
@@ -548,7 +582,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
         const uint32_t tl = (uint32_t)(32 * q) << 16;
         int cs = 0, cwrap = 0, as = tile, awrap = 0;     // this tile's A slots: tile, tile + 2
         bool waited = false;
-        const long long W = g.cost[p.pl.E];
+        const long long W = g.cost[p.pl.E], Gc = *g.ctas;
         for (int u = 0;; ++u) {
             if (!wait(&ufull[u % kDescs], u / kDescs, kStatusTmaWait)) break;
             const WDesc d = desc[u % kDescs];
@@ -589,19 +623,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                 grid_dep_wait();                         // counters and powers of two come from lay_rows_kernel
                 waited = true;
             }
+            bool safe = true;                            // a row's power of two squared stays in range
             // this warp's activation rows, 16 of every 32: row of y (negative: none) and scale
             const int blocks = (d.rows + 15) / 16;
             for (int b = h, x = 0; b < blocks; b += 4, x += 32) {
                 const int i = 16 * (b + (lane >> 4) * 2) + (lane & 15), m = d.row0 + i;
-                int o = -1;
-                float f = 0.0f;
+                RowInfo info = {nullptr, 0.0f, 0u};
                 if (i < d.rows) {
-                    o = p.out_rows ? __ldg(p.out_rows + m) : m;
-                    if (o >= p.Ty) o = -1;
-                    f = __ldcg(p.rscale + m);
+                    const int o = p.out_rows ? __ldg(p.out_rows + m) : m;
+                    if (o >= 0 && o < p.Ty) info.y = static_cast<__nv_bfloat16*>(p.y) + (size_t)o * p.pl.N + d.n0;
+                    info.scale = __ldcg(p.rscale + m);
+                    const float f = p.act ? info.scale * info.scale : info.scale;
+                    info.scale2 = (__float_as_uint(f) >> 16) * 0x10001u;
+                    if (p.act && !(info.scale > 1e-18f && info.scale < 1e18f)) safe = false;
                 }
-                if (x + lane < MC / 2) rowinfo[x + lane] = make_float2(__int_as_float(o), f);
+                if (x + lane < MC / 2) rowinfo[x + lane] = info;
             }
+            safe = __all_sync(~0u, safe);
             __syncwarp();
             const int db = u % ND;
             if (!wait(&dfull[db * kTiles + tile], u / ND, kStatusMmaWait)) break;
@@ -614,7 +652,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             // which of CTAs c0 .. c0 + 31 have stages of the unit
             auto parts_from = [&](int c0) {
                 const int c = c0 + lane;
-                const long long q0 = ceil_div((long long)c * W, gridDim.x) - d.pos, q1 = ceil_div(((long long)c + 1) * W, gridDim.x) - d.pos;
+                const long long q0 = ceil_div((long long)c * W, Gc) - d.pos, q1 = ceil_div(((long long)c + 1) * W, Gc) - d.pos;
                 const long long k0 = q0 <= 0 ? 0 : ceil_div(q0, d.cost), k1 = q1 <= 0 ? 0 : ceil_div(q1, d.cost);
                 return __ballot_sync(~0u, c <= d.last && k0 < k1 && k0 < T);
             };
@@ -664,46 +702,44 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                         }
                     }
                 }
-                const int nn = d.n0 + rr, N = p.pl.N;
-                int orow[16];
-                const float4* info = reinterpret_cast<const float4*>(rowinfo + (b >> 1) * 16);
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const float4 f = info[j / 2];
-                    orow[j] = __float_as_int(f.x);
-                    orow[j + 1] = __float_as_int(f.z);
-                    v[j] *= f.y;
-                    v[j + 1] *= f.w;
-                }
-                if (p.z) {
-                    const float* z = p.z + (size_t)(d.row0 + 16 * b) * p.ldz + nn;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (orow[j] >= 0 && nn < N) v[j] += __ldcg(z + (size_t)j * p.ldz);
-                }
-                if (p.act) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        v[j] = v[j] > 0.0f || v[j] != v[j] ? v[j] : 0.0f;
-                        v[j] *= v[j];
-                    }
-                }
-                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y);
-                if ((N & 1) == 0) {
-                    // lanes in pairs: the even one stores columns n, n + 1 of row j, the odd one those of row j + 1
+                const int left = p.pl.N - d.n0 - rr;                     // columns from this lane's on
+                const RowInfo* info = rowinfo + (b >> 1) * 16;
+                if ((p.pl.N & 1) == 0 && !p.z && safe) {
+                    // The row's power of two commutes with the rounding, so it is applied to the packed bf16 results.
+                    // Lanes in pairs: the even one stores columns n, n + 1 of row j, the odd one those of row j + 1.
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
-                        const float give = lane & 1 ? v[j] : v[j + 1];
-                        const float got = __shfl_xor_sync(~0u, give, 1);
-                        const __nv_bfloat162 h = lane & 1 ? __floats2bfloat162_rn(got, v[j + 1]) : __floats2bfloat162_rn(v[j], got);
-                        const int o = lane & 1 ? orow[j + 1] : orow[j];
-                        if (o >= 0 && nn < N)
-                            *reinterpret_cast<__nv_bfloat162*>(y + (size_t)o * N + (nn & ~1)) = h;
+                        float v0 = v[j], v1 = v[j + 1];
+                        if (p.act) {
+                            v0 = relu_nan(v0);
+                            v1 = relu_nan(v1);
+                            v0 *= v0;
+                            v1 *= v1;
+                        }
+                        const uint32_t own = pack2(v0, v1), other = __shfl_xor_sync(~0u, own, 1);
+                        const RowInfo f = info[j + (lane & 1)];
+                        const uint32_t h = mul_bf16x2(lane & 1 ? prmt(other, own, 0x7632u) : prmt(own, other, 0x5410u), f.scale2);
+                        if (f.y && left > 0) *reinterpret_cast<uint32_t*>(f.y + (rr & ~1)) = h;
                     }
                 } else {
+                    if (p.z) {                           // all loads before the first store
+                        const float* z = p.z + (size_t)(d.row0 + 16 * b) * p.ldz + d.n0 + rr;
+                        float zv[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (orow[j] >= 0 && nn < N) y[(size_t)orow[j] * N + nn] = __float2bfloat16_rn(v[j]);
+                        for (int j = 0; j < 16; ++j) zv[j] = 16 * b + j < d.rows && left > 0 ? __ldcg(z + (size_t)j * p.ldz) : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = fmaf(v[j], info[j].scale, zv[j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const RowInfo f = info[j];
+                        float r1 = p.z ? v[j] : v[j] * f.scale;
+                        if (p.act) {
+                            r1 = relu_nan(r1);
+                            r1 *= r1;
+                        }
+                        if (f.y && left > 0) f.y[rr] = __float2bfloat16_rn(r1);
+                    }
                 }
             }
             tc_fence_before();
@@ -733,13 +769,18 @@ WLayout wide_layout(int R, int K, int MC) {
     return l;
 }
 
-// Activation rows of a unit at most.
-int wide_mc(int R, int E) { return (R + E - 1) / E > 64 ? 128 : 64; }
+// Activation rows of a unit at most: 128 where that still makes a unit for
+// every second SM.
+int wide_mc(int R, int E, int N) {
+    const int per = (R + E - 1) / E;
+    if (per <= 64) return 64;
+    return (long long)((N + kUnitRows - 1) / kUnitRows) * E * ((per + 127) / 128) >= sm_count() / 2 ? 128 : 64;
+}
 
 template <int FMT, int MC>
 cudaError_t launch_wide_mc(const RowsArgs& a, WideParams& p, cudaStream_t st) {
     using G = Wide<FMT>;
-    const size_t fixed = kCodeSlots * G::CB + kDescs * sizeof(WDesc) + kWorkers * (MC / 2) * 8 + kBarBytes + wgroups_bytes(a.E);
+    const size_t fixed = kCodeSlots * G::CB + kDescs * sizeof(WDesc) + kWorkers * (MC / 2) * sizeof(RowInfo) + kBarBytes + wgroups_bytes(a.E);
     p.xslots = (int)((kWideSmem - fixed) / (MC * 256));
     if (p.xslots > kMaxX) p.xslots = kMaxX;
     if (p.xslots < 2) return cudaErrorInvalidValue;
@@ -773,7 +814,7 @@ cudaError_t launch_wide_fmt(const RowsArgs& a, cudaStream_t st) {
     using G = Wide<FMT>;
     const EncodeTiled enc = encoder();
     if (!enc) return cudaErrorNotSupported;
-    const int MC = wide_mc(a.R, a.E);
+    const int MC = wide_mc(a.R, a.E, a.N);
     const WLayout l = wide_layout(a.R, a.K, MC);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     unsigned* count = reinterpret_cast<unsigned*>(ws + l.count);
@@ -828,7 +869,7 @@ cudaError_t launch_wide_fmt(const RowsArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t wide_workspace(int R, int K, int E) { return wide_layout(R, K, wide_mc(R, E)).total; }
+size_t wide_workspace(int R, int K, int E) { return wide_layout(R, K, (R + E - 1) / E > 64 ? 128 : 64).total; }
 
 cudaError_t launch_wide(const RowsArgs& a, cudaStream_t st) {
     switch (a.fmt) {
