@@ -4,7 +4,7 @@
 // Up to eight rows the product's own kernels do it (rq_rows.cu): two launches.
 // Above, the adapters' term is made beside the product and added in its
 // epilogue, in fp32 before the one rounding:
-//   shrink_kernel  t = s_a A_a x (a warp per row and two ranks; bound by reading
+//   shrink_kernel  t = s_a A_a x (a block per row and eight ranks; bound by reading
 //                  the A of every adapter in use), and the rows' order by adapter
 //   expand_kernel  z = B_a t for eight rows x 128 weight rows per block, rows in
 //                  adapter order so that a block reads the B of few adapters
@@ -27,14 +27,13 @@ constexpr int kExpandThreads = 128;
 
 __global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const __grid_constant__ Adapters p, const __nv_bfloat16* x, int R, int* order) {
     __shared__ int slot[kBlockRows];
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     grid_dep_wait();
     grid_dep_launch();                                   // all work before this call is done
-    const long long i = ((long long)blockIdx.x * kShrinkThreads + tid) >> 5;
-    const int per = p.r / 2;
+    __shared__ float part[kShrinkThreads / 32][8];
+    const int per = p.r / 8;
     if (blockIdx.x < gridDim.x - 1) {
-        const int m = (int)(i / per);
-        if (m < R) shrink_pair<4>(p, x, m, 2 * (int)(i - (long long)m * per), lane);
+        shrink8<kShrinkThreads / 32>(p, x, blockIdx.x / per, 8 * (blockIdx.x % per), part);
         return;
     }
     // the last block: the rows' places in adapter order (rows without one last)
@@ -129,9 +128,8 @@ cudaError_t launch_lora(const RowsArgs& a0, cudaStream_t st) {
         a.ad.t = reinterpret_cast<float*>(ws + l.t);
         if (a0.R > kFewRows) {
             int* order = reinterpret_cast<int*>(ws + l.order);
-            const long long warps = (long long)a.R * (a.ad.r / 2);
-            cudaError_t e = launch(shrink_kernel, dim3((unsigned)((warps + kShrinkThreads / 32 - 1) / (kShrinkThreads / 32) + 1)), kShrinkThreads, st,
-                                   a.ad, static_cast<const __nv_bfloat16*>(a.x), a.R, order);
+            const cudaError_t e = launch(shrink_kernel, dim3((unsigned)(a.R * (a.ad.r / 8) + 1)), kShrinkThreads, st, a.ad,
+                                         static_cast<const __nv_bfloat16*>(a.x), a.R, order);
             if (e != cudaSuccess) return e;
             a.order = order;
             a.z = reinterpret_cast<float*>(ws + l.z);

@@ -287,9 +287,9 @@ __global__ void __launch_bounds__(kPrepThreads, 8) prep_kernel(const PrepParams 
             }
         }
     } else {
-        const int per = p.ad.r / (2 * (kPrepThreads / 32));
-        const int b = blockIdx.x - nx, m = b / per, j = 2 * ((b - m * per) * (kPrepThreads / 32) + warp);
-        shrink_pair<4>(p.ad, p.x, m, j, lane);
+        __shared__ float part[kPrepThreads / 32][8];
+        const int per = p.ad.r / 8, b = blockIdx.x - nx;
+        shrink8<kPrepThreads / 32>(p.ad, p.x, b / per, 8 * (b % per), part);
     }
     if (p.late) grid_dep_wait();                         // done means that the kernel before is done too
 }
@@ -994,7 +994,7 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
     q.kblocks = (l.T * G::KS / 8 + kPrepChunks - 1) / kPrepChunks;
     if (!a.z) q.ad = a.ad;                                // with z the adapters' term is made elsewhere
     q.late = a.z != nullptr;
-    const long long blocks = (long long)q.tiles_max * q.kblocks + (q.ad.row ? (long long)a.R * (q.ad.r / (2 * (kPrepThreads / 32))) : 0);
+    const long long blocks = (long long)q.tiles_max * q.kblocks + (q.ad.row ? (long long)a.R * (q.ad.r / 8) : 0);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);

@@ -27,35 +27,48 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return d;
 }
 
-// t[m][j], t[m][j + 1] = alpha A[j] . x[m] by one warp: the two ranks share the
-// row. A second one past the slot's rank is not read.
-template <int UNROLL>
-__device__ __forceinline__ void shrink_pair(const Adapters& p, const __nv_bfloat16* xs, int m, int j, int lane) {
-    const int a = p.row[m];
-    if (a < 0 || a >= p.n) return;
+// t[m][j .. j + 7] = alpha A . x[m] by a block of WARPS warps that share out K,
+// so that each lane has one load of x and eight of A in flight per round. Ranks
+// past the slot's are not read.
+template <int WARPS>
+__device__ __forceinline__ void shrink8(const Adapters& p, const __nv_bfloat16* xs, int m, int j, float (&part)[WARPS][8]) {
+    const int a = p.row[m], lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (a < 0 || a >= p.n) return;                       // the same for the whole block
     if (p.ranks && j >= p.ranks[a]) return;
     const uint4* x = reinterpret_cast<const uint4*>(xs + (size_t)m * p.K);
     const uint4* w = reinterpret_cast<const uint4*>(p.A + ((size_t)a * p.r + j) * p.K);
     const int nc = p.K / 8;
-    float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll UNROLL
-    for (int c = lane; c < nc; c += 32) {
-        const uint4 u = x[c], v0 = __ldg(w + c), v1 = __ldg(w + nc + c);
-        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, a0[4] = {v0.x, v0.y, v0.z, v0.w}, a1[4] = {v1.x, v1.y, v1.z, v1.w};
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 32 * warp + lane; c < nc; c += 32 * WARPS) {
+        const uint4 u = x[c];
+        uint4 v[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s0 = fmaf(bf16lo_f32(uu[i]), bf16lo_f32(a0[i]), s0);
-            s1 = fmaf(bf16lo_f32(uu[i]), bf16lo_f32(a1[i]), s1);
-            s0 = fmaf(bf16hi_f32(uu[i]), bf16hi_f32(a0[i]), s0);
-            s1 = fmaf(bf16hi_f32(uu[i]), bf16hi_f32(a1[i]), s1);
+        for (int q = 0; q < 8; ++q) v[q] = __ldg(w + (size_t)q * nc + c);
+        const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const uint32_t vv[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[q] = fmaf(bf16lo_f32(uu[i]), bf16lo_f32(vv[i]), s[q]);
+                s[q] = fmaf(bf16hi_f32(uu[i]), bf16hi_f32(vv[i]), s[q]);
+            }
         }
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        s0 += __shfl_xor_sync(~0u, s0, o);
-        s1 += __shfl_xor_sync(~0u, s1, o);
+    for (int q = 0; q < 8; ++q)
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s[q] += __shfl_xor_sync(~0u, s[q], o);
+    if (lane == 0)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) part[warp][q] = s[q];
+    __syncthreads();
+    if (threadIdx.x < 8) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) t += part[i][threadIdx.x];
+        p.t[(size_t)m * p.r + j + threadIdx.x] = t * p.alpha[a];
     }
-    if (lane < 2) p.t[(size_t)m * p.r + j + lane] = (lane ? s1 : s0) * p.alpha[a];
 }
 
 // Adds the adapters' term over ranks 32 c .. 32 c + 31 to one 8-row tile's

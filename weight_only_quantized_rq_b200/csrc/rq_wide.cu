@@ -94,53 +94,66 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One warp per row: the largest exponent, then the row under its power of two.
+// Eight bf16 values under the power of two f, as fp16 in the order that the codes unpack in.
 template <int ORDER>
-__global__ void __launch_bounds__(kLayThreads) lay_rows_kernel(const __nv_bfloat16* x, const int* in_rows, int rows_x, int R, int K,
-                                                             uint4* out, float* rscale, unsigned* count, int n_count, int late) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ uint4 lay8(uint4 v, float f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = half2_bits(bf16lo_f32(w[i]) * f, bf16hi_f32(w[i]) * f);
+    if (ORDER == 1) return make_uint4(prmt(h[0], h[2], 0x5410u), prmt(h[0], h[2], 0x7632u), prmt(h[1], h[3], 0x5410u), prmt(h[1], h[3], 0x7632u));
+    if (ORDER == 2) return make_uint4(prmt(h[0], h[1], 0x5410u), prmt(h[0], h[1], 0x7632u), prmt(h[2], h[3], 0x5410u), prmt(h[2], h[3], 0x7632u));
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+__device__ __forceinline__ uint32_t top8(uint4 v) {
+    const uint32_t m = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+}
+
+// One block per row: the largest exponent, then the row under its power of
+// two. Rows of up to 8192 values stay in registers between the two.
+template <int ORDER>
+__global__ void __launch_bounds__(kLayThreads) lay_rows_kernel(const __nv_bfloat16* x, const int* in_rows, int rows_x, int K, uint4* out,
+                                                             float* rscale, unsigned* count, int n_count, int late) {
+    __shared__ uint32_t tops[kLayThreads / 32];
+    const int tid = threadIdx.x, row = blockIdx.x;
     if (!late) grid_dep_wait();
     grid_dep_launch();
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < n_count; i += kLayThreads) count[i] = 0u;
-    const int row = blockIdx.x * (kLayThreads / 32) + (threadIdx.x >> 5);
-    if (row >= R) {
-        if (late) grid_dep_wait();
-        return;
-    }
+    if (row == 0)
+        for (int i = tid; i < n_count; i += kLayThreads) count[i] = 0u;
     int src = in_rows ? in_rows[row] : row;
     if (src < 0 || src >= rows_x) src = -1;
     const uint4* p = reinterpret_cast<const uint4*>(x + (size_t)(src < 0 ? 0 : src) * K);
-    const int nc = K / 8;
+    const int nc = src < 0 ? 0 : K / 8;
+    constexpr int KEEP = 4;
+    uint4 v[KEEP];
     uint32_t top = 0u;
-    if (src >= 0) {
-#pragma unroll 4
-        for (int c = lane; c < nc; c += 32) {
-            const uint4 v = p[c];
-            const uint32_t m = 0x7fff7fffu;
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m)));
-        }
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) {
+        const int c = tid + i * kLayThreads;
+        v[i] = c < nc ? p[c] : make_uint4(0u, 0u, 0u, 0u);
     }
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) top = __vmaxu2(top, top8(v[i]));
+    for (int c = tid + KEEP * kLayThreads; c < nc; c += kLayThreads) top = __vmaxu2(top, top8(p[c]));
     top = max(top & 0xffffu, top >> 16);
     top = __reduce_max_sync(~0u, top);
+    if ((tid & 31) == 0) tops[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kLayThreads / 32; ++i) top = max(top, tops[i]);
     const int ex = (int)(top >> 7);                      // biased exponent of the largest value; 255: not finite
     int sh = 0;
     if (ex < 255 && top) sh = max(-126, min(126, 141 - ex));
     const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
-    if (lane == 0) rscale[row] = __uint_as_float((uint32_t)(127 - sh) << 23);
-    uint4* o = out + (size_t)row * nc;
-#pragma unroll 2
-    for (int c = lane; c < nc; c += 32) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (src >= 0) v = p[c];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t h[4];
+    if (tid == 0) rscale[row] = __uint_as_float((uint32_t)(127 - sh) << 23);
+    uint4* o = out + (size_t)row * (K / 8);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = half2_bits(bf16lo_f32(w[i]) * f, bf16hi_f32(w[i]) * f);
-        if (ORDER == 1) o[c] = make_uint4(prmt(h[0], h[2], 0x5410u), prmt(h[0], h[2], 0x7632u), prmt(h[1], h[3], 0x5410u), prmt(h[1], h[3], 0x7632u));
-        else if (ORDER == 2) o[c] = make_uint4(prmt(h[0], h[1], 0x5410u), prmt(h[0], h[1], 0x7632u), prmt(h[2], h[3], 0x5410u), prmt(h[2], h[3], 0x7632u));
-        else o[c] = make_uint4(h[0], h[1], h[2], h[3]);
+    for (int i = 0; i < KEEP; ++i) {
+        const int c = tid + i * kLayThreads;
+        if (c < K / 8) o[c] = lay8<ORDER>(v[i], f);
     }
+    for (int c = tid + KEEP * kLayThreads; c < K / 8; c += kLayThreads) o[c] = lay8<ORDER>(c < nc ? p[c] : make_uint4(0u, 0u, 0u, 0u), f);
     if (late) grid_dep_wait();                           // done means that the kernel before is done too
 }
 
@@ -821,7 +834,7 @@ cudaError_t launch_wide_fmt(const RowsArgs& a, cudaStream_t st) {
     float* rscale = reinterpret_cast<float*>(ws + l.rscale);
 
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.R + kLayThreads / 32 - 1) / (kLayThreads / 32)));
+    cfg.gridDim = dim3((unsigned)a.R);
     cfg.blockDim = dim3(kLayThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -829,7 +842,7 @@ cudaError_t launch_wide_fmt(const RowsArgs& a, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, lay_rows_kernel<G::ORDER>, static_cast<const __nv_bfloat16*>(a.x), a.in_rows, a.T, a.R, a.K,
+    cudaError_t e = cudaLaunchKernelEx(&cfg, lay_rows_kernel<G::ORDER>, static_cast<const __nv_bfloat16*>(a.x), a.in_rows, a.T, a.K,
                                        reinterpret_cast<uint4*>(ws + l.xg), rscale, count, kWideMaxCtas * kWorkers, a.z ? 1 : 0);
     if (e != cudaSuccess) return e;
     if (a.z) {
