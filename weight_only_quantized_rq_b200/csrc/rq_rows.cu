@@ -202,8 +202,10 @@ __device__ __forceinline__ float bf16_sum8(uint4 v) {
            ((bf16lo_f32(v.z) + bf16hi_f32(v.z)) + (bf16lo_f32(v.w) + bf16hi_f32(v.w)));
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kPrepThreads, 8) prep_kernel(const PrepParams p) {
+// With 32 registers its blocks fit beside the CTAs of a product that is still
+// running; with SHRINK (adapters of few rows) it takes 64.
+template <int FMT, bool SHRINK>
+__global__ void __launch_bounds__(kPrepThreads, SHRINK ? 8 : 16) prep_kernel(const PrepParams p) {
     using G = Geo<FMT>;
     extern __shared__ __align__(16) uint8_t sm[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(kPrepThreads, 8) prep_kernel(const PrepParams 
                 }
             }
         }
-    } else {
+    } else if constexpr (SHRINK) {
         __shared__ float part[kPrepThreads / 32][8];
         const int per = p.ad.r / 8, b = blockIdx.x - nx;
         shrink8<kPrepThreads / 32>(p.ad, p.x, b / per, 8 * (b % per), part);
@@ -550,13 +552,19 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t ss
 // ----------------------------------------------------------------- product
 // One stretch of a unit in one CTA, written by the copy warp ahead of the
 // stretch's first stage.
-struct Desc {
-    int n0;            // first weight row within the expert
-    int row0, rows;    // rows of the call
+struct __align__(16) Desc {
+    int rows;          // rows of the call
     int k0, k1;        // stages
+    int n0;            // first weight row within the expert
+    int row0;          // first row
     int first, last;   // CTAs that share the unit
-    int e;
+    int pad;
 };
+
+__device__ __forceinline__ Desc read_desc(const Desc* p) {
+    const uint4 a = lds128_a(smem_u32(p)), b = lds128_a(smem_u32(p) + 16);
+    return {(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
 
 struct Work { int e, n0, row0, rows, tile0; };   // a unit: expert, first weight row, first row and rows, first 8-row tile
 
@@ -703,7 +711,7 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
             if (lane == 0) {
                 if (k == 0 || cx.i == 0) {
                     const long long us = cx.unit * T;
-                    Desc d = {w.n0, w.row0, w.rows, k, min(T, k + n - cx.i), (int)blockIdx.x, (int)blockIdx.x, w.e};
+                    Desc d = {w.rows, k, min(T, k + n - cx.i), w.n0, w.row0, (int)blockIdx.x, (int)blockIdx.x, 0};
                     if (d.k0 > 0) d.first = (int)(((us + 1) * Gc - 1) / S);
                     if (d.k1 < T) d.last = (int)(((us + T) * Gc - 1) / S);
                     desc[cx.u % kDescs] = d;
@@ -779,14 +787,10 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
     bool waited = false;
     for (int u = 0; left > 0; ++u) {
         if (!wait(&xfull[xslot], xwrap)) return;
-        const Desc d = desc[u % kDescs];
-        const int tiles = (d.rows + 7) / 8;
-        int out[NB];                                      // this lane's rows of y, for the end
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const int i = 8 * nb + (lane >> 2), m = d.row0 + i;
-            out[nb] = i >= d.rows ? -1 : p.out_rows ? p.out_rows[m] : m;
-        }
+        // The descriptor is read again after the stages, so that they keep no registers for it (its place is not
+        // written before the copy warp is kDescs units ahead, more than the slots allow).
+        const uint4 d0 = lds128_a(smem_u32(&desc[u % kDescs]));
+        const int tiles = ((int)d0.x + 7) / 8, count = (int)d0.z - (int)d0.y;
         float acc[2][NB][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -795,10 +799,10 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[mt][nb][i] = 0.0f;
 #pragma unroll 1
-        for (int k = d.k0; k < d.k1; ++k) {
+        for (int k = 0; k < count; ++k) {
             if (!wait(&cfull[cslot], cwrap)) return;
             const uint32_t cs = base + cslot * G::CB, xs = xbase + xslot * p.xslot;
-            if (k > d.k0 && !wait(&xfull[xslot], xwrap)) return;
+            if (k && !wait(&xfull[xslot], xwrap)) return;
             stage_math<FMT, NB>(cs, xs, xs + kSOff, sm, wr, lane, tiles, acc);
             __syncwarp();
             if (lane == 0) {
@@ -808,8 +812,15 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
             if (++cslot == ring) { cslot = 0; ++cwrap; }
             if (++xslot == kXRing) { xslot = 0; ++xwrap; }
         }
-        left -= d.k1 - d.k0;
+        left -= count;
 
+        const Desc d = read_desc(&desc[u % kDescs]);
+        int out[NB];                                      // this lane's rows of y
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int i = 8 * nb + (lane >> 2), m = d.row0 + i;
+            out[nb] = i >= d.rows ? -1 : p.out_rows ? p.out_rows[m] : m;
+        }
         const int parts = d.last - d.first + 1;
         if (!waited) {
             grid_dep_wait();                              // counters and the adapters' terms come from the kernels before
@@ -1006,7 +1017,7 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, prep_kernel<FMT>, q);
+    cudaError_t e = q.ad.row ? cudaLaunchKernelEx(&cfg, prep_kernel<FMT, true>, q) : cudaLaunchKernelEx(&cfg, prep_kernel<FMT, false>, q);
     if (e != cudaSuccess) return e;
     if (a.z) {
         e = launch_expand(a.ad, a.order, a.R, const_cast<float*>(a.z), a.ldz, st);
