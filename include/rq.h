@@ -329,8 +329,8 @@ int rq_route_topk(const void *logits, int logits_type, int T, int E, int k, int 
                   void *workspace, size_t workspace_bytes, void *stream);
 
 /* out[t] = sum_j weights[t][j] * y[t k + j] over the j with ids[t][j] >= 0, in
- * ascending j in fp32 (rows of y whose ids is negative are not read; a token
- * with none gets zeros).
+ * ascending j in fp32 (what the rows of y whose ids is negative hold does not
+ * matter; a token with none gets zeros).
  *   y  device fp32 or bf16 [T k][N] (y_type): the products written with
  *      out_rows = slots;  out  device fp32 or bf16 [T][N] (out_type) */
 int rq_route_combine(const void *y, int y_type, const int *ids, const float *weights, int T, int N, int k, void *out,

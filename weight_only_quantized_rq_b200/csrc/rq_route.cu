@@ -85,11 +85,11 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, int lane, int&
     if (my_id >= 0) my_w = my_w / den;
 }
 
-// Places a block's pairs [i0, i1) by expert: one warp, 32 pairs at a time in
-// order, at[e] the next free row of expert e.
-__device__ __forceinline__ void place(const RouteArgs& a, int* at, int i0, int i1, int lane) {
-    for (int i = i0; i < i1; i += 32) {
-        const int e = i + lane < i1 ? a.ids[i + lane] : -1;
+// Places a block's pairs i0 .. i0 + n - 1 by expert: one warp, 32 pairs at a
+// time in order, ids in shared memory, at[e] the next free row of expert e.
+__device__ __forceinline__ void place(const RouteArgs& a, int* at, const int* ids, int i0, int n, int lane) {
+    for (int i = 0; i < n; i += 32) {
+        const int e = i + lane < n ? ids[i + lane] : -1;
         const unsigned same = __match_any_sync(~0u, e);
         const int before = __popc(same & ((1u << lane) - 1u));
         int row = 0;
@@ -98,8 +98,8 @@ __device__ __forceinline__ void place(const RouteArgs& a, int* at, int i0, int i
         if (e >= 0 && before == 0) at[e] += __popc(same);
         __syncwarp();
         if (e >= 0) {
-            a.in_rows[row] = (i + lane) / a.k;
-            a.slots[row] = i + lane;
+            a.in_rows[row] = (i0 + i + lane) / a.k;
+            a.slots[row] = i0 + i + lane;
         }
     }
 }
@@ -126,6 +126,7 @@ __device__ __forceinline__ int scan_warp(int* v, int E, int lane) {
 template <int V>
 __global__ void __launch_bounds__(kRouteThreads) choose_kernel(RouteArgs a, int per) {
     __shared__ int count[1024];
+    __shared__ int chosen[kOneBlock * 16];               // with one block: the ids
     const int tid = threadIdx.x, lane = tid & 31;
     for (int e = tid; e < a.E; e += blockDim.x) count[e] = 0;
     grid_dep_wait();
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(kRouteThreads) choose_kernel(RouteArgs a, int 
         if (lane < a.k) {
             a.ids[(size_t)t * a.k + lane] = id;
             a.weights[(size_t)t * a.k + lane] = w;
+            if (gridDim.x == 1) chosen[t * a.k + lane] = id;
             if (id >= 0) atomicAdd(&count[id], 1);
         }
     }
@@ -154,30 +156,33 @@ __global__ void __launch_bounds__(kRouteThreads) choose_kernel(RouteArgs a, int 
         if (lane == 0) total = n;
         for (int e = lane; e <= a.E; e += 32) a.offsets[e] = e < a.E ? count[e] : n;
         __syncwarp();
-        place(a, count, 0, P, lane);
+        place(a, count, chosen, 0, P, lane);
     }
     __syncthreads();
     for (int i = total + tid; i < P; i += blockDim.x) a.in_rows[i] = a.slots[i] = -1;
 }
 
-constexpr int kPlaceThreads = 256;
+constexpr int kPlaceThreads = 1024;
 
 __global__ void __launch_bounds__(kPlaceThreads) place_kernel(RouteArgs a, int per) {
-    extern __shared__ int sm[];                          // at[E], then before[E] summed over threads
+    extern __shared__ int sm[];                          // at[E] and before[E] summed over threads, then the block's ids
     int* at = sm;
     int* before = sm + a.E;
+    int* ids = sm + 2 * a.E;
     const int tid = threadIdx.x, lane = tid & 31, nb = gridDim.x;
     for (int e = tid; e < 2 * a.E; e += kPlaceThreads) sm[e] = 0;
     grid_dep_wait();
     grid_dep_launch();
     __syncthreads();
     const int* c = static_cast<const int*>(a.ws);
+    const int i0 = blockIdx.x * per * a.k, n = min(a.T * a.k - i0, per * a.k);
+    for (int i = tid; i < n; i += kPlaceThreads) ids[i] = a.ids[i0 + i];
     // several threads per expert while there are fewer experts than threads
     const int ways = a.E >= kPlaceThreads ? 1 : kPlaceThreads / a.E;
     for (int x = tid; x < ways * a.E; x += kPlaceThreads) {
         const int e = x % a.E;
         int all = 0, low = 0;
-#pragma unroll 8
+#pragma unroll 16
         for (int b = x / a.E; b < nb; b += ways) {
             const int v = c[(size_t)b * a.E + e];
             all += v;
@@ -190,72 +195,91 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(RouteArgs a, int p
     __shared__ int total;
     const int P = a.T * a.k;
     if (tid < 32) {
-        const int n = scan_warp(at, a.E, lane);
-        if (lane == 0) total = n;
+        const int all = scan_warp(at, a.E, lane);
+        if (lane == 0) total = all;
         if (blockIdx.x == 0)
-            for (int e = lane; e <= a.E; e += 32) a.offsets[e] = e < a.E ? at[e] : n;
+            for (int e = lane; e <= a.E; e += 32) a.offsets[e] = e < a.E ? at[e] : all;
         __syncwarp();
         for (int e = lane; e < a.E; e += 32) at[e] += before[e];
         __syncwarp();
-        const int t0 = blockIdx.x * per;
-        place(a, at, t0 * a.k, min(a.T, t0 + per) * a.k, lane);
+        place(a, at, ids, i0, n, lane);
     }
     __syncthreads();
     for (int i = total + (int)blockIdx.x * kPlaceThreads + tid; i < P; i += nb * kPlaceThreads) a.in_rows[i] = a.slots[i] = -1;
 }
 
 // ---------------------------------------------------------------- combine
+// Eight consecutive values of y as they lie in memory.
 template <bool YB>
-__device__ __forceinline__ void load8(const void* y, size_t i, float (&v)[8]) {
-    if constexpr (YB) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(y) + i));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) { v[2 * q] = bf16lo_f32(w[q]); v[2 * q + 1] = bf16hi_f32(w[q]); }
-    } else {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(y) + i);
-        const float4 a = __ldcs(f), b = __ldcs(f + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+struct Raw8 {
+    uint4 a[YB ? 1 : 2];
+    __device__ __forceinline__ void load(const void* y, size_t i) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(y) + i * (YB ? 2 : 4));
+        a[0] = __ldcs(p);
+        if (!YB) a[YB ? 0 : 1] = __ldcs(p + 1);
     }
-}
+    __device__ __forceinline__ float at(int q) const {
+        const uint4 v = a[YB ? 0 : q >> 2];
+        const int i = YB ? q >> 1 : q & 3;
+        const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+        return !YB ? __uint_as_float(w) : q & 1 ? bf16hi_f32(w) : bf16lo_f32(w);
+    }
+};
 
-// Eight columns of a token per thread (N a multiple of 8), two choices'
-// loads at a time.
+// A block takes 512 vectors of eight columns of one token (N a multiple of 8):
+// two per thread, with two choices' loads of both in flight.
+constexpr int kCombineVecs = 512;
+
 template <bool YB, bool OB>
-__global__ void __launch_bounds__(256) combine8_kernel(CombineArgs a) {
+__global__ void __launch_bounds__(256) combine8_kernel(CombineArgs a, int chunks) {
     grid_dep_wait();
     grid_dep_launch();
-    const int per = a.N / 8;                             // vectors of a row
-    const long long n = (long long)a.T * per;
-    for (long long x = (long long)blockIdx.x * 256 + threadIdx.x; x < n; x += (long long)gridDim.x * 256) {
-        const int t = (int)(x / per), c = (int)(x - (long long)t * per) * 8;
-        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        for (int j = 0; j < a.k; j += 2) {
-            const size_t p = (size_t)t * a.k + j;
-            const bool on0 = __ldg(a.ids + p) >= 0, on1 = j + 1 < a.k && __ldg(a.ids + p + 1) >= 0;
-            float v0[8], v1[8];
-            if (on0) load8<YB>(a.y, p * a.N + c, v0);
-            if (on1) load8<YB>(a.y, (p + 1) * a.N + c, v1);
-            const float w0 = on0 ? __ldg(a.weights + p) : 0.0f, w1 = on1 ? __ldg(a.weights + p + 1) : 0.0f;
+    const int per = a.N / 8, t = blockIdx.x / chunks, v0 = (blockIdx.x - t * chunks) * kCombineVecs + threadIdx.x;
+    const size_t row = (size_t)t * a.k;
+    float s[2][8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                if (on0) s[q] = fmaf(w0, v0[q], s[q]);
-                if (on1) s[q] = fmaf(w1, v1[q], s[q]);
-            }
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s[h][q] = 0.0f;
+    for (int j = 0; j < a.k; j += 2) {
+        // The rows are loaded beside their ids, not after them (what a row without an expert holds is dropped), and
+        // all loads are unconditional (a choice or column past the end reads the last one).
+        Raw8<YB> v[2][2];
+        bool on[2];
+        float w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[i][h].load(a.y, (row + min(j + i, a.k - 1)) * a.N + 8 * min(v0 + 256 * h, per - 1));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            on[i] = __ldg(a.ids + row + min(j + i, a.k - 1)) >= 0 && j + i < a.k;
+            w[i] = __ldg(a.weights + row + min(j + i, a.k - 1));
         }
-        const size_t o = (size_t)t * a.N + c;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (on[i])
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) s[h][q] = fmaf(w[i], v[i][h].at(q), s[h][q]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (v0 + 256 * h >= per) break;
+        const size_t o = (size_t)t * a.N + 8 * (v0 + 256 * h);
         if constexpr (OB) {
             uint32_t u[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * q], s[2 * q + 1]);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(s[h][2 * q], s[h][2 * q + 1]);
                 u[q] = *reinterpret_cast<const uint32_t*>(&b);
             }
             *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o) = make_uint4(u[0], u[1], u[2], u[3]);
         } else {
             float4* f = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o);
-            f[0] = make_float4(s[0], s[1], s[2], s[3]);
-            f[1] = make_float4(s[4], s[5], s[6], s[7]);
+            f[0] = make_float4(s[h][0], s[h][1], s[h][2], s[h][3]);
+            f[1] = make_float4(s[h][4], s[h][5], s[h][6], s[h][7]);
         }
     }
 }
@@ -321,19 +345,20 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
                         : v <= 16 ? launch(choose_kernel<16>, blocks, threads, 0, st, a, per)
                                   : launch(choose_kernel<32>, blocks, threads, 0, st, a, per);
     if (e != cudaSuccess || blocks == 1) return e;
-    return launch(place_kernel, blocks, kPlaceThreads, (size_t)2 * a.E * 4, st, a, per);
+    return launch(place_kernel, blocks, kPlaceThreads, (size_t)(2 * a.E + per * a.k) * 4, st, a, per);
 }
 
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st) {
-    const bool wide = a.N % 8 == 0;
-    const long long n = (long long)a.T * (wide ? a.N / 8 : a.N);
-    const long long want = (n + 255) / 256, most = (long long)sm_count() * 64;
-    const int grid = (int)(want < most ? want : most);
-    if (!wide) return launch(combine1_kernel, grid, 256, 0, st, a);
-    if (a.ybf16) return a.obf16 ? launch(combine8_kernel<true, true>, grid, 256, 0, st, a)
-                                : launch(combine8_kernel<true, false>, grid, 256, 0, st, a);
-    return a.obf16 ? launch(combine8_kernel<false, true>, grid, 256, 0, st, a)
-                   : launch(combine8_kernel<false, false>, grid, 256, 0, st, a);
+    const int chunks = (a.N / 8 + kCombineVecs - 1) / kCombineVecs;
+    if (a.N % 8 || (long long)a.T * chunks > 0x7fffffff) {
+        const long long want = ((long long)a.T * a.N + 255) / 256, most = (long long)sm_count() * 64;
+        return launch(combine1_kernel, (int)(want < most ? want : most), 256, 0, st, a);
+    }
+    const int grid = a.T * chunks;
+    if (a.ybf16) return a.obf16 ? launch(combine8_kernel<true, true>, grid, 256, 0, st, a, chunks)
+                                : launch(combine8_kernel<true, false>, grid, 256, 0, st, a, chunks);
+    return a.obf16 ? launch(combine8_kernel<false, true>, grid, 256, 0, st, a, chunks)
+                   : launch(combine8_kernel<false, false>, grid, 256, 0, st, a, chunks);
 }
 
 }  // namespace rq

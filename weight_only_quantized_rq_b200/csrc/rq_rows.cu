@@ -928,7 +928,7 @@ constexpr int kMaxCtas = 768;          // CTAs of a launch at most
 // group with more rows than a unit holds streams its weights once per unit.
 int pick_nb(int R, int E) {
     const int per = (R + E - 1) / E;
-    return R <= 8 || per <= 3 ? 1 : per <= 12 ? 2 : 4;
+    return R <= 8 || per <= 4 ? 1 : per <= 12 ? 2 : 4;
 }
 
 struct Layout { size_t xf, part, count, total; int tiles, T; };

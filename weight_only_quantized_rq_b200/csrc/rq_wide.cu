@@ -43,13 +43,13 @@ constexpr int kTiles = 2;               // weight tiles of a unit; warps 8 t .. 
                                         // the first 64 of each 128 K, four the others
 constexpr int kUnitRows = kTiles * kTcRows;
 constexpr int kWideThreads = 32 * (kWorkers + 4);
-constexpr int kMaxX = 6;                // activation slots at most (128 K each)
-constexpr int kCodeSlots = 2;
+constexpr int kMaxX = 4;                // activation slots at most (128 K each)
+constexpr int kMaxCodes = 4;            // code slots at most
 constexpr int kDescs = 8;
 constexpr size_t kWideSmem = 226 * 1024;
 constexpr int kWideMaxCtas = 256;
 constexpr int kA = 4;                   // A slots: 128 K of one tile, 64 columns
-constexpr int kBarBytes = (2 * kCodeSlots + 2 * kMaxX + 2 * kA + kDescs + 4 * 2 + 3) * 8;
+constexpr int kBarBytes = (2 * kMaxCodes + 2 * kMaxX + 2 * kA + kDescs + 4 * 2 + 3) * 8;
 
 template <int FMT>
 struct Wide {
@@ -57,8 +57,8 @@ struct Wide {
     static constexpr int RB = FMT == kFmtW4G64 || is_w8(FMT) ? 128 : FMT == kFmtW6G16 ? 96 : sb_record(FMT);
     static constexpr int CB = (kUnitRows * RB + 1023) & ~1023;
     static constexpr int PAIRS = KS / 128;                                        // 128-K steps of a stage
-    // order of a row's values within 8 (1: 0 4 1 5 2 6 3 7) or 4 (2: 0 2 1 3)
-    static constexpr int ORDER = is_sb(FMT) ? 0 : is_w8(FMT) ? 2 : 1;
+    // order of a row's values: within 8 (1: 0 4 1 5 2 6 3 7) or within 4 (2: 0 2 1 3)
+    static constexpr int ORDER = is_w8(FMT) ? 2 : 1;
 };
 
 struct WidePlan {
@@ -81,7 +81,7 @@ struct WideParams {
     int Ty, act;
     const float* z;                     // [R][ldz] the adapters' term, or NULL
     int ldz;
-    int xslots;
+    int xslots, cslots;
     unsigned long long wait_ns;
     int test_flags;
 };
@@ -102,8 +102,7 @@ __device__ __forceinline__ uint4 lay8(uint4 v, float f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = half2_bits(bf16lo_f32(w[i]) * f, bf16hi_f32(w[i]) * f);
     if (ORDER == 1) return make_uint4(prmt(h[0], h[2], 0x5410u), prmt(h[0], h[2], 0x7632u), prmt(h[1], h[3], 0x5410u), prmt(h[1], h[3], 0x7632u));
-    if (ORDER == 2) return make_uint4(prmt(h[0], h[1], 0x5410u), prmt(h[0], h[1], 0x7632u), prmt(h[2], h[3], 0x5410u), prmt(h[2], h[3], 0x7632u));
-    return make_uint4(h[0], h[1], h[2], h[3]);
+    return make_uint4(prmt(h[0], h[1], 0x5410u), prmt(h[0], h[1], 0x7632u), prmt(h[2], h[3], 0x5410u), prmt(h[2], h[3], 0x7632u));
 }
 __device__ __forceinline__ uint32_t top8(uint4 v) {
     const uint32_t m = 0x7fff7fffu;
@@ -357,15 +356,16 @@ __device__ __forceinline__ void unpack_atom(uint32_t cs, int at, int sw, const u
             }
         }
     } else {
-        // S u - M in fp32, S = d sc and M = dmin m exact, then one rounding
+        // u exactly, then S u - M in one step with S = d sc and M = dmin m rounded to fp16 (2^-12 each): about
+        // 3.5e-4 of a weight, a fifth of the result's own rounding, for half the operations of fp32
         const uint4 hd = lds4(cs);
         const float d = __half2float(__ushort_as_half((uint16_t)(hd.x & 0xffffu)));
         const float dm = __half2float(__ushort_as_half((uint16_t)(hd.x >> 16)));
 #pragma unroll
         for (int gl = 0; gl < 2; ++gl) {
             const int j = 2 * at + gl;
-            const float S = __fmul_rn(d, (float)sb_field(hd.y, hd.z, hd.w, 0, j));
-            const float c = __fmaf_rn(-128.0f, S, -__fmul_rn(dm, (float)sb_field(hd.y, hd.z, hd.w, 1, j)));
+            const uint32_t S = half2_bits(d * (float)sb_field(hd.y, hd.z, hd.w, 0, j), 0.0f) * 0x10001u;
+            const uint32_t M = half2_bits(-dm * (float)sb_field(hd.y, hd.z, hd.w, 1, j), 0.0f) * 0x10001u;
             const uint4 cw = lds4(cs + 16 + 16 * j);
             const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
             uint32_t pl[2] = {0u, 0u};
@@ -376,23 +376,27 @@ __device__ __forceinline__ void unpack_atom(uint32_t cs, int at, int sw, const u
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t lo = w[i] & 0x0F0F0F0Fu, hi = (w[i] >> 4) & 0x0F0F0F0Fu;        // weights 0 2 4 6 / 1 3 5 7
-                if constexpr (FMT == kFmtW5SB32) {
-                    const uint32_t pb = pl[0] >> (8 * i);                                 // bit k of weight k to bit 4 of its byte
-                    lo |= ((pb & 0x55u) * 0x00410410u) & 0x10101010u;
-                    hi |= (((pb >> 1) & 0x55u) * 0x00410410u) & 0x10101010u;
-                } else if constexpr (FMT == kFmtW6SB32) {
-                    const uint32_t pb = (pl[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-                    const uint32_t e = pb & 0x3333u, f = (pb >> 2) & 0x3333u;
-                    lo |= prmt(e << 4, e, 0x5140u) & 0x30303030u;
-                    hi |= prmt(f << 4, f, 0x5140u) & 0x30303030u;
+                uint32_t u[4];
+                if constexpr (FMT == kFmtW4SB32) {
+                    const uint32_t v = w[i] >> 8;
+                    u[0] = hadd2(and_or(w[i], 0x000F000Fu, 0x64006400u), 0xE400E400u);
+                    u[1] = hfma2(and_or(w[i], 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD400D400u);
+                    u[2] = hadd2(and_or(v, 0x000F000Fu, 0x64006400u), 0xE400E400u);
+                    u[3] = hfma2(and_or(v, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD400D400u);
+                } else {
+                    // the higher bits of weights k and k + 4 to bits 4 and 20 on
+                    constexpr int B = FMT == kFmtW5SB32 ? 1 : 2;
+                    constexpr uint32_t HM = B == 1 ? 0x00100010u : 0x00300030u;
+                    uint32_t h = B == 1 ? (pl[0] >> (8 * i)) & 0xffu : (pl[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+                    h |= h << (B == 1 ? 12 : 8);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t hs = 4 - B * q >= 0 ? h << (4 - B * q < 0 ? 0 : 4 - B * q) : h >> (B * q - 4 < 0 ? 0 : B * q - 4);
+                        u[q] = hadd2(and_or(hs, HM, and_or(w[i] >> (4 * q), 0x000F000Fu, 0x64006400u)), 0xE400E400u);
+                    }
                 }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float a = __uint_as_float(prmt(lo, kW4Magic, 0x7044u + 0x100u * q));   // 128 + u
-                    const float b = __uint_as_float(prmt(hi, kW4Magic, 0x7044u + 0x100u * q));
-                    o[16 * gl + 4 * i + q] = half2_bits(__fmaf_rn(a, S, c), __fmaf_rn(b, S, c));
-                }
+                for (int q = 0; q < 4; ++q) o[16 * gl + 4 * i + q] = hfma2(u[q], S, M);
             }
         }
     }
@@ -435,15 +439,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     static_assert(A0 + 64 * kA <= 512, "tensor memory");
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int NX = p.xslots;
-    uint8_t* at = smem + kCodeSlots * G::CB + (size_t)NX * MC * 256;
+    const int NX = p.xslots, NC = p.cslots;
+    uint8_t* at = smem + NC * G::CB + (size_t)NX * MC * 256;
     WDesc* desc = reinterpret_cast<WDesc*>(at);
     at += kDescs * sizeof(WDesc);
     RowInfo* rowinfo = reinterpret_cast<RowInfo*>(at) + (warp & (kWorkers - 1)) * (MC / 2);
     at += kWorkers * (MC / 2) * sizeof(RowInfo);
     uint64_t* cfull = reinterpret_cast<uint64_t*>(at);
-    uint64_t* cempty = cfull + kCodeSlots;
-    uint64_t* xfull = cempty + kCodeSlots;
+    uint64_t* cempty = cfull + kMaxCodes;
+    uint64_t* xfull = cempty + kMaxCodes;
     uint64_t* xempty = xfull + kMaxX;
     uint64_t* afull = xempty + kMaxX;
     uint64_t* aempty = afull + kA;
@@ -459,7 +463,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     g.ctas = g.row + p.pl.E + 1;
 
     if (tid == 0) {
-        for (int s = 0; s < kCodeSlots; ++s) {
+        for (int s = 0; s < NC; ++s) {
             mbar_init(&cfull[s], 1);
             mbar_init(&cempty[s], kWorkers);
         }
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     grid_dep_launch();
 
     const int T = p.pl.T;
-    const uint32_t cbase = smem_u32(smem), xbase = cbase + kCodeSlots * G::CB;
+    const uint32_t cbase = smem_u32(smem), xbase = cbase + NC * G::CB;
     auto wait = [&](uint64_t* bar, int phase, unsigned flag) {
         return __all_sync(~0u, mbar_try_wait(bar, (uint32_t)phase & 1u)) ||
                __all_sync(~0u, mbar_wait_bounded(bar, (uint32_t)phase & 1u, flag, 0u, p.wait_ns));
@@ -549,11 +553,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                     mbar_arrive_expect_tx(&cfull[cs], (uint32_t)(kUnitRows * G::RB));
                     tma_2d(cbase + cs * G::CB, &p.cmap, k * G::RB, d.wrow, &cfull[cs]);
                     ++issued;
-                    if (++cs == kCodeSlots) { cs = 0; ++cwrap; }
+                    if (++cs == NC) { cs = 0; ++cwrap; }
                 }
             }
-            for (int q = 0; q < kCodeSlots && q < issued; ++q)
-                mbar_wait_bounded(&cfull[q], (uint32_t)(issued / kCodeSlots + (q < issued % kCodeSlots ? 1 : 0) - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
+            for (int q = 0; q < NC && q < issued; ++q)
+                mbar_wait_bounded(&cfull[q], (uint32_t)(issued / NC + (q < issued % NC ? 1 : 0) - 1) & 1u, kStatusTmaWait, 64u, p.wait_ns);
         }
         __syncwarp();
     } else if (warp >= kWorkers) {
@@ -629,7 +633,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                     as += kTiles;
                     if (as >= kA) { as = tile; ++awrap; }
                 }
-                if (++cs == kCodeSlots) { cs = 0; ++cwrap; }
+                if (++cs == NC) { cs = 0; ++cwrap; }
             }
             if (!ok) break;
             if (!waited) {
@@ -793,10 +797,13 @@ int wide_mc(int R, int E, int N) {
 template <int FMT, int MC>
 cudaError_t launch_wide_mc(const RowsArgs& a, WideParams& p, cudaStream_t st) {
     using G = Wide<FMT>;
-    const size_t fixed = kCodeSlots * G::CB + kDescs * sizeof(WDesc) + kWorkers * (MC / 2) * sizeof(RowInfo) + kBarBytes + wgroups_bytes(a.E);
-    p.xslots = (int)((kWideSmem - fixed) / (MC * 256));
-    if (p.xslots > kMaxX) p.xslots = kMaxX;
-    if (p.xslots < 2) return cudaErrorInvalidValue;
+    const size_t fixed = kDescs * sizeof(WDesc) + kWorkers * (MC / 2) * sizeof(RowInfo) + kBarBytes + wgroups_bytes(a.E);
+    p.xslots = kMaxX;
+    auto codes = [&]() { return (int)((kWideSmem - fixed - (size_t)p.xslots * MC * 256) / G::CB); };
+    if (fixed + (size_t)p.xslots * MC * 256 + 2 * (size_t)G::CB > kWideSmem) p.xslots = 2;   // wide codes, many experts
+    p.cslots = codes();
+    if (p.cslots > kMaxCodes) p.cslots = kMaxCodes;
+    if (p.cslots < 2) return cudaErrorInvalidValue;
     auto kern = wide_kernel<FMT, MC>;
     static unsigned long long attr_done = 0ull;
     int dev = 0;
@@ -812,7 +819,7 @@ cudaError_t launch_wide_mc(const RowsArgs& a, WideParams& p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms < kWideMaxCtas ? sms : kWideMaxCtas));
     cfg.blockDim = dim3(kWideThreads);
-    cfg.dynamicSmemBytes = fixed + (size_t)p.xslots * MC * 256;
+    cfg.dynamicSmemBytes = fixed + (size_t)p.xslots * MC * 256 + (size_t)p.cslots * G::CB;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
