@@ -21,7 +21,7 @@ namespace rq {
 namespace {
 
 constexpr int kRouteThreads = 1024;
-constexpr int kMaxBlocks = 256;
+constexpr int kMaxBlocks = 128;                        // a lane of a warp sums four of them
 constexpr int kOneBlock = 64;
 
 // fp32 as an unsigned key with the same order; 0 for a logit that is never
@@ -146,7 +146,9 @@ __global__ void __launch_bounds__(kRouteThreads) choose_kernel(RouteArgs a, int 
     }
     __syncthreads();
     if (gridDim.x > 1) {
-        for (int e = tid; e < a.E; e += blockDim.x) static_cast<int*>(a.ws)[(size_t)blockIdx.x * a.E + e] = count[e];
+        // an expert's counts lie together; a token counts once for an expert, so that 16 bits hold a block's
+        for (int e = tid; e < a.E; e += blockDim.x)
+            static_cast<uint16_t*>(a.ws)[(size_t)e * kMaxBlocks + blockIdx.x] = (uint16_t)count[e];
         return;
     }
     const int P = a.T * a.k;
@@ -165,31 +167,32 @@ __global__ void __launch_bounds__(kRouteThreads) choose_kernel(RouteArgs a, int 
 constexpr int kPlaceThreads = 1024;
 
 __global__ void __launch_bounds__(kPlaceThreads) place_kernel(RouteArgs a, int per) {
-    extern __shared__ int sm[];                          // at[E] and before[E] summed over threads, then the block's ids
+    extern __shared__ int sm[];                          // per expert: all blocks' sum, the sum before this block; the block's ids
     int* at = sm;
     int* before = sm + a.E;
     int* ids = sm + 2 * a.E;
     const int tid = threadIdx.x, lane = tid & 31, nb = gridDim.x;
-    for (int e = tid; e < 2 * a.E; e += kPlaceThreads) sm[e] = 0;
     grid_dep_wait();
     grid_dep_launch();
-    __syncthreads();
-    const int* c = static_cast<const int*>(a.ws);
     const int i0 = blockIdx.x * per * a.k, n = min(a.T * a.k - i0, per * a.k);
     for (int i = tid; i < n; i += kPlaceThreads) ids[i] = a.ids[i0 + i];
-    // several threads per expert while there are fewer experts than threads
-    const int ways = a.E >= kPlaceThreads ? 1 : kPlaceThreads / a.E;
-    for (int x = tid; x < ways * a.E; x += kPlaceThreads) {
-        const int e = x % a.E;
+    // a warp per expert, four blocks' counts per lane
+#pragma unroll 4
+    for (int e = tid >> 5; e < a.E; e += kPlaceThreads / 32) {
+        const uint2 c = static_cast<const uint2*>(a.ws)[(size_t)e * (kMaxBlocks / 4) + lane];
+        const int v[4] = {(int)(c.x & 0xffff), (int)(c.x >> 16), (int)(c.y & 0xffff), (int)(c.y >> 16)};
         int all = 0, low = 0;
-#pragma unroll 16
-        for (int b = x / a.E; b < nb; b += ways) {
-            const int v = c[(size_t)b * a.E + e];
-            all += v;
-            if (b < (int)blockIdx.x) low += v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (4 * lane + i < nb) all += v[i];
+            if (4 * lane + i < (int)blockIdx.x) low += v[i];
         }
-        atomicAdd(&at[e], all);
-        atomicAdd(&before[e], low);
+        all = __reduce_add_sync(~0u, all);
+        low = __reduce_add_sync(~0u, low);
+        if (lane == 0) {
+            at[e] = all;
+            before[e] = low;
+        }
     }
     __syncthreads();
     __shared__ int total;
@@ -329,8 +332,7 @@ int tokens_per_block(int T) {
 }  // namespace
 
 size_t route_workspace(int T, int E, int) {
-    const int per = tokens_per_block(T);
-    return round16((size_t)((T + per - 1) / per) * E * 4);
+    return T <= kOneBlock ? 16 : round16((size_t)E * kMaxBlocks * 2);
 }
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
