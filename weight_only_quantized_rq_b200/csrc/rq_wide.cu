@@ -207,13 +207,20 @@ __device__ __forceinline__ void scan_wide(const WidePlan& pl, WGroups g, int lan
         base += __shfl_sync(~0u, c, 31);
         units += __shfl_sync(~0u, un, 31);
     }
-    // Cutting a unit into p parts takes its K loop (about 0.65 us per 128 K) down to a p-th and costs about
-    // 0.5 us per part and 2.5 more per 128 rows to sum them: p = the root of the two's ratio, where the
-    // units alone do not fill the SMs.
+    // A unit's K loop takes about 0.65 us per 128 K, and summing the parts of a cut unit 0.5 us per part and 2.5 more
+    // per 128 rows. Units that do not fill the SMs are either cut into p equal parts each (p = the root of the two's
+    // ratio, as far as there are SMs), or shared out evenly over all SMs, most of which then have parts of two units to
+    // sum (4 us more). 80 units of 10 stages: whole 50.0, in even shares 57.7 us.
     if (lane == 0) {
         const float loop = 0.65f * (float)((pl.K + 127) / 128), part = 0.5f + 2.5f / 128.0f * (float)min(pl.MC, (top + pl.E - 1) / pl.E);
-        const long long want = units * max(1, (int)(sqrtf(loop / part) + 0.5f));
-        *g.ctas = (int)min((long long)gridDim.x, max(1ll, want));
+        const int G = (int)gridDim.x;
+        int ctas = G;
+        if (units < G) {
+            const int p = max(1, min(G / (int)max(units, 1ll), (int)(sqrtf(loop / part) + 0.5f)));
+            const float even = (float)G / (float)max(units, 1ll);        // parts of a unit in even shares
+            if (loop / (float)p + (p > 1 ? part * (float)p : 0.0f) < loop / even + part * (even + 1.0f) + 4.0f) ctas = max(1, (int)units * p);
+        }
+        *g.ctas = ctas;
     }
     __syncwarp();
 }
