@@ -139,8 +139,12 @@ struct RowsArgs {
 size_t rows_workspace(int fmt, int R, int K, int E);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st);
 
-// The grouped products for groups of many rows, bf16 results (rq_wide.cu).
-inline bool wide_rows(int R, int E) { return R >= 32 * E; }
+// The products for groups of many rows, bf16 results (rq_wide.cu): from 16 rows
+// per group on average. w4g64, 8 experts, K 2048, N 8192, this way and rq_rows.cu's:
+// 12 rows 36.0 and 35.2 us, 16 rows 36.9 and 39.1, 32 rows 41.7 and 54.0; w8g16,
+// K 8192, N 2048, 16 rows 42 and 60; with adapters (w4g64, 4096 x 4096) 16 rows
+// 21.3 and 22.6, 32 rows 23.3 and 26.6.
+inline bool wide_rows(int R, int E) { return R >= 16 * E; }
 size_t wide_workspace(int R, int K, int E);
 cudaError_t launch_wide(const RowsArgs& a, cudaStream_t st);
 

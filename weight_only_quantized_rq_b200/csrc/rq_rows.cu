@@ -1,6 +1,7 @@
 // rq_rows.cu -- packed products whose weights depend on the activation row:
 // products grouped by expert with ragged sizes, and a low-rank adapter per row
-// beside a shared packed projection.
+// beside a shared packed projection. fp32 results, and bf16 ones of groups with
+// few rows (rq_wide.cu makes those of many rows).
 //
 //   grouped  y[i] = act(x[in(i)] W_e^T),            i in [offsets[e], offsets[e + 1])
 //   adapter  y[m] = x[m] W^T + s_a B_a (A_a x[m]),  a = row_adapter[m]
@@ -11,18 +12,18 @@
 //   eight rows (the last one padded with zeros), each tile as the B fragments
 //   of mma.m16n8k16 in the order that the weights' codes unpack in, so that the
 //   product kernel reads 16 bytes per lane with no bank conflict and no
-//   permutation. For the superblock formats it adds each row's sums over the
-//   32-weight groups (w = S u - M needs sum x). It clears the split counters,
-//   and for adapters it also computes t = s_a A_a x[m] in fp32. It lets the
-//   product kernel start once its own predecessors are done, so the product's
-//   weight copies run while prep works.
+//   permutation. For codes below a byte it adds what the sums start from,
+//   -OFF sum x per weight group (codes unpack as OFF + q, and w = S u - M needs
+//   sum x besides). It clears the counters of the cut units, and up to eight
+//   rows with adapters it computes t = s_a A_a x[m] in fp32. The product kernel
+//   starts beside it: its weight copies run while prep works.
 //
 // rows_kernel  multiplies. Bound by the weight stream while a group has few
 //   rows: what has to be read is the packed plane of each expert in use.
 //   * Codes are exact small integers in bf16 (q, |q| <= 127; u <= 63 for the
 //     superblocks), x is bf16: every product is exact in the tensor core's
 //     fp32 sums, and the group's scale multiplies the fp32 group sum. So no
-//     weight is rounded, and fp32 results are good to fp32 (about 5e-7 on the
+//     weight is rounded, and fp32 results are good to fp32 (2e-7 on the
 //     sums here), unlike weights rounded to bf16 before the product (2e-3).
 //   * mma.sync, not tcgen05: with a handful of rows the products are not what
 //     counts. The A operand of mma.sync comes straight from the registers that
@@ -30,15 +31,23 @@
 //     applied; through tensor memory each 64-weight group would need its own
 //     accumulator and a read back (measured for this library's other kernel:
 //     1.9 against 2.4 TB/s).
-//   * A unit of work is 128 weight rows x K x up to 8 NB activation rows.
-//     Warps 0-3 take 32 weight rows each over the first half of every stage's
-//     K, warps 4-7 over the second half: 32 rows per warp halve the shared-
-//     memory reads of x against 16.
-//   * All units' K stages form one line that the CTAs (two per SM) share out
-//     evenly, so neither ragged groups nor few tiles leave SMs idle. A unit cut
-//     by a CTA border is summed through the workspace: each part is written,
-//     the last to arrive adds all parts in K order (the same bits whoever is
-//     last; nobody waits).
+//   * A unit of work is 128 weight rows x K x up to 8 NB activation rows. Four
+//     warps take 32 weight rows each, from the codes to y with no barrier among
+//     them (16 rows per warp would double the shared-memory reads of x); a
+//     fifth copies: codes by TMA through a ring of their own, activations and
+//     scales through two slots. Small CTAs, three or four per SM: one CTA's
+//     start and end run beside the others' stream (eight warps with barriers, two
+//     CTAs per SM: 66 against 51 us at the time for 141 MB of w4g64 codes and 4
+//     rows per expert).
+//   * All units' K stages form one line that the CTAs share out evenly, so
+//     neither ragged groups nor few tiles leave SMs idle. A unit cut by a CTA
+//     border is summed through the workspace: each part is written, the last to
+//     arrive adds all parts in K order (the same bits whoever is last; nobody
+//     waits).
+// Measured (both kernels, device time): 16 experts of w4g64, K 2048, N 8192, 4
+// rows each, 141 MB: 42 us, 3.4 TB/s; the stream alone takes 33 of it, the rest
+// is the front (7 us from the call to the first products) and the CTAs' uneven
+// ends. Two rows, 2 experts, 18 MB: 13 us.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -922,10 +931,11 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
 // ------------------------------------------------------------------ host
 constexpr int kMaxCtas = 768;          // CTAs of a launch at most
 
-// CTAs of a launch at most
-
 // 8-row tiles per unit: as many as an even split of the rows fills, since a
-// group with more rows than a unit holds streams its weights once per unit.
+// group with more rows than a unit holds streams its weights once per unit. One
+// tile up to four rows on average (w4g64, 64 rows of 16 experts: 42 us against
+// 44 with two; a group of up to 16 rows then streams twice, from the L2), since
+// a second tile costs a CTA per SM its registers and every stage its MMAs.
 int pick_nb(int R, int E) {
     const int per = (R + E - 1) / E;
     return R <= 8 || per <= 4 ? 1 : per <= 12 ? 2 : 4;

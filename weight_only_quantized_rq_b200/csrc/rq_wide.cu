@@ -20,6 +20,12 @@
 //   * Units are cut where an even share of the work (rows x K) ends, so every
 //     CTA (one per SM) has the same; a cut unit's parts are summed through the
 //     workspace in K order by whichever CTA arrives last.
+// Measured: 4096 rows of 8 experts, w4g64, K 2048, N 8192: 171 us, 802 TFLOP/s.
+// A unit takes 11.7 us of products (an atom's issue to issue 340 cycles, 256 of
+// them products: unpacking and the products share the shared memory's and the
+// tensor memory's ports), 1.4 to drain, 3.1 to move its sums out; without the
+// last 150 us. Not kept: the next unit's first stages unpacked before the sums
+// move out (185 us), sums stored 16 bytes at a time through more shuffles (176).
 // Roles: 16 unpacking warps (they also move the sums out), a warp per weight
 // tile that issues its MMAs (one warp alone issued for 380 of the 256 cycles
 // that the products of an atom take), one thread that copies codes and one
