@@ -278,7 +278,13 @@ size_t rq_grouped_workspace_size(int fmt, int R, int K, int N, int E);
  * A row whose in(i) is outside [0, T) is a row of zeros; one whose out(i) is
  * outside [0, Ty) is not stored. Two rows with the same out(i): one of the two
  * results is stored, element by element. A non-finite x value reaches the y
- * of its own rows only. */
+ * of its own rows only.
+ * fp32 results, and bf16 ones where R < 16 E, come from exact products (codes
+ * and bf16 x) summed in fp32. bf16 results where R >= 16 E come from weights
+ * rounded once to fp16 (2^-12 of the weight; for the superblocks S and M are
+ * rounded too, 2^-11 of S u + |M| in all, a hundredth of a code's step), which
+ * must stay below 65504 in magnitude, and from each row of x relative to its
+ * largest value (values below 2^-39 of it count as zero). */
 int rq_wgemm_grouped(const void *x, int T, int K, int N, const rq_packed *w, const rq_groups *g, void *y, int Ty,
                      int act, int out_type, void *workspace, size_t workspace_bytes, void *stream);
 
@@ -300,7 +306,8 @@ size_t rq_lora_workspace_size(int fmt, int M, int K, int N, int rank);
 
 /* y[m] = x[m] * w_hat^T + scales[a] * B_a (A_a x[m]), a = row_adapter[m]; a row
  * whose a is outside [0, n) has no adapter. Sums in fp32; A_a x[m] is kept in
- * fp32 between the two products.
+ * fp32 between the two products. What is infinite or NaN in an adapter reaches
+ * the rows that use it only. The product itself as rq_wgemm_grouped's with E 1.
  *   x  device bf16 [M][K], 1 <= M <= 2^20;  row_adapter device int32 [M]
  *   y  device [M][N], fp32 or bf16 by out_type, overwritten */
 int rq_wgemm_lora(const void *x, int M, int K, int N, const rq_packed *w, const rq_lora *ad, const int *row_adapter,

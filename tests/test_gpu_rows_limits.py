@@ -143,3 +143,68 @@ def test_same_row_read_by_many_and_rows_behind_stay(orc, dtype):
     ref = grouped_ref(x, What, E, off, src)
     check(y[torch.from_numpy(dst).long().to(DEV)], torch.stack([ref[i][0] for i in range(80)]), torch.stack([ref[i][1] for i in range(80)]), K)
     assert (y[:5] == 7.5).all() and (y[85:] == 7.5).all()
+
+
+@pytest.mark.parametrize("M,dtype", [(5, torch.float32), (20, torch.float32), (70, torch.bfloat16)])
+def test_lora_nonfinite_adapter_stays_with_its_rows(orc, M, dtype):
+    """Infinities and NaN in one adapter reach only the rows that use it, whatever shares a tile with them."""
+    K, N = 512, 136
+    w, _ = random_packed(orc, "w4g64", N, K, 55)
+    A, B, sc = adapters(4, 40, K, N, 55)
+    x, row = rows_of(M, K, 55), torch.arange(M, dtype=torch.int32, device=DEV) % 5 - 1
+    want = rq.rq_wgemm_lora(x, w, A, B, sc, row, out_dtype=dtype)
+    A[1, 3, 5], A[2, 39, 0], B[1, 7], B[2, :, 39], B[2, 100, 0] = float("nan"), float("inf"), float("inf"), -float("inf"), float("nan")
+    got = rq.rq_wgemm_lora(x, w, A, B, sc, row, out_dtype=dtype)
+    hit = (row == 1) | (row == 2)
+    assert torch.equal(got[~hit], want[~hit])
+    assert not torch.isfinite(got[row == 1][:, 7]).any() and not torch.isfinite(got[row == 2]).any()
+
+
+@pytest.mark.parametrize("fmt", ["w4sb32", "w6sb32"])
+def test_superblocks_that_cancel(orc, fmt):
+    """Weights S u - M far below M: many-row bf16 results are within 2^-11 of the sums of |x| (S u + |M|), as
+    S and M are rounded to fp16 (2^-12 each), fp32 results within fp32's bound of them."""
+    K, N, M, size = 512, 200, 96, {"w4sb32": 144, "w6sb32": 208}[fmt]
+    r = np.random.default_rng(56)
+    rec = r.integers(0, 256, (N, K // 256, size), dtype=np.uint8)
+    rec[..., 4:16] = 0xFF                               # group scales and minima at their largest
+    d = (r.uniform(0.5, 1.5, (N, K // 256)) * 1e-4).astype(np.float16)
+    def packed(dmin):
+        rec[..., :4] = np.stack([d, dmin.astype(np.float16)], -1).view(np.uint8)
+        codes = rec.reshape(-1).copy()
+        return codes, torch.from_numpy(np.asarray(orc.dequant(fmt, K, N, codes, None)).reshape(N, K)).to(DEV).double()
+    _, Su = packed(np.zeros_like(d))
+    codes, What = packed(d.astype(np.float32) * (7.5 if fmt == "w4sb32" else 31.5))
+    w = rq.Packed(rq.fmt_id(fmt), K, N, torch.from_numpy(codes).to(DEV), None)
+    x = rows_of(M, K, 56)
+    xd = x.double()
+    off = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+    wide = xd.abs() @ (Su + (Su - What).abs()).t()
+    for dtype in (torch.float32, torch.bfloat16):
+        y = rq.rq_wgemm_grouped(x, w, off, out_dtype=dtype)
+        check(y, xd @ What.t(), wide, K)
+
+
+def test_many_rows_with_indices_out_of_range_and_not_finite(orc):
+    """Many-row bf16 products: rows of x that do not exist, rows of y that do not, duplicates, infinities and NaN."""
+    E, N, K, R = 3, 264, 320, 150
+    w, What = random_packed(orc, "w8g64", E * N, K, 57)
+    x = rows_of(40, K, 57)
+    x[3, 7], x[9, 300] = float("inf"), float("nan")
+    r = np.random.default_rng(57)
+    src = r.integers(-2, 43, R).astype(np.int32)
+    dst = r.permutation(R + 10)[:R].astype(np.int32)
+    dst[::17] = -1
+    dst[5::31] = 1 << 30
+    raw = np.array([3, 70, 60, 400], np.int32)
+    off = np.minimum(np.maximum.accumulate(raw), R)
+    y = torch.full((R + 10, N), 7.5, dtype=torch.bfloat16, device=DEV)
+    t = lambda a: torch.from_numpy(a).to(DEV)
+    rq.rq_wgemm_grouped(x, w, t(raw), t(src), t(dst), y=y)
+    ref = grouped_ref(torch.where(torch.isfinite(x), x, 0), What, E, off, src)
+    stored = [i for i in sorted(ref) if 0 <= dst[i] < R + 10]
+    good, bad = [i for i in stored if src[i] not in (3, 9)], [i for i in stored if src[i] in (3, 9)]
+    check(y[[int(dst[i]) for i in good]], torch.stack([ref[i][0] for i in good]), torch.stack([ref[i][1] for i in good]), K)
+    assert bad and not torch.isfinite(y[[int(dst[i]) for i in bad]]).any()
+    rest = sorted(set(range(R + 10)) - {int(dst[i]) for i in stored})
+    assert (y[rest] == 7.5).all()

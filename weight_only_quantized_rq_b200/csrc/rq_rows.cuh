@@ -72,8 +72,9 @@ __device__ __forceinline__ void shrink8(const Adapters& p, const __nv_bfloat16* 
 }
 
 // Adds the adapters' term over ranks 32 c .. 32 c + 31 to one 8-row tile's
-// sums: for each adapter among the tile's rows D += B_a t^T, with t zero for
-// the other rows. t is split into three bf16 parts (24 bits), so that nothing
+// sums: for each adapter among the tile's rows D = B_a t^T with t zero for the
+// other rows, and D added to the adapter's own rows only (an infinite or NaN
+// B_a stays with them). t is split into three bf16 parts (24 bits), so that nothing
 // of it is lost to the tensor core's operand type. Lane 4 g + q holds ranks
 // 8 q .. 8 q + 7 of the chunk: of weight rows n + 8 i (i = 0..3) and of
 // activation row g, which is row m of the call (negative: none).
@@ -105,7 +106,8 @@ __device__ __forceinline__ void add_adapters(const Adapters& p, int m, int c, in
     while (todo) {
         const int src = __ffs(todo) - 1, aa = __shfl_sync(~0u, a, src), rk = __shfl_sync(~0u, rank, src);
         const bool same = a == aa;
-        todo &= ~__ballot_sync(~0u, same);
+        const unsigned with = __ballot_sync(~0u, same);
+        todo &= ~with;
         uint4 b[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -117,15 +119,22 @@ __device__ __forceinline__ void add_adapters(const Adapters& p, int m, int c, in
                 b[q] = make_uint4(cut(b[q].x, 0), cut(b[q].y, 2), cut(b[q].z, 4), cut(b[q].w, 6));
             }
         }
+        float d0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
             const uint32_t t0 = same ? t[s][0] : 0u, t1 = same ? t[s][1] : 0u, t2 = same ? t[s][2] : 0u, t3 = same ? t[s][3] : 0u;
             const uint32_t a0[4] = {b[0].x, b[1].x, b[0].y, b[1].y}, a1[4] = {b[2].x, b[3].x, b[2].y, b[3].y};
             const uint32_t a2[4] = {b[0].z, b[1].z, b[0].w, b[1].w}, a3[4] = {b[2].z, b[3].z, b[2].w, b[3].w};
-            mma16816(acc0, a0, t0, t1, acc0[0], acc0[1], acc0[2], acc0[3]);
-            mma16816(acc1, a1, t0, t1, acc1[0], acc1[1], acc1[2], acc1[3]);
-            mma16816(acc0, a2, t2, t3, acc0[0], acc0[1], acc0[2], acc0[3]);
-            mma16816(acc1, a3, t2, t3, acc1[0], acc1[1], acc1[2], acc1[3]);
+            mma16816(d0, a0, t0, t1, d0[0], d0[1], d0[2], d0[3]);
+            mma16816(d1, a1, t0, t1, d1[0], d1[1], d1[2], d1[3]);
+            mma16816(d0, a2, t2, t3, d0[0], d0[1], d0[2], d0[3]);
+            mma16816(d1, a3, t2, t3, d1[0], d1[1], d1[2], d1[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                    // columns: activation rows 2 (lane & 3) + (i & 1)
+            const bool own = with >> (4 * (2 * (lane & 3) + (i & 1))) & 1u;
+            acc0[i] += own ? d0[i] : 0.0f;
+            acc1[i] += own ? d1[i] : 0.0f;
         }
     }
 }

@@ -13,10 +13,13 @@
 //     weights are the narrow operand, so a CTA fetches 24 instead of 36 KB per
 //     64 K, and it was the fetching that bound it.
 //   * Sixteen warps unpack: a thread owns one weight row of a tile (its
-//     tensor-memory lane) and half of its K. A weight is q s (or S u - M)
-//     rounded once to fp16 (2^-12 relative, an eighth of the result's own
-//     rounding to bf16); fp16 instead of bf16 for both operands buys that.
-//     |w_hat| above 65504 overflows.
+//     tensor-memory lane) and half of its K. A weight is q s rounded once to
+//     fp16 (2^-12 relative, an eighth of the result's own rounding to bf16; q s
+//     is a multiple of 2^-24, so that small ones are exact); fp16 instead of
+//     bf16 for both operands buys that. For the superblocks S and M are rounded
+//     to fp16 as well, and S u - M is one more rounding: 2^-11 of S u + |M| in
+//     all, a hundredth of a code's step (S u - M in fp32 took a tenth longer to
+//     unpack). |w_hat| above 65504 overflows.
 //   * Units are cut where an even share of the work (rows x K) ends, so every
 //     CTA (one per SM) has the same; a cut unit's parts are summed through the
 //     workspace in K order by whichever CTA arrives last.
