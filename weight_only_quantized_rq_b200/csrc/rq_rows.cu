@@ -935,10 +935,15 @@ constexpr int kMaxCtas = 768;          // CTAs of a launch at most
 // group with more rows than a unit holds streams its weights once per unit. One
 // tile up to four rows on average (w4g64, 64 rows of 16 experts: 42 us against
 // 44 with two; a group of up to 16 rows then streams twice, from the L2), since
-// a second tile costs a CTA per SM its registers and every stage its MMAs.
+// a second tile costs a CTA per SM its registers and every stage its MMAs. Two
+// up to 16 rows, for w4sb32 up to 64: four tiles of a superblock stage leave
+// room for two CTAs per SM instead of three (8 experts, K 2560, N 2501, fp32:
+// w4sb32 16 rows 28 against 34 us, 64 rows 59 and 64, 128 rows 102 both; w5sb32
+// 16 rows 43 and 49, 32 rows 65 and 63; w4g64 16 rows 39.8 and 39.3).
+template <int FMT>
 int pick_nb(int R, int E) {
     const int per = (R + E - 1) / E;
-    return R <= 8 || per <= 4 ? 1 : per <= 12 ? 2 : 4;
+    return R <= 8 || per <= 4 ? 1 : per <= (FMT == kFmtW4SB32 ? 64 : is_sb(FMT) ? 16 : 12) ? 2 : 4;
 }
 
 struct Layout { size_t xf, part, count, total; int tiles, T; };
@@ -950,7 +955,7 @@ Layout layout(int R, int K, int E) {
     l.tiles = R / 8 + (E < R ? E : R);                   // sum of ceil(m_e / 8) at most
     l.xf = 0;
     l.part = round16((size_t)l.tiles * l.T * Geo<FMT>::XB);
-    l.count = l.part + (size_t)2 * kMaxCtas * pick_nb(R, E) * 4096;
+    l.count = l.part + (size_t)2 * kMaxCtas * pick_nb<FMT>(R, E) * 4096;
     l.total = l.count + kMaxCtas * kMathWarps * 4;
     return l;
 }
@@ -1001,7 +1006,7 @@ cudaError_t launch_fmt(const RowsArgs& a, cudaStream_t st) {
     if (!enc) return cudaErrorNotSupported;
     const Layout l = layout<FMT>(a.R, a.K, a.E);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
-    Plan pl = {a.offsets, a.E, a.R, a.N, a.K, l.T, pick_nb(a.R, a.E)};
+    Plan pl = {a.offsets, a.E, a.R, a.N, a.K, l.T, pick_nb<FMT>(a.R, a.E)};
 
     PrepParams q = {};
     q.pl = pl;

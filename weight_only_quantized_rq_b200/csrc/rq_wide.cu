@@ -18,8 +18,8 @@
 //     is a multiple of 2^-24, so that small ones are exact); fp16 instead of
 //     bf16 for both operands buys that. For the superblocks S and M are rounded
 //     to fp16 as well, and S u - M is one more rounding: 2^-11 of S u + |M| in
-//     all, a hundredth of a code's step (S u - M in fp32 took a tenth longer to
-//     unpack). |w_hat| above 65504 overflows.
+//     all, a hundredth of a code's step (in fp32: 54 against 53 us for 128 rows of
+//     w4sb32, K 2560, N 10240, with adapters). |w_hat| above 65504 overflows.
 //   * Units are cut where an even share of the work (rows x K) ends, so every
 //     CTA (one per SM) has the same; a cut unit's parts are summed through the
 //     workspace in K order by whichever CTA arrives last.
