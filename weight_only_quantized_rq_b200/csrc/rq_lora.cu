@@ -9,6 +9,10 @@
 //   expand_kernel  z = B_a t for eight rows x 128 weight rows per block, rows in
 //                  adapter order so that a block reads the B of few adapters
 // The product starts while expand runs and waits for it only at its end.
+// Measured (the whole call): 32 rows of 16 adapters, r 32, w8g16 4096 x 4096,
+// 27 MB: 25.5 us; 128 rows of 24, r 64, w4sb32 2560 -> 10240, 40 MB: 45 us (34
+// without expand); 1024 rows of 64, r 64, w4g64 4096 x 4096: 106 us. What bounds
+// it is the chain of launches ahead of the product's sums, not the bytes.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

