@@ -131,7 +131,7 @@ struct RowsArgs {
     void* y;                   // [Ty][N]
     int ybf16, act;            // act 1: max(v, 0)^2
     Adapters ad;               // ad.row NULL: none
-    const int* order;          // rows in adapter order, and the adapters' term [R][ldz], made beside the product
+    int* order;                // rows in adapter order, and the adapters' term [R][ldz], made beside the product
     const float* z;            // (NULL: the product makes it)
     int ldz;
     void* ws;

@@ -42,6 +42,7 @@
 
 #include "rq_device.cuh"
 #include "rq_internal.h"
+#include "rq_lora.cuh"
 #include "rq_rows.cuh"
 #include "rq_tc.cuh"
 
@@ -119,51 +120,74 @@ __device__ __forceinline__ uint32_t top8(uint4 v) {
     return __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
 }
 
+struct LayParams {
+    const __nv_bfloat16* x;
+    const int* in_rows;
+    int rows_x, K;
+    uint4* out;
+    float* rscale;
+    unsigned* count;
+    int n_count;
+};
+
 // One block per row: the largest exponent, then the row under its power of
-// two. Rows of up to 8192 values stay in registers between the two.
-template <int ORDER>
-__global__ void __launch_bounds__(kLayThreads) lay_rows_kernel(const __nv_bfloat16* x, const int* in_rows, int rows_x, int K, uint4* out,
-                                                             float* rscale, unsigned* count, int n_count, int late) {
-    __shared__ uint32_t tops[kLayThreads / 32];
-    const int tid = threadIdx.x, row = blockIdx.x;
-    if (!late) grid_dep_wait();
-    grid_dep_launch();
+// two. Rows of up to 32 THREADS values stay in registers between the two.
+template <int ORDER, int THREADS>
+__device__ __forceinline__ void lay_row(const LayParams& l, int row) {
+    __shared__ uint32_t tops[THREADS / 32];
+    const int tid = threadIdx.x, K = l.K;
     if (row == 0)
-        for (int i = tid; i < n_count; i += kLayThreads) count[i] = 0u;
-    int src = in_rows ? in_rows[row] : row;
-    if (src < 0 || src >= rows_x) src = -1;
-    const uint4* p = reinterpret_cast<const uint4*>(x + (size_t)(src < 0 ? 0 : src) * K);
+        for (int i = tid; i < l.n_count; i += THREADS) l.count[i] = 0u;
+    int src = l.in_rows ? l.in_rows[row] : row;
+    if (src < 0 || src >= l.rows_x) src = -1;
+    const uint4* p = reinterpret_cast<const uint4*>(l.x + (size_t)(src < 0 ? 0 : src) * K);
     const int nc = src < 0 ? 0 : K / 8;
     constexpr int KEEP = 4;
     uint4 v[KEEP];
     uint32_t top = 0u;
 #pragma unroll
     for (int i = 0; i < KEEP; ++i) {
-        const int c = tid + i * kLayThreads;
+        const int c = tid + i * THREADS;
         v[i] = c < nc ? p[c] : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int i = 0; i < KEEP; ++i) top = __vmaxu2(top, top8(v[i]));
-    for (int c = tid + KEEP * kLayThreads; c < nc; c += kLayThreads) top = __vmaxu2(top, top8(p[c]));
+    for (int c = tid + KEEP * THREADS; c < nc; c += THREADS) top = __vmaxu2(top, top8(p[c]));
     top = max(top & 0xffffu, top >> 16);
     top = __reduce_max_sync(~0u, top);
     if ((tid & 31) == 0) tops[tid >> 5] = top;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kLayThreads / 32; ++i) top = max(top, tops[i]);
+    for (int i = 0; i < THREADS / 32; ++i) top = max(top, tops[i]);
     const int ex = (int)(top >> 7);                      // biased exponent of the largest value; 255: not finite
     int sh = 0;
     if (ex < 255 && top) sh = max(-126, min(126, 141 - ex));
     const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
-    if (tid == 0) rscale[row] = __uint_as_float((uint32_t)(127 - sh) << 23);
-    uint4* o = out + (size_t)row * (K / 8);
+    if (tid == 0) l.rscale[row] = __uint_as_float((uint32_t)(127 - sh) << 23);
+    uint4* o = l.out + (size_t)row * (K / 8);
 #pragma unroll
     for (int i = 0; i < KEEP; ++i) {
-        const int c = tid + i * kLayThreads;
+        const int c = tid + i * THREADS;
         if (c < K / 8) o[c] = lay8<ORDER>(v[i], f);
     }
-    for (int c = tid + KEEP * kLayThreads; c < K / 8; c += kLayThreads) o[c] = lay8<ORDER>(c < nc ? p[c] : make_uint4(0u, 0u, 0u, 0u), f);
-    if (late) grid_dep_wait();                           // done means that the kernel before is done too
+    for (int c = tid + KEEP * THREADS; c < K / 8; c += THREADS) o[c] = lay8<ORDER>(c < nc ? p[c] : make_uint4(0u, 0u, 0u, 0u), f);
+}
+
+template <int ORDER>
+__global__ void __launch_bounds__(kLayThreads) lay_rows_kernel(const __grid_constant__ LayParams l) {
+    grid_dep_wait();
+    grid_dep_launch();
+    lay_row<ORDER, kLayThreads>(l, blockIdx.x);
+}
+
+// With adapters: their first product's blocks, then the rows'.
+template <int ORDER, int THREADS>
+__global__ void __launch_bounds__(THREADS) lay_shrink_kernel(const __grid_constant__ LayParams l, const __grid_constant__ Adapters ad, int R, int* order) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int n = R * (ad.r / 8), b = blockIdx.x;
+    if (b < n) shrink_block<THREADS>(ad, l.x, R, order, b);
+    else lay_row<ORDER, THREADS>(l, b - n);
 }
 
 // ------------------------------------------------------------------ groups
@@ -866,8 +890,18 @@ cudaError_t launch_wide_fmt(const RowsArgs& a, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, lay_rows_kernel<G::ORDER>, static_cast<const __nv_bfloat16*>(a.x), a.in_rows, a.T, a.K,
-                                       reinterpret_cast<uint4*>(ws + l.xg), rscale, count, kWideMaxCtas * kWorkers, a.z ? 1 : 0);
+    const LayParams lay = {static_cast<const __nv_bfloat16*>(a.x), a.in_rows, a.T, a.K, reinterpret_cast<uint4*>(ws + l.xg), rscale, count,
+                           kWideMaxCtas * kWorkers};
+    cudaError_t e;
+    if (!a.z) {
+        e = cudaLaunchKernelEx(&cfg, lay_rows_kernel<G::ORDER>, lay);
+    } else {
+        const int threads = shrink_threads(a.R);
+        cfg.gridDim = dim3((unsigned)(a.R * (a.ad.r / 8) + a.R));
+        cfg.blockDim = dim3((unsigned)threads);
+        e = threads == 512 ? cudaLaunchKernelEx(&cfg, lay_shrink_kernel<G::ORDER, 512>, lay, a.ad, a.R, a.order)
+                           : cudaLaunchKernelEx(&cfg, lay_shrink_kernel<G::ORDER, 256>, lay, a.ad, a.R, a.order);
+    }
     if (e != cudaSuccess) return e;
     if (a.z) {
         e = launch_expand(a.ad, a.order, a.R, const_cast<float*>(a.z), a.ldz, st);
