@@ -208,3 +208,39 @@ def test_many_rows_with_indices_out_of_range_and_not_finite(orc):
     assert bad and not torch.isfinite(y[[int(dst[i]) for i in bad]]).any()
     rest = sorted(set(range(R + 10)) - {int(dst[i]) for i in stored})
     assert (y[rest] == 7.5).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_offsets_past_32_bits(orc, dtype):
+    """The most rows, x and y of more than 2^31 elements, indices at their ends; then the combine of the rows."""
+    E, K, N, R = 2, 2560, 2304, 1 << 20
+    w, What = random_packed(orc, "w4g64", E * N, K, 58)
+    g = torch.Generator(DEV).manual_seed(58)
+    x = torch.empty(R, K, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    off = torch.tensor([0, R - 300001, R], dtype=torch.int32, device=DEV)
+    rows = torch.arange(R, dtype=torch.int32, device=DEV)
+    y = torch.empty(R, N, dtype=dtype, device=DEV)
+    rq.rq_wgemm_grouped(x, w, off, in_rows=R - 1 - rows, out_rows=rows, y=y)
+    at = torch.cat([torch.arange(40, device=DEV), torch.randint(0, R, (200,), device=DEV, generator=g), torch.arange(R - 40, R, device=DEV)])
+    e = (at >= R - 300001).long()
+    v = x[R - 1 - at].double()
+    ref, S = torch.empty(len(at), N, dtype=torch.float64, device=DEV), torch.empty(len(at), N, dtype=torch.float64, device=DEV)
+    for i in range(E):
+        We = What[i * N:(i + 1) * N]
+        ref[e == i], S[e == i] = v[e == i] @ We.t(), v[e == i].abs() @ We.abs().t()
+    check(y[at], ref, S, K)
+    out = rq.rq_route_combine(y, torch.zeros(R // 2, 2, dtype=torch.int32, device=DEV), torch.ones(R // 2, 2, device=DEV), out_dtype=torch.float32)
+    t = at // 2
+    want = y[2 * t].double() + y[2 * t + 1].double()
+    assert ((out[t].double() - want).abs() <= 2.0 ** -23 * (y[2 * t].double().abs() + y[2 * t + 1].double().abs())).all()
+    one = rq.Packed(w.fmt, K, N, w.codes[:w.codes.numel() // E].clone(), w.scales[:N * (K // 64) * 2].clone())
+    A, B, sc = adapters(3, 8, K, N, 58)
+    rq.LoraProjection(one, A, B, sc, max_rows=R)(x, rows % 4 - 1, y=y)
+    v, a = x[at].double(), at % 4 - 1
+    ref, S, extra = v @ What[:N].t(), v.abs() @ What[:N].abs().t(), torch.zeros_like(ref)
+    for i in range(3):
+        Ad, Bd, m = A[i].double(), B[i].double(), a == i
+        ref[m] += float(sc[i]) * (v[m] @ Ad.t()) @ Bd.t()
+        extra[m] = (K + 12) * 2.0 ** -23 * float(sc[i]) * (v[m].abs() @ Ad.abs().t()) @ Bd.abs().t()
+    check(y[at], ref, S, K, extra=extra)
+    assert rq.rq_device_status() == 0
