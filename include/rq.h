@@ -280,7 +280,8 @@ size_t rq_grouped_workspace_size(int fmt, int R, int K, int N, int E);
  * results is stored, element by element. A non-finite x value reaches the y
  * of its own rows only.
  * fp32 results, and bf16 ones where R < 16 E, come from exact products (codes
- * and bf16 x) summed in fp32. bf16 results where R >= 16 E come from weights
+ * and bf16 x) summed in fp32, the superblocks' sums of S u x and of M x apart
+ * (their rounding follows sum |x| (S u + |M|)). bf16 results where R >= 16 E come from weights
  * rounded once to fp16 (2^-12 of the weight; for the superblocks S and M are
  * rounded too, 2^-11 of S u + |M| in all, a hundredth of a code's step), which
  * must stay below 65504 in magnitude, and from each row of x relative to its

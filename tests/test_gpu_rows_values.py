@@ -1,0 +1,142 @@
+"""Row-dependent products where a rounding or a range shows: planes made code by
+code, so that what a weight is, and what each bound allows, is known exactly.
+
+Bounds (derived): fp32 results are sums of products that are exact in fp32's
+range, K 2^-23 sum |x| |w_hat| (an adder that truncates); for the superblocks,
+w_hat = S u - M, the two parts are summed apart: K 2^-23 sum |x| (S u + |M|).
+bf16 results of many rows come from weights rounded once to fp16: half a step,
+2^-11 |w_hat|, or 2^-25 below fp16's normal range. A bf16 result adds its own
+half step, 2^-8.
+"""
+import numpy as np
+import pytest
+import torch
+
+import weight_only_quantized_rq_b200 as rq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BITS = {"w4g64": 4, "w8g16": 8, "w8g64": 8, "w6g16": 6, "w4sb32": 4, "w5sb32": 5, "w6sb32": 6}
+SYM = ("w4g64", "w8g16", "w8g64", "w6g16")
+SB = ("w4sb32", "w5sb32", "w6sb32")
+
+
+def _pack_bits(v, width):
+    """Consecutive `width`-bit fields (last axis) as bytes, lowest bit first."""
+    bits = (v[..., None].astype(np.int64) >> np.arange(width)) & 1
+    return np.packbits(bits.reshape(*v.shape[:-1], -1).astype(np.uint8), axis=-1, bitorder="little")
+
+
+def symmetric(fmt, q, s):
+    """Packed, w_hat and |w_hat| in 64 bits, from codes q [N][K] and scales s [N][K / group]."""
+    N, K = q.shape
+    b, s = BITS[fmt], s.astype(np.float16)
+    u = (q + 2 ** (b - 1)).astype(np.uint8)
+    if fmt == "w4g64":
+        codes = _pack_bits(u, 4)
+    elif fmt == "w6g16":
+        v = u.reshape(N, K // 64, 64)
+        codes = np.concatenate((_pack_bits(v & 15, 4), _pack_bits(v >> 4, 2)), -1)
+    else:
+        codes = u
+    _, sb = rq.rq_packed_size(fmt, K, N)
+    plane = np.zeros(sb, np.uint8)
+    plane[:2 * s.size] = s.reshape(-1).view(np.uint8)
+    w = q * np.repeat(s.astype(np.float64), K // s.shape[1], 1)
+    return _on_gpu(fmt, K, N, codes, plane, w, np.abs(w))
+
+
+def superblocks(fmt, u, d, dmin, sc, mn):
+    """Packed, w_hat and S u + |M| in 64 bits, from codes u [N][K], d and dmin [N][K / 256], 6-bit sc and mn [N][K / 256][8]."""
+    N, K = u.shape
+    d, dmin = d.astype(np.float16), dmin.astype(np.float16)
+    v = u.reshape(N, K // 256, 256)
+    parts = [np.stack((d, dmin), -1).view(np.uint8), _pack_bits(np.concatenate((sc, mn), -1), 6), _pack_bits(v & 15, 4)]
+    if BITS[fmt] > 4:
+        parts.append(_pack_bits(v >> 4, BITS[fmt] - 4))
+    S = np.repeat(d.astype(np.float64)[..., None] * sc, 32, -1).reshape(N, K)
+    M = np.repeat(dmin.astype(np.float64)[..., None] * mn, 32, -1).reshape(N, K)
+    return _on_gpu(fmt, K, N, np.concatenate(parts, -1), None, S * u - M, S * u + np.abs(M))
+
+
+def _on_gpu(fmt, K, N, codes, scales, w, size):
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+    p = rq.Packed(rq.fmt_id(fmt), K, N, t(codes.reshape(-1)), None if scales is None else t(scales))
+    return p, t(w), t(size)
+
+
+def grouped(w, x, dtype, E=1, sizes=None, **more):
+    off = np.concatenate(([0], np.cumsum(sizes if sizes is not None else [x.shape[0]]))).astype(np.int32)
+    y = rq.rq_wgemm_grouped(x, w, torch.from_numpy(off).to(DEV), out_dtype=dtype, **more)
+    assert rq.rq_device_status() == 0
+    return y
+
+
+def within(y, ref, tol):
+    if y.dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+    err = (y.double() - ref).abs()
+    bad = ~(err <= tol)
+    assert not bad.any(), (int(bad.sum()), float((err / tol.clamp(min=1e-300)).max()))
+
+
+# Codes that are zero, under scales that are not, at the channels where x is large: what such a channel adds is exactly
+# nothing, whatever its size.
+def few_codes(fmt, N, K, seed, gone=slice(5, None, 64)):
+    """Random codes with zeros at the channels `gone`; no minima for the superblocks (w_hat = S u)."""
+    r = np.random.default_rng(seed)
+    b = BITS[fmt]
+    if fmt in SYM:
+        q = r.integers(1 - 2 ** (b - 1), 2 ** (b - 1), (N, K))
+        q[:, gone] = 0
+        return symmetric(fmt, q, r.uniform(0.5, 1.5, (N, K // (64 if fmt.endswith("g64") else 16))) * 3e-3)
+    u = r.integers(0, 2 ** b, (N, K))
+    u[:, gone] = 0
+    n = (N, K // 256)
+    return superblocks(fmt, u, r.uniform(0.5, 1.5, n) * 1e-4, np.zeros(n), r.integers(1, 64, (*n, 8)), r.integers(0, 64, (*n, 8)))
+
+
+@pytest.mark.parametrize("fmt", SYM + SB)
+@pytest.mark.parametrize("M", [1, 8, 15, 40])
+@pytest.mark.parametrize("large", [200.0, 3e4])
+def test_zero_codes_under_large_activations(fmt, M, large):
+    """The same bits as without those channels, and the fp32 bound of the others."""
+    K, N = 512, 136
+    w, What, _ = few_codes(fmt, N, K, 60 + M)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M))
+    x[:, 5::64] *= large
+    x = x.to(torch.bfloat16).to(DEV)
+    without = x.clone()
+    without[:, 5::64] = 0.0
+    for dtype in (torch.float32, torch.bfloat16):
+        assert torch.equal(grouped(w, x, dtype), grouped(w, without, dtype))
+    xd = without.double()
+    within(grouped(w, x, torch.float32), xd @ What.t(), K * 2.0 ** -23 * (xd.abs() @ What.abs().t()))
+
+
+@pytest.mark.parametrize("fmt", SYM + SB)
+@pytest.mark.parametrize("M", [1, 12, 40])
+def test_all_codes_zero(fmt, M):
+    """A matrix of zeros under scales that are not zero gives zeros."""
+    K, N = 512, 72
+    w, _, _ = few_codes(fmt, N, K, 61, gone=slice(None))
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).to(DEV)
+    for dtype in (torch.float32, torch.bfloat16):
+        assert (grouped(w, x, dtype) == 0).all()
+
+
+@pytest.mark.parametrize("fmt", SYM + SB)
+@pytest.mark.parametrize("M", [3, 20])
+@pytest.mark.parametrize("top", [124, 127])
+def test_activations_near_the_largest(fmt, M, top):
+    """Finite sums of values up to 2^127: nothing on the way to them leaves fp32's range."""
+    K, N = 256, 72
+    w, What, _ = few_codes(fmt, N, K, 62)
+    keep = 1.0 if top < 127 else 2.0 ** -10               # one channel at the top, the others so that the sums stay finite
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).clamp(-1.9, 1.9).double() * keep
+    x[:, 7] = 1.0
+    x = (x * 2.0 ** (top - 1)).to(torch.bfloat16).to(DEV)
+    xd = x.double()
+    y = grouped(w, x, torch.float32)
+    assert torch.isfinite(y).all()
+    within(y, xd @ What.t(), K * 2.0 ** -23 * (xd.abs() @ What.abs().t()))

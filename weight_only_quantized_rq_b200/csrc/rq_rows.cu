@@ -12,19 +12,25 @@
 //   eight rows (the last one padded with zeros), each tile as the B fragments
 //   of mma.m16n8k16 in the order that the weights' codes unpack in, so that the
 //   product kernel reads 16 bytes per lane with no bank conflict and no
-//   permutation. For codes below a byte it adds what the sums start from,
-//   -OFF sum x per weight group (codes unpack as OFF + q, and w = S u - M needs
-//   sum x besides). It clears the counters of the cut units, and up to eight
+//   permutation. For the superblocks it adds -sum x per group of 32 (w = S u - M
+//   needs it beside the products). It clears the counters of the cut units, and up to eight
 //   rows with adapters it computes t = s_a A_a x[m] in fp32. The product kernel
 //   starts beside it: its weight copies run while prep works.
 //
 // rows_kernel  multiplies. Bound by the weight stream while a group has few
 //   rows: what has to be read is the packed plane of each expert in use.
-//   * Codes are exact small integers in bf16 (q, |q| <= 127; u <= 63 for the
+//   * Codes are exact small integers in bf16 (q, |q| <= 128; u <= 63 for the
 //     superblocks), x is bf16: every product is exact in the tensor core's
 //     fp32 sums, and the group's scale multiplies the fp32 group sum. So no
 //     weight is rounded, and fp32 results are good to fp32 (2e-7 on the
 //     sums here), unlike weights rounded to bf16 before the product (2e-3).
+//     The offset that a code unpacks under is subtracted from the code, not from
+//     the sum: a code of zero adds nothing however large its x (16 + u summed
+//     against a start of -24 sum x saved that subtraction, but its error
+//     followed 24 sum |x|: 20 times as large with outliers of 200 on zero codes).
+//     Codes carry a factor of 2^-14, so that no sum of a group leaves fp32's
+//     range before its scale is applied; a unit's sums get it back at the end
+//     (exact, but for results below 2^-112, which keep 2^-135 absolute).
 //   * mma.sync, not tcgen05: with a handful of rows the products are not what
 //     counts. The A operand of mma.sync comes straight from the registers that
 //     unpacked it, and its result is in registers when the group's scale is
@@ -75,20 +81,18 @@ template <int FMT>
 struct Geo {
     static constexpr int KS = is_w8(FMT) || FMT == kFmtW6G16 ? 128 : 256;         // K per stage
     static constexpr int RB = FMT == kFmtW4G64 ? 128 : is_w8(FMT) ? 128 : FMT == kFmtW6G16 ? 96 : sb_record(FMT);
-    // Activations of one 8-row tile's stage: the fragments, then for sub-byte codes the rows' sums over
-    // the groups of GS weights, 64 bytes per group (row pairs 2t, 2t + 1 for t = 0..3, each pair twice: the
-    // four values that start a product).
-    static constexpr int GS = FMT == kFmtW4G64 ? 64 : FMT == kFmtW6G16 ? 16 : 32;
-    static constexpr int XB = KS * 16 + (is_w8(FMT) ? 0 : KS / GS * 64);
+    // Activations of one 8-row tile's stage: the fragments, then for the superblocks minus the rows' sums
+    // over each group, 32 bytes per group (of rows 0..7).
+    static constexpr int XB = KS * 16 + (is_sb(FMT) ? KS : 0);
     static constexpr int SB = is_sb(FMT) ? 0 : KS / sym_group(FMT) * 2;           // scale bytes of a weight row's stage
     static constexpr bool SWZ = RB == 128;
     static constexpr int CB = (kRowsPerTile * RB + 1023) & ~1023;                 // a code slot
     static constexpr int SCRATCH = is_sb(FMT) ? 2048 : 1024;                      // shared bytes of a math warp
-    // Sub-byte codes u unpack as 2^B + u (B code bits, the top of bf16's seven fraction bits); the products
-    // start from -OFF sum x, so that they give sum q x (symmetric) or sum u x (superblocks).
-    static constexpr int B = FMT == kFmtW6G16 ? 6 : FMT == kFmtW4G64 ? 4 : is_sb(FMT) ? sb_bits(FMT) : 0;
-    static constexpr float OFF = is_sb(FMT) ? (float)(1 << B) : 1.5f * (float)(1 << B);
 };
+
+// Codes are multiplied as q 2^-kDown (u 2^-kDown): with 64 codes of up to 128 in a group's sum, a quarter of fp32's
+// largest value is not passed.
+constexpr int kDown = 14;
 
 // CTAs per SM: four while their accumulators and two stages each fit.
 __host__ __device__ constexpr int ctas_per_sm(int fmt, int nb) {
@@ -206,9 +210,16 @@ constexpr int kPrepThreads = 128;
 constexpr int kPrepUnroll = 4;         // 16-byte chunks per thread
 constexpr int kPrepChunks = 4 * (kPrepThreads / 32) * kPrepUnroll;   // of each of a block's eight rows
 
+// -2^-kDown times the sum of eight values.
 __device__ __forceinline__ float bf16_sum8(uint4 v) {
-    return ((bf16lo_f32(v.x) + bf16hi_f32(v.x)) + (bf16lo_f32(v.y) + bf16hi_f32(v.y))) +
-           ((bf16lo_f32(v.z) + bf16hi_f32(v.z)) + (bf16lo_f32(v.w) + bf16hi_f32(v.w)));
+    constexpr float F = -1.0f / (1 << kDown);
+    float a = bf16lo_f32(v.x) * F, b = bf16hi_f32(v.x) * F;
+    a = fmaf(bf16lo_f32(v.y), F, a);
+    b = fmaf(bf16hi_f32(v.y), F, b);
+    a = fmaf(bf16lo_f32(v.z), F, a);
+    b = fmaf(bf16hi_f32(v.z), F, b);
+    a = fmaf(bf16lo_f32(v.w), F, a);
+    return fmaf(bf16hi_f32(v.w), F, b) + a;
 }
 
 // With 32 registers its blocks fit beside the CTAs of a product that is still
@@ -242,12 +253,6 @@ __global__ void __launch_bounds__(kPrepThreads, SHRINK ? 8 : 16) prep_kernel(con
         const int c_end = p.pl.T * G::KS / 8;                                // 8-value chunks of a row, padded to whole stages
         uint8_t* out = p.xf + (size_t)tile * p.pl.T * G::XB;
         uint4 vv[kPrepUnroll];
-        float sum64 = 0.0f;
-        // -OFF times this row's sum over group gr of a stage, to its place behind the fragments
-        auto put_sum = [&](uint8_t* o, int gr, float sum) {
-            float* d = reinterpret_cast<float*>(o + G::KS * 16 + gr * 64 + (lane >> 3) * 16) + ((lane >> 2) & 1);
-            d[0] = d[2] = -G::OFF * sum;
-        };
 #pragma unroll
         for (int q = 0; q < kPrepUnroll; ++q) {
             const int c = kb * kPrepChunks + 4 * (kPrepUnroll * warp + q) + (lane & 3);
@@ -269,15 +274,11 @@ __global__ void __launch_bounds__(kPrepThreads, SHRINK ? 8 : 16) prep_kernel(con
                 w.z = prmt(v.y, v.w, 0x5410u);
                 w.w = prmt(v.y, v.w, 0x7632u);
                 *reinterpret_cast<uint4*>(o + ((cs >> 2) * 32 + lane) * 16) = w;
-                float s = bf16_sum8(v);                  // the row's sum over 32 weights
-                s += __shfl_xor_sync(~0u, s, 1);
-                s += __shfl_xor_sync(~0u, s, 2);
-                if (G::GS == 32) {
-                    if ((lane & 3) == 0) put_sum(o, cs >> 2, s);
-                } else if (q & 1) {                      // a thread's chunks q - 1 and q lie in one group of 64
-                    if ((lane & 3) == 0) put_sum(o, cs >> 3, sum64 + s);
-                } else {
-                    sum64 = s;
+                if constexpr (is_sb(FMT)) {              // the row's sum over 32 weights, behind the fragments
+                    float s = bf16_sum8(v);
+                    s += __shfl_xor_sync(~0u, s, 1);
+                    s += __shfl_xor_sync(~0u, s, 2);
+                    if ((lane & 3) == 0) reinterpret_cast<float*>(o + G::KS * 16)[(cs >> 2) * 8 + (lane >> 2)] = s;
                 }
             } else {
                 // four-weight words unpack as the pairs (0, 2), (1, 3); lane t of a quad takes weights
@@ -289,11 +290,6 @@ __global__ void __launch_bounds__(kPrepThreads, SHRINK ? 8 : 16) prep_kernel(con
                     const int t = 2 * (cs & 1) + h, half = (cs >> 1) & 1;
                     const uint2 w = make_uint2(prmt(a, b, 0x5410u), prmt(a, b, 0x7632u));
                     *reinterpret_cast<uint2*>(o + ((cs >> 2) * 32 + g8 * 4 + t) * 16 + half * 8) = w;
-                }
-                if constexpr (!is_w8(FMT)) {
-                    float s = bf16_sum8(v);              // over 16 weights
-                    s += __shfl_xor_sync(~0u, s, 1);
-                    if ((lane & 1) == 0) put_sum(o, cs >> 1, s);
                 }
             }
         }
@@ -344,30 +340,44 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 
 // ------------------------------------------------------------------ unpack
 // A bf16 has seven fraction bits. Codes of B < 7 bits go to the top B of them
-// under the exponent of 2^B: 2^B + u, exact, with one shift and one logic
-// operation per two weights (two more for the bits above a nibble).
+// under the exponent of 2^B (less kDown): 2^B + u, from which 2^B (superblocks) or
+// 1.5 2^B (symmetric) is subtracted, all exact: a shift, a logic operation and a
+// subtraction per two weights (two more for the bits above a nibble).
+constexpr uint32_t code_base(int B) { return (uint32_t)(127 + B - kDown) << 7; }
 __device__ __forceinline__ uint32_t shift_to(uint32_t w, int from, int to) { return from >= to ? w >> (from - to) : w << (to - from); }
 
 // Eight nibbles of w as the pairs (0, 4), (1, 5), (2, 6), (3, 7); h holds the
 // codes' B - 4 higher bits at bits 16 (k / 4) + (B - 4) (k % 4).
-template <int B>
+template <int B, bool SYM>
 __device__ __forceinline__ void unpack_nibbles(uint32_t w, uint32_t h, uint32_t (&o)[4]) {
-    constexpr uint32_t P = 7 - B, M = 0x000F000Fu << P, E = (0x4180u + 0x80u * (B - 4)) * 0x10001u;
+    if constexpr (B == 4) {
+        // every other nibble stays at the bottom of the fraction, under the exponent of 2^7: one shift less
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t P = i & 1 ? 3u : 0u, E = code_base(i & 1 ? 4 : 7) * 0x10001u;
+            o[i] = sub_bf16x2(and_or(shift_to(w, 4 * i, P), 0x000F000Fu << P, E), E | (SYM ? 0x00080008u << P : 0u));
+        }
+        return;
+    }
+    constexpr uint32_t P = 7 - B, M = 0x000F000Fu << P, E = code_base(B) * 0x10001u, OFF = E | (SYM ? 0x00400040u : 0u);
     constexpr uint32_t HM = (B == 5 ? 0x00010001u : 0x00030003u) << (P + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         o[i] = and_or(shift_to(w, 4 * i, P), M, E);
         if (B > 4) o[i] = and_or(shift_to(h, (B - 4) * i, P + 4), HM, o[i]);
+        o[i] = sub_bf16x2(o[i], OFF);
     }
 }
 // Four bytes u = q + 128 of w as the pairs (0, 2), (1, 3): the low seven bits
-// under 128, minus 128 where the byte's top bit is set (0x4300) and 256 where
-// it is not (0x4380).
+// under 128, minus 128 where the byte's top bit is set and 256 where it is not
+// (the next exponent, whose lowest bit is 1 as kDown is even).
 __device__ __forceinline__ void unpack_bytes(uint32_t w, uint32_t (&o)[2]) {
+    static_assert(kDown % 2 == 0, "the exponent of 128 is even");
+    constexpr uint32_t E = code_base(7) * 0x10001u;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t v = i ? w >> 8 : w;
-        o[i] = sub_bf16x2(and_or(v, 0x007F007Fu, 0x43004300u), and_xor(v, 0x00800080u, 0x43804380u));
+        o[i] = sub_bf16x2(and_or(v, 0x007F007Fu, E), and_xor(v, 0x00800080u, E + 0x00800080u));
     }
 }
 
@@ -377,12 +387,12 @@ __device__ __forceinline__ float half_at(uint32_t w, int h) {
 }
 
 // A superblock stage's scales, each lane those of weight row wr + lane: S_j and
-// M_j / 2^B of the eight groups to shared memory.
+// M_j of the eight groups to shared memory.
 template <int FMT>
 __device__ __forceinline__ void decode_superblock(uint32_t cs, uint32_t smin, int wr, int lane) {
     using G = Geo<FMT>;
     const uint4 hd = lds128_a(cs + (uint32_t)(wr + lane) * G::RB);
-    const float d = half_at(hd.x, 0), dm = __fmul_rn(half_at(hd.x, 1), 1.0f / G::OFF);
+    const float d = half_at(hd.x, 0), dm = half_at(hd.x, 1);
     __syncwarp();                                        // the previous stage's values have been read
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -407,7 +417,7 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t ss
                                            float (&acc)[2][NB][4]) {
     using G = Geo<FMT>;
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t xl = xs + lane * 16, xg = xs + G::KS * 16 + t * 16;
+    const uint32_t xl = xs + lane * 16;
     const uint32_t rb = cs + (uint32_t)(wr + g) * G::RB;                 // first of the thread's weight rows, 8 apart
     const uint32_t rs = ss + (uint32_t)(wr + g) * G::SB;
     if constexpr (FMT == kFmtW4G64 || FMT == kFmtW8G64) {
@@ -424,7 +434,7 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t ss
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         uint32_t o[4];
-                        unpack_nibbles<4>(lds32_a(rb + 8 * mr * G::RB + (((2 * gr + j) ^ g) << 4) + 4 * t), 0u, o);
+                        unpack_nibbles<4, true>(lds32_a(rb + 8 * mr * G::RB + (((2 * gr + j) ^ g) << 4) + 4 * t), 0u, o);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             a[mr >> 1][2 * j + h][mr & 1] = o[2 * h];
@@ -445,12 +455,10 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t ss
             for (int nb = 0; nb < NB; ++nb) {
                 if (NB > 1 && nb >= tiles) break;
                 const uint4 x0 = lds128_a(xl + nb * G::XB + (2 * gr) * 512), x1 = lds128_a(xl + nb * G::XB + (2 * gr + 1) * 512);
-                float4 c = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (FMT == kFmtW4G64) c = lds128f_a(xg + nb * G::XB + gr * 64);
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     float d[4];
-                    mma16816(d, a[mt][0], x0.x, x0.y, c.x, c.y, c.z, c.w);
+                    mma16816(d, a[mt][0], x0.x, x0.y, 0.0f, 0.0f, 0.0f, 0.0f);
                     mma16816(d, a[mt][1], x0.z, x0.w, d[0], d[1], d[2], d[3]);
                     mma16816(d, a[mt][2], x1.x, x1.y, d[0], d[1], d[2], d[3]);
                     mma16816(d, a[mt][3], x1.z, x1.w, d[0], d[1], d[2], d[3]);
@@ -479,8 +487,9 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t ss
                         uint32_t pl;
                         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(pl) : "r"(b + 32 + 4 * (st & 3) + t));
                         const uint32_t v = n | (n << 8), hh = pl | (pl << 12);     // pairs (0, 2), (1, 3), as for the bytes
-                        o[0] = and_or(hh << 5, 0x00600060u, and_or(v << 1, 0x001E001Eu, 0x42804280u));
-                        o[1] = and_or(hh << 3, 0x00600060u, and_or(v >> 3, 0x001E001Eu, 0x42804280u));
+                        constexpr uint32_t E = code_base(6) * 0x10001u;
+                        o[0] = sub_bf16x2(and_or(hh << 5, 0x00600060u, and_or(v << 1, 0x001E001Eu, E)), E | 0x00400040u);
+                        o[1] = sub_bf16x2(and_or(hh << 3, 0x00600060u, and_or(v >> 3, 0x001E001Eu, E)), E | 0x00400040u);
                     } else {
                         unpack_bytes(lds32_a(rb + 8 * mr * G::RB + ((st ^ g) << 4) + 4 * t), o);
                     }
@@ -492,16 +501,11 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t ss
             for (int nb = 0; nb < NB; ++nb) {
                 if (NB > 1 && nb >= tiles) break;
                 const uint4 x = lds128_a(xl + nb * G::XB + sp * 512);
-                float4 c0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), c1 = c0;
-                if constexpr (FMT == kFmtW6G16) {
-                    c0 = lds128f_a(xg + nb * G::XB + 2 * sp * 64);
-                    c1 = lds128f_a(xg + nb * G::XB + (2 * sp + 1) * 64);
-                }
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     float d0[4], d1[4];
-                    mma16816(d0, a[mt][0], x.x, x.y, c0.x, c0.y, c0.z, c0.w);
-                    mma16816(d1, a[mt][1], x.z, x.w, c1.x, c1.y, c1.z, c1.w);
+                    mma16816(d0, a[mt][0], x.x, x.y, 0.0f, 0.0f, 0.0f, 0.0f);
+                    mma16816(d1, a[mt][1], x.z, x.w, 0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         acc[mt][nb][i] = fmaf(s[0][2 * mt + (i >> 1)], d0[i], acc[mt][nb][i]);
@@ -528,7 +532,7 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t ss
                     h = lds16_a(r + 144 + 8 * gr + 2 * t);
                     h |= h << 8;
                 }
-                unpack_nibbles<G::B>(lds32_a(r + 16 + 16 * gr + 4 * t), h, o);
+                unpack_nibbles<sb_bits(FMT), false>(lds32_a(r + 16 + 16 * gr + 4 * t), h, o);
                 sm2[mr] = lds64f_a(smin + (8 * mr + g) * 64 + (((gr >> 1) ^ ((g >> 1) & 3)) << 4) + 8 * (gr & 1));
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
@@ -540,11 +544,11 @@ __device__ __forceinline__ void stage_math(uint32_t cs, uint32_t xs, uint32_t ss
             for (int nb = 0; nb < NB; ++nb) {
                 if (NB > 1 && nb >= tiles) break;
                 const uint4 x = lds128_a(xl + nb * G::XB + gr * 512);
-                const float4 c = lds128f_a(xg + nb * G::XB + gr * 64);
+                const float2 c = lds64f_a(xs + nb * G::XB + G::KS * 16 + gr * 32 + t * 8);       // rows 2t, 2t + 1
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     float d[4];
-                    mma16816(d, a[mt][0], x.x, x.y, c.x, c.y, c.z, c.w);
+                    mma16816(d, a[mt][0], x.x, x.y, 0.0f, 0.0f, 0.0f, 0.0f);
                     mma16816(d, a[mt][1], x.z, x.w, d[0], d[1], d[2], d[3]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -822,6 +826,12 @@ __global__ void __launch_bounds__(kRowsThreads, ctas_per_sm(FMT, NB)) rows_kerne
             if (++xslot == kXRing) { xslot = 0; ++xwrap; }
         }
         left -= count;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[mt][nb][i] *= (float)(1 << kDown);
 
         const Desc d = read_desc(&desc[u % kDescs]);
         int out[NB];                                      // this lane's rows of y
