@@ -281,11 +281,13 @@ size_t rq_grouped_workspace_size(int fmt, int R, int K, int N, int E);
  * of its own rows only.
  * fp32 results, and bf16 ones where R < 16 E, come from exact products (codes
  * and bf16 x) summed in fp32, the superblocks' sums of S u x and of M x apart
- * (their rounding follows sum |x| (S u + |M|)). bf16 results where R >= 16 E come from weights
- * rounded once to fp16 (2^-12 of the weight; for the superblocks S and M are
- * rounded too, 2^-11 of S u + |M| in all, a hundredth of a code's step), which
- * must stay below 65504 in magnitude, and from each row of x relative to its
- * largest value (values below 2^-39 of it count as zero). */
+ * (their rounding follows sum |x| (S u + |M|)). bf16 results where R >= 16 E
+ * come from weights in fp16, summed in fp32: symmetric ones rounded once (half a
+ * step, 2^-11 of the weight), superblocks' within 2^-10 (|w| + |w(c)|), w(c) the
+ * weight of the group's middle code c = 2^(b-1); |w| must stay below 65504. There
+ * each row of x counts relative to its largest value (exact down to 2^-31 of
+ * it, within 2^-39 of it below). So a row's bits may differ between calls of
+ * few and of many rows. */
 int rq_wgemm_grouped(const void *x, int T, int K, int N, const rq_packed *w, const rq_groups *g, void *y, int Ty,
                      int act, int out_type, void *workspace, size_t workspace_bytes, void *stream);
 

@@ -5,8 +5,10 @@ Bounds (derived): fp32 results are sums of products that are exact in fp32's
 range, K 2^-23 sum |x| |w_hat| (an adder that truncates); for the superblocks,
 w_hat = S u - M, the two parts are summed apart: K 2^-23 sum |x| (S u + |M|).
 bf16 results of many rows come from weights rounded once to fp16: half a step,
-2^-11 |w_hat|, or 2^-25 below fp16's normal range. A bf16 result adds its own
-half step, 2^-8.
+2^-11 |w_hat|, or 2^-25 below fp16's normal range; the superblocks' from
+S (u - c) + (c S - M), c the middle code, with S, c S - M and the weight rounded
+so: 2^-11 (S |u - c| + |c S - M| + |w_hat|) <= 2^-10 (|w_hat| + |c S - M|). A bf16
+result adds its own half step, 2^-8.
 """
 import numpy as np
 import pytest
@@ -140,3 +142,30 @@ def test_activations_near_the_largest(fmt, M, top):
     y = grouped(w, x, torch.float32)
     assert torch.isfinite(y).all()
     within(y, xd @ What.t(), K * 2.0 ** -23 * (xd.abs() @ What.abs().t()))
+
+
+@pytest.mark.parametrize("fmt", SYM + SB)
+def test_many_rows_round_each_weight_once(fmt):
+    """One channel per row, so that each result is one weight: symmetric formats within fp16's half step of it,
+    superblocks within 2^-10 of it and of the group's middle weight, also where S u and M nearly cancel."""
+    K, N, M = 512, 264, 96
+    r = np.random.default_rng(63)
+    b, n = BITS[fmt], (N, K // 256)
+    if fmt in SYM:
+        w, What, _ = few_codes(fmt, N, K, 63, gone=slice(0, 0))
+        bound = 2.0 ** -11 * What.abs()
+    else:
+        d = (r.uniform(0.5, 1.5, n) * 1e-4).astype(np.float16)
+        dmin = (d * r.uniform(0.3, 0.7, n) * 2 ** b).astype(np.float16)
+        f = lambda: r.integers(48, 64, (*n, 8))
+        sc, mn = f(), f()
+        w, What, _ = superblocks(fmt, r.integers(0, 2 ** b, (N, K)), d, dmin, sc, mn)
+        middle = superblocks(fmt, np.full((N, K), 2 ** (b - 1)), d, dmin, sc, mn)[1]
+        bound = 2.0 ** -10 * (What.abs() + middle.abs())
+    k = torch.from_numpy(r.permutation(K)[:M]).to(DEV)
+    x = torch.zeros(M, K, device=DEV)
+    x[torch.arange(M, device=DEV), k] = 2.0 ** torch.randint(-20, 20, (M,), generator=torch.Generator().manual_seed(1)).to(DEV).float()
+    x = x.to(torch.bfloat16)
+    ref = x.double() @ What.t()
+    scale = x.double().sum(1, keepdim=True)
+    within(grouped(w, x, torch.bfloat16), ref, x.double() @ bound.t() + 2.0 ** -25 * scale)
