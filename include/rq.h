@@ -284,10 +284,11 @@ size_t rq_grouped_workspace_size(int fmt, int R, int K, int N, int E);
  * (their rounding follows sum |x| (S u + |M|)). bf16 results where R >= 16 E
  * come from weights in fp16, summed in fp32: symmetric ones rounded once (half a
  * step, 2^-11 of the weight), superblocks' within 2^-10 (|w| + |w(c)|), w(c) the
- * weight of the group's middle code c = 2^(b-1); |w| must stay below 65504. There
- * each row of x counts relative to its largest value (exact down to 2^-31 of
- * it, within 2^-39 of it below). So a row's bits may differ between calls of
- * few and of many rows. */
+ * weight of the group's middle code c = 2^(b-1). There each row of x counts
+ * relative to its largest value (exact down to 2^-31 of it, within 2^-39 of it
+ * below). So a row's bits may differ between calls of few and of many rows.
+ * Weight rows whose scales let a code pass 65504 are multiplied in fp32
+ * instead, slowly. */
 int rq_wgemm_grouped(const void *x, int T, int K, int N, const rq_packed *w, const rq_groups *g, void *y, int Ty,
                      int act, int out_type, void *workspace, size_t workspace_bytes, void *stream);
 

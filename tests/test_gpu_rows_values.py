@@ -169,3 +169,67 @@ def test_many_rows_round_each_weight_once(fmt):
     ref = x.double() @ What.t()
     scale = x.double().sum(1, keepdim=True)
     within(grouped(w, x, torch.bfloat16), ref, x.double() @ bound.t() + 2.0 ** -25 * scale)
+
+
+def wide_scales(fmt, N, K, seed):
+    """Scales over the whole of fp16: a third of the rows ordinary, a third with one huge group, a third huge throughout."""
+    r = np.random.default_rng(seed)
+    b = BITS[fmt]
+    groups = K // (256 if fmt in SB else 64 if fmt.endswith("g64") else 16)
+    s = r.uniform(0.5, 1.0, (N, groups)) * 2e-3
+    one = np.arange(N) % 3 == 1
+    s[one, r.integers(0, groups, int(one.sum()))] = 65504.0
+    s[np.arange(N) % 3 == 2] = r.uniform(0.3, 1.0, (int((np.arange(N) % 3 == 2).sum()), groups)) * 65504.0
+    if fmt in SYM:
+        return symmetric(fmt, r.integers(1 - 2 ** (b - 1), 2 ** (b - 1), (N, K)), s)
+    f = lambda: r.integers(0, 64, (N, groups, 8))
+    return superblocks(fmt, r.integers(0, 2 ** b, (N, K)), s, s * r.uniform(0.2, 1.0, s.shape), f(), f())
+
+
+@pytest.mark.parametrize("fmt", SYM + SB)
+@pytest.mark.parametrize("M,N,K", [(32, 200, 512), (150, 600, 1024), (700, 130, 256)])
+def test_weights_past_half_precision(fmt, M, N, K):
+    """Every valid plane gives finite results: weights up to 65504 x 128 (superblocks 65504 x 63 x 64), few and many rows."""
+    w, What, size = wide_scales(fmt, 2 * N, K, 64)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).to(DEV)
+    xd = x.double()
+    h = M // 3
+    both = lambda v, W: torch.cat((v[:h] @ W[:N].t(), v[h:] @ W[N:].t()))
+    ref, S, F = both(xd, What), both(xd.abs(), What.abs()), both(xd.abs(), size)
+    for dtype in (torch.bfloat16, torch.float32):
+        tol = K * 2.0 ** -23 * F
+        if dtype == torch.bfloat16:
+            tol = tol + 2.0 ** -11 * S
+        within(grouped(w, x, dtype, sizes=[h, M - h]), ref, tol)
+    tol = K * 2.0 ** -23 * F + 2.0 ** -11 * S
+    y = grouped(w, x, torch.bfloat16, sizes=[h, M - h], act="relu2")
+    within(y, ref.clamp(min=0) ** 2, 2 * ref.abs() * tol + tol * tol + 2.0 ** -23 * ref * ref)
+
+
+def test_longest_rows_of_weights_past_half_precision():
+    """The slow sums of the largest units (128 rows x 256 weight rows x K 32768) end well before any wait gives up."""
+    M, N, K = 9500, 150, 32768
+    w, What, _ = wide_scales("w8g16", 2 * N, K, 70)
+    x = torch.randn(M, K, generator=torch.Generator(device=DEV).manual_seed(70), device=DEV).to(torch.bfloat16)
+    y = grouped(w, x, torch.bfloat16, sizes=[M // 2, M // 2])
+    for rows, W in ((slice(0, M // 2), What[:N]), (slice(M // 2, M), What[N:])):
+        xd = x[rows].double()
+        S = xd.abs() @ W.abs().t()
+        within(y[rows], xd @ W.t(), (K * 2.0 ** -23 + 2.0 ** -11) * S)
+
+
+@pytest.mark.parametrize("fmt", ["w4g64", "w8g16", "w6sb32"])
+def test_adapters_beside_weights_past_half_precision(fmt):
+    M, N, K, r = 70, 200, 512, 16
+    w, What, size = wide_scales(fmt, N, K, 65)
+    g = torch.Generator().manual_seed(65)
+    x = torch.randn(M, K, generator=g).to(torch.bfloat16).to(DEV)
+    A = (torch.randn(3, r, K, generator=g) / K ** 0.5).to(torch.bfloat16).to(DEV)
+    B = (torch.randn(3, N, r, generator=g) * 1e3).to(torch.bfloat16).to(DEV)
+    a = torch.arange(M, device=DEV) % 3
+    xd, Ad, Bd = x.double(), A[a].double(), B[a].double()
+    term = torch.einsum("mnr,mrk,mk->mn", Bd, Ad, xd)
+    size_t = torch.einsum("mnr,mrk,mk->mn", Bd.abs(), Ad.abs(), xd.abs())
+    y = rq.rq_wgemm_lora(x, w, A, B, torch.ones(3, device=DEV), a.to(torch.int32), out_dtype=torch.bfloat16)
+    tol = K * 2.0 ** -23 * (xd.abs() @ size.t()) + 2.0 ** -11 * (xd.abs() @ What.abs().t()) + (K + r + 4) * 2.0 ** -23 * size_t
+    within(y, xd @ What.t() + term, tol)

@@ -18,7 +18,8 @@
 //     bf16; q s is a multiple of 2^-24, so that small ones are exact); fp16
 //     instead of bf16 for both operands buys that. The superblocks' weights are
 //     within 2^-10 (|w| + |w(c)|), w(c) the group's weight of the middle code
-//     (unpack_atom). |w_hat| above 65504 overflows.
+//     (unpack_atom). Scales under which a code could pass fp16's 65504 are seen
+//     while unpacking; such a row's sums are made again in fp32 (exact_sums).
 //   * Units are cut where an even share of the work (rows x K) ends, so every
 //     CTA (one per SM) has the same; a cut unit's parts are summed through the
 //     workspace in K order by whichever CTA arrives last.
@@ -56,8 +57,9 @@ constexpr int kWideThreads = 32 * (kWorkers + 4);
 constexpr int kMaxX = 4;                // activation slots at most (128 K each)
 constexpr int kMaxCodes = 4;            // code slots at most
 constexpr int kDescs = 8;
-constexpr size_t kWideSmem = 226 * 1024;
+constexpr size_t kWideSmem = 227 * 1024;
 constexpr int kWideMaxCtas = 256;
+constexpr int kOverBytes = 2 * kUnitRows * 2;
 constexpr int kA = 4;                   // A slots: 128 K of one tile, 64 columns
 constexpr int kBarBytes = (2 * kMaxCodes + 2 * kMaxX + 2 * kA + kDescs + 4 * 2 + 3) * 8;
 
@@ -80,9 +82,11 @@ struct WideParams {
     CUtensorMap cmap;                   // codes: uint8 [E N][row bytes], box [256][RB]
     CUtensorMap xmap;                   // rows: fp16 [R][K] viewed as [K / 64][R][64], box [1][32][64]
     WidePlan pl;
+    const uint8_t* codes;
     const uint8_t* scales;
     unsigned long long total_rows;
-    uint32_t srb;
+    uint32_t crb, srb;                  // code and scale bytes per weight row
+    const uint4* xg;                    // the laid-out rows
     const float* rscale;                // [R] inverse of a row's power of two
     float* part;                        // partial tiles, two per CTA
     unsigned* count;                    // stages summed of a cut unit, by its first CTA and warp
@@ -91,7 +95,7 @@ struct WideParams {
     int Ty, act;
     const float* z;                     // [R][ldz] the adapters' term, or NULL
     int ldz;
-    int xslots, cslots;
+    int xslots, cslots, over_at;
     unsigned long long wait_ns;
     int test_flags;
 };
@@ -351,11 +355,19 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t m, uint32_t c) { return lop_mask_or(v, m, c); }
 __device__ __forceinline__ uint4 lds4(uint32_t a) { return lds128_a(a); }
 
+// Largest magnitude (as bits) of four fp16 scales.
+__device__ __forceinline__ uint32_t top_scale(const uint32_t (&sc)[2]) {
+    const uint32_t m = __vmaxu2(sc[0] & 0x7fff7fffu, sc[1] & 0x7fff7fffu);
+    return max(m & 0xffffu, m >> 16);
+}
+
 // 64 weights of the thread's row in an atom -> 32 fp16 pairs. cs: the row's
 // bytes of the slot; at: atom of the slot; sc: its scale words (two fp16
-// each); sw: swizzle of 16-byte chunks (row % 8, or 0).
+// each); sw: swizzle of 16-byte chunks (row % 8, or 0). True if a code under
+// these scales could pass 65504 (0x7BFF; a power of two of codes less, as many
+// exponents less).
 template <int FMT>
-__device__ __forceinline__ void unpack_atom(uint32_t cs, int at, int sw, const uint32_t (&sc)[2], uint32_t (&o)[32]) {
+__device__ __forceinline__ bool unpack_atom(uint32_t cs, int at, int sw, const uint32_t (&sc)[2], uint32_t (&o)[32]) {
     if constexpr (FMT == kFmtW4G64) {
         // (1024 + u) - 1032 and (1024 + 16 u) / 16 - 72 give q exactly; q s is rounded once
         const uint4 c0 = lds4(cs + (((2 * at) ^ sw) << 4)), c1 = lds4(cs + (((2 * at + 1) ^ sw) << 4));
@@ -369,6 +381,7 @@ __device__ __forceinline__ void unpack_atom(uint32_t cs, int at, int sw, const u
             o[4 * i + 2] = hmul2(hadd2(and_or(v, 0x000F000Fu, 0x64006400u), 0xE408E408u), s);
             o[4 * i + 3] = hmul2(hfma2(and_or(v, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u), s);
         }
+        return (sc[0] & 0x7fffu) > 0x7BFFu - 3 * 0x400;
     } else if constexpr (is_w8(FMT)) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -381,6 +394,7 @@ __device__ __forceinline__ void unpack_atom(uint32_t cs, int at, int sw, const u
                 o[8 * c + 2 * i + 1] = hmul2(hadd2(and_or(w[i] >> 8, 0x00FF00FFu, 0x64006400u), 0xE480E480u), s);
             }
         }
+        return top_scale(sc) > 0x7BFFu - 7 * 0x400;
     } else if constexpr (FMT == kFmtW6G16) {
         const uint4 c0 = lds4(cs + 48 * at), c1 = lds4(cs + 48 * at + 16), pl = lds4(cs + 48 * at + 32);
         const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w}, p[4] = {pl.x, pl.y, pl.z, pl.w};
@@ -395,12 +409,14 @@ __device__ __forceinline__ void unpack_atom(uint32_t cs, int at, int sw, const u
                 o[4 * i + q] = hmul2(hadd2(u, 0xE420E420u), s);                                                // - 1056
             }
         }
+        return top_scale(sc) > 0x7BFFu - 5 * 0x400;
     } else {
         // v = u - c exactly (c = 2^(B - 1)), then S v + (c S - M) in one step, S = d sc and c S - M rounded to fp16 (half a
         // step, 2^-11, each): within 2^-11 (S |v| + |c S - M| + |w|) <= 2^-10 (|w| + |c S - M|). Subtracting M from S u
         // instead would leave 2^-11 of both parts where they cancel. In fp32 with one rounding: 4096 rows of 8 experts,
         // K 2048, N 8192, w4sb32 178 -> 200 us, w6sb32 217 -> 260.
         constexpr float C = (float)(1 << (sb_bits(FMT) - 1));
+        bool over = false;
         const uint4 hd = lds4(cs);
         const float d = __half2float(__ushort_as_half((uint16_t)(hd.x & 0xffffu)));
         const float dm = __half2float(__ushort_as_half((uint16_t)(hd.x >> 16)));
@@ -412,6 +428,7 @@ __device__ __forceinline__ void unpack_atom(uint32_t cs, int at, int sw, const u
             // below fp16's normal range the middle goes by the rounded S, so that a code of 0 with M 0 stays 0
             const float mid = fmaf(C, fabsf(s) < 6.103515625e-5f ? __half2float(sh) : s, -dm * (float)sb_field(hd.y, hd.z, hd.w, 1, j));
             const uint32_t S = h2(__half_as_ushort(sh)), M = h2(__half_as_ushort(__float2half_rn(mid)));
+            over |= !(fmaf(C, fabsf(s), fabsf(mid)) <= 65504.0f);
             const uint4 cw = lds4(cs + 16 + 16 * j);
             const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
             uint32_t pl[2] = {0u, 0u};
@@ -445,7 +462,79 @@ __device__ __forceinline__ void unpack_atom(uint32_t cs, int at, int sw, const u
                 for (int q = 0; q < 4; ++q) o[16 * gl + 4 * i + q] = hfma2(u[q], S, M);
             }
         }
+        return over;
     }
+}
+
+// Eight weights of a plane's row from K 8 c on, in fp32.
+template <int FMT>
+__device__ __forceinline__ void weights8(const WideParams& p, unsigned long long row, int c, float (&w)[8]) {
+    const uint8_t* code = p.codes + row * p.crb;
+    uint32_t lo = 0u, hi = 0u;                           // nibbles (bytes for the 8-bit codes), and the bits above them
+    int bits = 0, off = 0;
+    float s = 0.0f, m = 0.0f;
+    if constexpr (is_sb(FMT)) {
+        const uint8_t* rec = code + (c >> 5) * sb_record(FMT);
+        const int i = c & 31, j = i >> 2;
+        const uint4 hd = __ldg(reinterpret_cast<const uint4*>(rec));
+        lo = __ldg(reinterpret_cast<const uint32_t*>(rec + 16) + i);
+        if (FMT == kFmtW5SB32) hi = __ldg(rec + 144 + i);
+        if (FMT == kFmtW6SB32) hi = __ldg(reinterpret_cast<const uint16_t*>(rec + 144) + i);
+        bits = sb_bits(FMT) - 4;
+        s = __half2float(__ushort_as_half((uint16_t)(hd.x & 0xffffu))) * (float)sb_field(hd.y, hd.z, hd.w, 0, j);
+        m = __half2float(__ushort_as_half((uint16_t)(hd.x >> 16))) * (float)sb_field(hd.y, hd.z, hd.w, 1, j);
+    } else {
+        s = __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(p.scales + row * p.srb) + 8 * c / sym_group(FMT))));
+        if (FMT == kFmtW4G64) {
+            lo = __ldg(reinterpret_cast<const uint32_t*>(code) + c);
+            off = 8;
+        } else if (FMT == kFmtW6G16) {
+            const uint8_t* b = code + (c >> 3) * 48;
+            lo = __ldg(reinterpret_cast<const uint32_t*>(b) + (c & 7));
+            hi = __ldg(reinterpret_cast<const uint16_t*>(b + 32) + (c & 7));
+            bits = 2;
+            off = 32;
+        } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(code) + c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = s * (float)((int)((k < 4 ? v.x : v.y) >> (8 * (k & 3)) & 255u) - 128);
+            return;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int u = (int)(lo >> (4 * k) & 15u) + (int)((hi >> (bits * k) & ((1u << bits) - 1u)) << 4);
+        w[k] = fmaf(s, (float)(u - off), -m);
+    }
+}
+
+// The sums of one weight row over K 8 c0 .. 8 c1 - 1 with the laid-out rows m0 .. m0 + 15 in fp32: for weights out of
+// fp16's range, which trained matrices do not have. Slow (512 rows, 2 experts, w4g64 2048 x 512: 1.8 ms), but a unit of
+// 128 rows and the longest K ends in 56 ms, far below the limit of the waits beside it. Looking for such scales costs
+// the other calls 1 % (4096 rows of 8 experts, w4g64 2048 x 8192: 171 -> 173 us).
+template <int FMT>
+__device__ __noinline__ void exact_sums(const WideParams& p, unsigned long long row, int c0, int c1, int m0, float* sums) {
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+    for (int c = c0; c < c1; ++c) {
+        float w[8];
+        weights8<FMT>(p, row, c, w);
+#pragma unroll 4
+        for (int j = 0; j < 16; ++j) {
+            const uint4 u = __ldg(p.xg + (size_t)min(m0 + j, p.pl.R - 1) * (p.pl.K / 8) + c);
+            const uint32_t h[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {                // the pairs that lay8 makes
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+                const int k = Wide<FMT>::ORDER == 1 ? i : (i & 1) + 4 * (i >> 1);
+                v[j] = fmaf(w[k], f.x, v[j]);
+                v[j] = fmaf(w[k + (Wide<FMT>::ORDER == 1 ? 4 : 2)], f.y, v[j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sums[j] = v[j];
 }
 
 // Scale words of the row's atom (64 weights from K 64 a on).
@@ -507,7 +596,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
     g.cost = reinterpret_cast<long long*>(at);
     g.row = reinterpret_cast<int*>(g.cost + p.pl.E + 1);
     g.ctas = g.row + p.pl.E + 1;
+    // Per weight row, for even and odd units (a row's two unpacking warps are less than two units apart): 1 + the last
+    // unit with weights past fp16.
+    volatile uint16_t* over = reinterpret_cast<uint16_t*>(smem + p.over_at);
 
+    for (int i = tid; i < 2 * kUnitRows; i += kWideThreads) over[i] = 0;
     if (tid == 0) {
         for (int s = 0; s < NC; ++s) {
             mbar_init(&cfull[s], 1);
@@ -664,7 +757,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                     sc[1] = nx[1];
                     if (a + 2 < a1) atom_scales<FMT>(srow, a + 2, p.pl.K, nx);
                     uint32_t o[32];
-                    unpack_atom<FMT>(cbase + cs * G::CB + rr * G::RB, 2 * i + h, G::RB == 128 ? r & 7 : 0, sc, o);
+                    if (unpack_atom<FMT>(cbase + cs * G::CB + rr * G::RB, 2 * i + h, G::RB == 128 ? r & 7 : 0, sc, o)) over[(u & 1) * kUnitRows + rr] = (uint16_t)(u + 1);
                     if (i == G::PAIRS - 1) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&cempty[cs]);
@@ -709,6 +802,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             tc_fence_after();
             // sums: this warp's 32 weight rows, 16 activation rows at a time
             const uint32_t dcol = tmem + tl + (db * kTiles + tile) * MC;
+            // made again where a weight passed fp16's range (a row past the expert's end is not stored)
+            const bool again = over[(u & 1) * kUnitRows + rr] == (uint16_t)(u + 1) && d.n0 + rr < p.pl.N, any_again = __any_sync(~0u, again);
+            auto load16 = [&](int b, float (&v)[16]) {
+                tmem_ld16(dcol + 16u * b, v);
+                if (any_again) {
+                    float t[16];
+                    if (again) exact_sums<FMT>(p, (unsigned long long)d.wrow + rr, d.k0 * (G::KS / 8), min(d.k1 * (G::KS / 8), p.pl.K / 8), d.row0 + 16 * b, t);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = again ? t[j] : v[j];
+                    __syncwarp();
+                }
+            };
             const bool cut = d.first != d.last || d.k0 > 0 || d.k1 < T;
             constexpr size_t kPart = (size_t)MC * kUnitRows;
             bool store = true;
@@ -724,7 +829,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
                 float* mine = p.part + (2 * (size_t)blockIdx.x + (d.k0 == 0)) * kPart + rr;
                 for (int b = h; b < blocks; b += 2) {
                     float v[16];
-                    tmem_ld16(dcol + 16u * b, v);
+                    load16(b, v);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) __stcg(mine + (size_t)(16 * b + j) * kUnitRows, v[j]);
                 }
@@ -742,7 +847,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_cons
             for (int b = h; store && b < blocks; b += 2) {
                 float v[16];
                 if (!cut) {
-                    tmem_ld16(dcol + 16u * b, v);
+                    load16(b, v);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] = 0.0f;
@@ -843,7 +948,7 @@ int wide_mc(int R, int E, int N) {
 template <int FMT, int MC>
 cudaError_t launch_wide_mc(const RowsArgs& a, WideParams& p, cudaStream_t st) {
     using G = Wide<FMT>;
-    const size_t fixed = kDescs * sizeof(WDesc) + kWorkers * (MC / 2) * sizeof(RowInfo) + kBarBytes + wgroups_bytes(a.E);
+    const size_t fixed = kDescs * sizeof(WDesc) + kWorkers * (MC / 2) * sizeof(RowInfo) + kBarBytes + wgroups_bytes(a.E) + kOverBytes;
     p.xslots = kMaxX;
     auto codes = [&]() { return (int)((kWideSmem - fixed - (size_t)p.xslots * MC * 256) / G::CB); };
     if (fixed + (size_t)p.xslots * MC * 256 + 2 * (size_t)G::CB > kWideSmem) p.xslots = 2;   // wide codes, many experts
@@ -866,6 +971,7 @@ cudaError_t launch_wide_mc(const RowsArgs& a, WideParams& p, cudaStream_t st) {
     cfg.gridDim = dim3((unsigned)(sms < kWideMaxCtas ? sms : kWideMaxCtas));
     cfg.blockDim = dim3(kWideThreads);
     cfg.dynamicSmemBytes = fixed + (size_t)p.xslots * MC * 256 + (size_t)p.cslots * G::CB;
+    p.over_at = (int)(cfg.dynamicSmemBytes - kOverBytes);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -926,9 +1032,12 @@ cudaError_t launch_wide_fmt(const RowsArgs& a, cudaStream_t st) {
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     p.pl = {a.offsets, a.E, a.R, a.N, a.K, (a.K + G::KS - 1) / G::KS, MC};
+    p.codes = static_cast<const uint8_t*>(a.codes);
     p.scales = static_cast<const uint8_t*>(a.scales);
     p.total_rows = rows;
+    p.crb = (uint32_t)crb;
     p.srb = (uint32_t)scale_row_bytes(FMT, a.K);
+    p.xg = reinterpret_cast<const uint4*>(ws + l.xg);
     p.rscale = rscale;
     p.part = reinterpret_cast<float*>(ws + l.part);
     p.count = count;
