@@ -233,3 +233,20 @@ def test_adapters_beside_weights_past_half_precision(fmt):
     y = rq.rq_wgemm_lora(x, w, A, B, torch.ones(3, device=DEV), a.to(torch.int32), out_dtype=torch.bfloat16)
     tol = K * 2.0 ** -23 * (xd.abs() @ size.t()) + 2.0 ** -11 * (xd.abs() @ What.abs().t()) + (K + r + 4) * 2.0 ** -23 * size_t
     within(y, xd @ What.t() + term, tol)
+
+
+@pytest.mark.parametrize("M", [1025, 1030, 1039, 2055])
+def test_equal_rows_of_an_adapter_call_are_equal(M):
+    """More rows than one round of launches takes, a few left for the last: the call's rows decide how all are multiplied.
+    One channel per row (no order of sums), weights of 18 bits, so that a rounding to fp16 in some rows only would show."""
+    K, N = 256, 2000
+    w, _, _ = few_codes("w8g16", N, K, 66, gone=slice(0, 0))
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    x[:, 77] = 1.0
+    g = torch.Generator().manual_seed(66)
+    A, B = (torch.randn(1, 8, K, generator=g) / 16).to(torch.bfloat16).to(DEV), torch.randn(1, N, 8, generator=g).to(torch.bfloat16).to(DEV)
+    for adapter in (-1, 0):
+        rows = torch.full((M,), adapter, dtype=torch.int32, device=DEV)
+        y = rq.rq_wgemm_lora(x, w, A, B, torch.ones(1, device=DEV), rows, out_dtype=torch.bfloat16)
+        assert (y == y[0]).all(), int((y != y[0]).any(1).sum())
+    assert rq.rq_device_status() == 0

@@ -106,6 +106,7 @@ size_t lora_workspace(int fmt, int R, int K, int N, int rank) { return lora_layo
 cudaError_t launch_lora(const RowsArgs& a0, cudaStream_t st) {
     const LoraLayout l = lora_layout(a0.fmt, a0.R, a0.K, a0.N, a0.ad.r);
     uint8_t* ws = static_cast<uint8_t*>(a0.ws);
+    const bool wide = a0.ybf16 && wide_rows(a0.R, 1);    // of the call, not of a round: a short last round is multiplied as the others
     for (int m0 = 0; m0 < a0.R; m0 += kBlockRows) {
         RowsArgs a = a0;
         a.R = a.T = a.Ty = a0.R - m0 < kBlockRows ? a0.R - m0 : kBlockRows;
@@ -114,7 +115,6 @@ cudaError_t launch_lora(const RowsArgs& a0, cudaStream_t st) {
         a.ws = ws + l.product;
         a.ad.row = a0.ad.row + m0;
         a.ad.t = reinterpret_cast<float*>(ws + l.t);
-        const bool wide = a.ybf16 && wide_rows(a.R, 1);
         if (a0.R > kFewRows) {
             a.order = reinterpret_cast<int*>(ws + l.order);
             if (!wide) {
