@@ -250,3 +250,15 @@ def test_equal_rows_of_an_adapter_call_are_equal(M):
         y = rq.rq_wgemm_lora(x, w, A, B, torch.ones(1, device=DEV), rows, out_dtype=torch.bfloat16)
         assert (y == y[0]).all(), int((y != y[0]).any(1).sum())
     assert rq.rq_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R", [3, 40])
+def test_no_rows_of_x(dtype, R):
+    """Indices into an x without rows name no row of it: such rows of the call are rows of zeros, as any other out of range."""
+    w, _, _ = few_codes("w4g64", 2 * 40, 256, 67)
+    y = torch.full((R + 1, 40), 7.5, dtype=dtype, device=DEV)
+    rows = torch.arange(R, dtype=torch.int32, device=DEV)
+    off = torch.tensor([0, 1, R - 1], dtype=torch.int32, device=DEV)
+    rq.rq_wgemm_grouped(torch.empty(0, 256, dtype=torch.bfloat16, device=DEV), w, off, in_rows=rows - 1, out_rows=rows, y=y[:R])
+    assert (y[:R - 1] == 0).all() and (y[R - 1:] == 7.5).all()

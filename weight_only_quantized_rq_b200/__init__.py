@@ -409,7 +409,10 @@ class GroupedExperts:
         Ty = _rows(y, "y")
         out = _out_type(y.dtype)
         py = _want(y, "y", y.dtype, (Ty, N), dev)
-        if T and R and Ty:
+        if R and Ty:
+            if not T:                                   # no row of x: every row of the call is a row of zeros
+                T, zeros = 1, torch.zeros(1, self.K, dtype=torch.bfloat16, device=dev)
+                px = zeros.data_ptr()
             # temporary memory from PyTorch's caching allocator on the call's stream: calls on other streams and
             # captured graphs get their own
             ws = torch.empty(self._bytes, dtype=torch.uint8, device=dev)
