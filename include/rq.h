@@ -278,7 +278,8 @@ size_t rq_grouped_workspace_size(int fmt, int R, int K, int N, int E);
  * A row whose in(i) is outside [0, T) is a row of zeros; one whose out(i) is
  * outside [0, Ty) is not stored. Two rows with the same out(i): one of the two
  * results is stored, element by element. A non-finite x value reaches the y
- * of its own rows only.
+ * of its own rows only: an infinity as the formula has it, but NaN in the
+ * superblocks' exact products (S u x and M x are both infinite).
  * fp32 results, and bf16 ones where R < 16 E, come from exact products (codes
  * and bf16 x) summed in fp32, the superblocks' sums of S u x and of M x apart
  * (their rounding follows sum |x| (S u + |M|)). bf16 results where R >= 16 E

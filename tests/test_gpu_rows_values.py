@@ -262,3 +262,29 @@ def test_no_rows_of_x(dtype, R):
     off = torch.tensor([0, 1, R - 1], dtype=torch.int32, device=DEV)
     rq.rq_wgemm_grouped(torch.empty(0, 256, dtype=torch.bfloat16, device=DEV), w, off, in_rows=rows - 1, out_rows=rows, y=y[:R])
     assert (y[:R - 1] == 0).all() and (y[R - 1:] == 7.5).all()
+
+
+def same_infinities(y, ref):
+    """Where the formula gives an infinity y has it, where it gives NaN y has NaN."""
+    y = y.double()
+    assert torch.equal(torch.isnan(y), torch.isnan(ref)), int((torch.isnan(y) != torch.isnan(ref)).sum())
+    assert torch.equal(y[torch.isinf(ref)], ref[torch.isinf(ref)])
+
+
+@pytest.mark.parametrize("fmt", SYM + SB)
+@pytest.mark.parametrize("M", [3, 40])
+def test_infinite_activations(fmt, M):
+    """An infinity beside values of every finite size: its sign with each weight's, NaN where the weight is zero (or, for the
+    superblocks' exact products, wherever S u and M are both not zero)."""
+    K, N = 256, 72
+    w, What, _ = few_codes(fmt, N, K, 68)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(68))
+    x[:, 1::3] *= 2.0 ** 100
+    x[:, 2::3] *= 2.0 ** -100
+    x[0, 9], x[1, 200], x[2, 5] = float("inf"), -float("inf"), float("inf")
+    x = x.to(torch.bfloat16).to(DEV)
+    ref = x.double() @ What.t()
+    for dtype in (torch.float32, torch.bfloat16):
+        if fmt in SB and (dtype == torch.float32 or M < 16):
+            continue
+        same_infinities(grouped(w, x, dtype)[:3], ref[:3])

@@ -162,9 +162,9 @@ __device__ __forceinline__ void lay_row(const LayParams& l, int row) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) top = max(top, tops[i]);
-    const int ex = (int)(top >> 7);                      // biased exponent of the largest value; 255: not finite
-    int sh = 0;
-    if (ex < 255 && top) sh = max(-126, min(126, 141 - ex));
+    // biased exponent of the largest value; 255 (not finite) as 254, so that no finite value beside it becomes infinite
+    const int ex = min(254, (int)(top >> 7));
+    const int sh = top ? max(-126, min(126, 141 - ex)) : 0;
     const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
     if (tid == 0) l.rscale[row] = __uint_as_float((uint32_t)(127 - sh) << 23);
     uint4* o = l.out + (size_t)row * (K / 8);
