@@ -288,3 +288,29 @@ def test_infinite_activations(fmt, M):
         if fmt in SB and (dtype == torch.float32 or M < 16):
             continue
         same_infinities(grouped(w, x, dtype)[:3], ref[:3])
+
+
+@pytest.mark.parametrize("M,dtype", [(4, torch.float32), (20, torch.float32), (40, torch.bfloat16)])
+def test_infinite_adapters(M, dtype):
+    """Infinities in A or B, and a term larger than bf16's largest: the formula's infinities, not NaN."""
+    K, N, r = 256, 72, 16
+    w, What, _ = few_codes("w8g16", N, K, 69)
+    g = torch.Generator().manual_seed(69)
+    A = (torch.randn(4, r, K, generator=g) / K ** 0.5).to(torch.bfloat16).to(DEV)
+    B = torch.randn(4, N, r, generator=g).to(torch.bfloat16).to(DEV)
+    A[0, 3, 17] = float("inf")
+    B[1, 40, 5], B[1, 41, 11] = -float("inf"), float("inf")
+    A[2] = 0.0
+    A[2, 0, 0] = 1.0
+    B[2] *= 2.0 ** -20
+    x = torch.randn(M, K, generator=g).to(torch.bfloat16).to(DEV)
+    x[2, 0] = 1.0
+    sc = torch.tensor([1.0, 1.0, 3.4e38, 1.0], device=DEV)          # t = 3.4e38 rounds to infinity in bf16, not in fp32
+    a = torch.arange(M, device=DEV) % 4
+    y = rq.rq_wgemm_lora(x, w, A, B, sc, a.to(torch.int32), out_dtype=dtype)
+    xd, Ad, Bd = x.double(), A[a].double(), B[a].double()
+    t = (Ad @ xd[..., None]) * sc[a].double()[:, None, None]
+    ref = xd @ What.t() + (Bd @ t)[..., 0]
+    same_infinities(y[:4], ref[:4])
+    assert torch.isfinite(y[[2, 3]]).all()
+    within(y[2:3], ref[2:3], 2.0 ** -16 * ref[2:3].abs() + K * 2.0 ** -23 * (xd.abs() @ What.abs().t())[2:3])

@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(THREADS) shrink_kernel(const __grid_constant__
     shrink_block<THREADS>(p, x, R, order, blockIdx.x);
 }
 
-__global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_constant__ Adapters p, const int* order, int R, float* z, int ldz) {
+__global__ void __launch_bounds__(kExpandThreads, 7) expand_kernel(const __grid_constant__ Adapters p, const int* order, int R, float* z, int ldz) {
     __shared__ float4 scratch[kExpandThreads / 32][64];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dep_wait();

@@ -27,6 +27,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return d;
 }
 
+// fp32 pair -> bf16x2, cut off towards zero.
+__device__ __forceinline__ uint32_t cut2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 // t[m][j .. j + 7] = alpha A . x[m] by a block of WARPS warps that share out K,
 // so that each lane has one load of x and eight of A in flight per round. Ranks
 // past the slot's are not read.
@@ -75,7 +82,10 @@ __device__ __forceinline__ void shrink8(const Adapters& p, const __nv_bfloat16* 
 // sums: for each adapter among the tile's rows D = B_a t^T with t zero for the
 // other rows, and D added to the adapter's own rows only (an infinite or NaN
 // B_a stays with them). t is split into three bf16 parts (24 bits), so that nothing
-// of it is lost to the tensor core's operand type. Lane 4 g + q holds ranks
+// of it is lost to the tensor core's operand type; the first is cut off, so that
+// a finite t keeps a finite one. The lower parts have sums of their own, which
+// count where the first part's is finite: where t or B is infinite, they, zero or
+// of the other sign, would make NaN of the formula's infinity. Lane 4 g + q holds ranks
 // 8 q .. 8 q + 7 of the chunk: of weight rows n + 8 i (i = 0..3) and of
 // activation row g, which is row m of the call (negative: none).
 __device__ __forceinline__ void add_adapters(const Adapters& p, int m, int c, int n, int lane, float (&acc0)[4], float (&acc1)[4]) {
@@ -94,7 +104,7 @@ __device__ __forceinline__ void add_adapters(const Adapters& p, int m, int c, in
             v = *reinterpret_cast<const float2*>(p.t + (size_t)m * p.r + j0 + 2 * q);
             if (j0 + 2 * q + 1 >= rank) v.y = 0.0f;
         }
-        t[0][q] = pack2(v.x, v.y);
+        t[0][q] = cut2(v.x, v.y);
         v.x -= bf16lo_f32(t[0][q]);
         v.y -= bf16hi_f32(t[0][q]);
         t[1][q] = pack2(v.x, v.y);
@@ -119,22 +129,29 @@ __device__ __forceinline__ void add_adapters(const Adapters& p, int m, int c, in
                 b[q] = make_uint4(cut(b[q].x, 0), cut(b[q].y, 2), cut(b[q].z, 4), cut(b[q].w, 6));
             }
         }
-        float d0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float d[2][2][4];                                // [first part, lower parts][weight rows n + 16 i]
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
             const uint32_t t0 = same ? t[s][0] : 0u, t1 = same ? t[s][1] : 0u, t2 = same ? t[s][2] : 0u, t3 = same ? t[s][3] : 0u;
             const uint32_t a0[4] = {b[0].x, b[1].x, b[0].y, b[1].y}, a1[4] = {b[2].x, b[3].x, b[2].y, b[3].y};
             const uint32_t a2[4] = {b[0].z, b[1].z, b[0].w, b[1].w}, a3[4] = {b[2].z, b[3].z, b[2].w, b[3].w};
-            mma16816(d0, a0, t0, t1, d0[0], d0[1], d0[2], d0[3]);
-            mma16816(d1, a1, t0, t1, d1[0], d1[1], d1[2], d1[3]);
-            mma16816(d0, a2, t2, t3, d0[0], d0[1], d0[2], d0[3]);
-            mma16816(d1, a3, t2, t3, d1[0], d1[1], d1[2], d1[3]);
+            auto& e = d[s > 0];
+            if (s < 2) {
+                mma16816(e[0], a0, t0, t1, 0.0f, 0.0f, 0.0f, 0.0f);
+                mma16816(e[1], a1, t0, t1, 0.0f, 0.0f, 0.0f, 0.0f);
+            } else {
+                mma16816(e[0], a0, t0, t1, e[0][0], e[0][1], e[0][2], e[0][3]);
+                mma16816(e[1], a1, t0, t1, e[1][0], e[1][1], e[1][2], e[1][3]);
+            }
+            mma16816(e[0], a2, t2, t3, e[0][0], e[0][1], e[0][2], e[0][3]);
+            mma16816(e[1], a3, t2, t3, e[1][0], e[1][1], e[1][2], e[1][3]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {                    // columns: activation rows 2 (lane & 3) + (i & 1)
             const bool own = with >> (4 * (2 * (lane & 3) + (i & 1))) & 1u;
-            acc0[i] += own ? d0[i] : 0.0f;
-            acc1[i] += own ? d1[i] : 0.0f;
+            const auto sum = [&](int h) { return d[0][h][i] + (fabsf(d[0][h][i]) < INFINITY ? d[1][h][i] : 0.0f); };
+            acc0[i] += own ? sum(0) : 0.0f;
+            acc1[i] += own ? sum(1) : 0.0f;
         }
     }
 }
