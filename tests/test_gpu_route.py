@@ -138,3 +138,28 @@ def test_combine(T, k, N, dtype, out):
         tol = tol + 2.0 ** -8 * (ref.abs() + tol)
     assert ((guard[:T].double() - ref).abs() <= tol).all()
     assert (guard[T] == 7.5).all()
+
+
+@pytest.mark.parametrize("N", [2056, 4096, 4104, 8200])
+@pytest.mark.parametrize("k", [1, 2, 3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_combine_wide_rows(N, k, dtype, out):
+    """Rows of several blocks, the last one partly filled; what a slot without an expert holds is not used."""
+    T = 5
+    g = torch.Generator().manual_seed(N + k)
+    y = torch.randn(T * k, N, generator=g).to(dtype).to(DEV)
+    ids = torch.randint(0, 9, (T, k), generator=g, dtype=torch.int32)
+    ids[1, 0] = -1
+    ids[3] = -1
+    y[ids.view(-1).to(DEV) < 0] = float("nan")
+    w = torch.randn(T, k, generator=g).to(DEV)
+    guard = torch.full((T + 1, N), 7.5, dtype=out, device=DEV)
+    rq.rq_route_combine(y, ids.to(DEV), w, out=guard[:T])
+    yd = torch.where((ids >= 0).to(DEV).view(-1, 1), y.double(), 0.0).view(T, k, N)
+    ref, S = (yd * w.double()[..., None]).sum(1), (yd.abs() * w.double().abs()[..., None]).sum(1)
+    tol = k * 2.0 ** -24 * S                             # k products, each added with one rounding
+    if out == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+    assert ((guard[:T].double() - ref).abs() <= tol).all()
+    assert (guard[T] == 7.5).all()
