@@ -314,3 +314,16 @@ def test_infinite_adapters(M, dtype):
     same_infinities(y[:4], ref[:4])
     assert torch.isfinite(y[[2, 3]]).all()
     within(y[2:3], ref[2:3], 2.0 ** -16 * ref[2:3].abs() + K * 2.0 ** -23 * (xd.abs() @ What.abs().t())[2:3])
+
+
+@pytest.mark.parametrize("fmt", SYM + SB)
+@pytest.mark.parametrize("exp", [-100, -112, -118, -124])
+def test_activations_near_the_smallest(fmt, exp):
+    """Exact products of values down to 2^-124 and below: codes carry 2^-14, so sums keep fp32's smallest step, 2^-149, times 2^14
+    per product of a group (its scale is below 2^-6 here)."""
+    K, N, M = 512, 72, 12
+    w, What, size = few_codes(fmt, N, K, 71)
+    x = (torch.randn(M, K, generator=torch.Generator().manual_seed(71)) * 2.0 ** exp).to(torch.bfloat16).to(DEV)
+    xd = x.double()
+    y = grouped(w, x, torch.float32)
+    within(y, xd @ What.t(), K * 2.0 ** -23 * (xd.abs() @ size.t()) + 2 * K * 2.0 ** -135)
