@@ -13,7 +13,7 @@
 // Shrink and layout in one launch instead of two: 128 rows 45.5 -> 44.1 us, 1024
 // rows of 8 adapters 72 -> 67, but 32 rows 26.0 -> 26.8.
 // Measured (the whole call): 32 rows of 16 adapters, r 32, w8g16 4096 x 4096,
-// 27 MB: 27 us; 128 rows of 24, r 64, w4sb32 2560 -> 10240, 40 MB: 44 us (33
+// 27 MB: 27 us; 128 rows of 24, r 64, w4sb32 2560 -> 10240, 40 MB: 45 us (33
 // without expand); 1024 rows of 64, r 64, w4g64 4096 x 4096: 104 us. What bounds
 // it is the chain of launches ahead of the product's sums, not the bytes.
 #include <cstdint>

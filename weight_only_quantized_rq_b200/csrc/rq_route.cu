@@ -10,10 +10,12 @@
 // tokens one block does both in one launch: a decode step pays for latency,
 // not for work. The combine reads k rows and writes one per token: bound by
 // memory, 16 bytes per load.
-// Measured: 8191 tokens, E 64, k 4, bf16: 11.0 us, the latency of two launches
-// (an expert's counts summed by several threads with shared atomics instead of
-// one warp: 16.4; 256 blocks instead of 128: 2 us more). 1 token: 3.4 us.
-// Combine of 8192 tokens, k 2, N 4096, bf16: 35 us, 5.7 TB/s (88 % of a copy).
+// Measured: 8191 tokens, E 64, k 4, bf16: 11.0 us: two launches, and in the
+// second one warp of a block places its pairs while the others wait (an expert's
+// counts summed by several threads with shared atomics instead of one warp:
+// 16.4; 256 blocks instead of 128: 2 us more). 1 token: 3.4 us.
+// Combine of 8192 tokens, k 2, N 4096, bf16: 35 us, 5.7 TB/s (87 % of a copy);
+// where N is no multiple of 8, one element per load: N 4095 240 us, 0.84 TB/s.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
